@@ -67,8 +67,13 @@ typedef enum {
     LSSAR_ERR_ALIGN = -6,   /* a pointer is not 16-byte aligned                       */
     LSSAR_ERR_CUDA = -7,    /* a CUDA call failed (launch, pool allocation, ...)      */
     LSSAR_ERR_ALIAS = -8,   /* an output overlaps an input (or another output)         */
-    LSSAR_ERR_SCRATCH = -9  /* lssar_attn_fwd_noalloc: problem needs more scratch than
+    LSSAR_ERR_SCRATCH = -9, /* lssar_attn_fwd_noalloc: problem needs more scratch than
                                LSSAR_NOALLOC_SCRATCH_BYTES                            */
+    LSSAR_ERR_PAGE = -10,   /* paged cache: page_size not a multiple of 8 in 8..256, no
+                               page, or a page_stride that does not fit               */
+    LSSAR_ERR_DTYPE = -11,  /* paged cache: dtype is not an lssar_dtype_t              */
+    LSSAR_ERR_KEEP = -12    /* lssar_paged_evict: keep < 1, recent < 0, sinks < 0 or
+                               recent + sinks > keep                                  */
 } lssar_status_t;
 
 /*
@@ -209,6 +214,111 @@ int lssar_attn_decode(const void *q, const void *k_cache, const void *v_cache, v
                       int B, int H, int L, int d, int p, int mode, cudaStream_t stream);
 
 /*
+ * Paged key-value cache: the decode step for sequences of different lengths
+ * whose keys and values lie in pages, with grouped heads (query head h reads
+ * key head h / (H / Hkv)).
+ *
+ *   k_pages, v_pages : 16-bit elements (dtype), device, 16-byte aligned.  Row r
+ *       of page g and key head h starts at element
+ *       g * page_stride + (h * page_size + r) * d: [n_pages, Hkv, page_size, d],
+ *       whose first stride may be larger than a page (both share it), so that K
+ *       and V can be slices of one buffer.
+ *   table : [B, max_pages] int32, device.  Slot s of sequence b lies in page
+ *       table[b][s / page_size], row s % page_size.  Entries past the last page
+ *       in use are not read.
+ *   lens  : [B] int32, device: the tokens cached for each sequence, 0 ..
+ *       max_pages * page_size (the capacity).
+ *
+ * The contents of table and lens are on the device, so that the kernels check
+ * them: a length outside 0..capacity records code 51 in the device error word,
+ * a page number outside 0..n_pages-1 code 52, and no access is made through
+ * either; what each call then does is said below.  Sequences may share pages
+ * that are only read.
+ */
+typedef enum { LSSAR_DTYPE_BF16 = 0, LSSAR_DTYPE_FP16 = 1 } lssar_dtype_t;
+
+typedef struct {
+    void *k_pages;
+    void *v_pages;
+    const int *table;
+    const int *lens;
+    long long page_stride;   /* elements from one page to the next, a multiple of 8 */
+    int n_pages;
+    int max_pages;           /* columns of table; max_pages * page_size <= 2^24 */
+    int page_size;           /* tokens per page: a multiple of 8 in 8..256 */
+    int B, Hkv, d;           /* d is 64 or 128 */
+    int dtype;               /* lssar_dtype_t */
+} lssar_paged_cache_t;
+
+/*
+ * Append: token t < counts[b] of sequence b goes to slot lens[b] + t.
+ *   k_new, v_new : [B, Hkv, n, d] of the cache's type, device; k_strides and
+ *       v_strides are HOST arrays of the element strides of (B, Hkv, n), each a
+ *       multiple of 8 where its dimension is above 1 (slices of a fused
+ *       projection need no copy).  Rows t >= counts[b] are not read.
+ *   n      : 0 .. 2^24 (0: k_new and v_new may be NULL).
+ *   counts : [B] int32, device, 0..n each; NULL: n for every sequence.
+ *   first_positions : [B] int32, device: position of token 0; NULL: lens[b].
+ *   scores : [B, Hkv, capacity] float32, or NULL: the new slots become 0.
+ *   positions : [B, Hkv, capacity] int32, or NULL: the new slots become
+ *       first_positions[b] + t.
+ *   lens_out : [B] int32, written: lens[b] + counts[b].  Not lens itself.
+ * Nothing else is written.  Two sequences must not append to one page.  A
+ * sequence with a bad length or count, or whose new length passes the
+ * capacity, is left alone (code 51, lens_out[b] = lens[b]); rows of a bad page
+ * number are dropped (code 52).
+ * Errors: LSSAR_ERR_NULL, SHAPE, HEADDIM, PAGE, DTYPE, ALIGN (a pointer or a
+ * stride), ALIAS (an output overlaps anything else; k_new, v_new, counts or
+ * first_positions overlap the pages, table or lens), CUDA.
+ */
+int lssar_paged_append(const lssar_paged_cache_t *cache, const void *k_new, const long long *k_strides,
+                       const void *v_new, const long long *v_strides, int n, const int *counts,
+                       const int *first_positions, float *scores, int *positions, int *lens_out, cudaStream_t stream);
+
+/*
+ * Decode: row i = lens[b] of the attention in every mode, for one new query
+ * per head against the sequence's cached tokens, the new one among them
+ * (append first).  i is the number of cached tokens, also after an eviction.
+ *   q   : [B, H, d] of the cache's type; q_strides is a HOST array of the
+ *         element strides of (B, H), multiples of 8 where the dimension is above 1.
+ *   out : [B, H, d] contiguous, of the cache's type, written.
+ *   H   : query heads, a multiple of Hkv.
+ *   scores, scores_out : [B, Hkv, capacity] float32, both or neither:
+ *         scores_out[b][h][s] = scores[b][h][s] + the normalised weights of slot
+ *         s of the query heads of h, for s < lens[b]; other slots are not
+ *         written.  scores_out may be scores itself.
+ * A sequence of length 0 gets out = 0.  One with a bad length gets NaN rows and
+ * no scores; with a bad page number, NaN rows and NaN scores in the heads.
+ * Results do not depend on the order of anything: the same call gives the same
+ * bits.  Scratch: about 4 B * H * (capacity + d) bytes from the library's pool.
+ * Errors as lssar_paged_append, and LSSAR_ERR_MODE, LSSAR_ERR_P.
+ */
+int lssar_paged_decode(const lssar_paged_cache_t *cache, const void *q, const long long *q_strides, void *out, int H,
+                       int p, int mode, const float *scores, float *scores_out, cudaStream_t stream);
+
+/*
+ * Evict: of each (sequence, key head) with n = lens[b] > keep, the `keep`
+ * tokens of the highest rank stay.  Rank: protected tokens first (position <
+ * sinks, or position > newest - recent, newest being the largest position of
+ * the row), then by score, equal scores (-0 = 0) by the lower slot, NaN last.
+ * Kept tokens in slots >= keep move into the slots < keep that were evicted,
+ * the j-th into the j-th in the order of the slots; the others stay where they
+ * are.  Keys, values, scores and positions move; a row of K and V at or behind
+ * slot `keep` is left as it was.
+ *   scores, positions : [B, Hkv, capacity], as the two calls above fill them.
+ *   scores_out, positions_out : the slots below the new length are written; both
+ *         may be the inputs themselves (then only the moved slots are written),
+ *         otherwise they must overlap nothing.
+ *   lens_out : [B] int32, written: min(lens[b], keep).  Not lens itself.
+ * Sequences must not share pages with one another here, except pages in which
+ * nothing moves.  A bad length: nothing moves, lens_out[b] = lens[b]; rows
+ * to or from a bad page number are not copied.
+ * Scratch: 8 B * Hkv * keep bytes.  Errors as above, and LSSAR_ERR_KEEP.
+ */
+int lssar_paged_evict(const lssar_paged_cache_t *cache, const float *scores, const int *positions, int keep, int recent,
+                      int sinks, float *scores_out, int *positions_out, int *lens_out, cudaStream_t stream);
+
+/*
  * Same operation and contract as lssar_attn_fwd, computed by a plain CUDA-core
  * kernel (one warp per query row, fp32 throughout, accurate libm softplus).
  * It is a second, independent GPU implementation kept for cross-checking the
@@ -312,8 +422,9 @@ const char *lssar_status_string(int status);
 
 /*
  * Reads and clears the device error word of the current device: 0 when no
- * kernel of this library has hit a bounded wait since the last call, else a
- * code (1-based pipeline stage) of the first wait that gave up.  Synchronises
+ * kernel of this library has hit a bounded wait or a bad length (51) or page
+ * number (52) of a paged cache since the last call, else the code (of a wait:
+ * its 1-based pipeline stage) of the first.  Synchronises
  * the current device.  Returns LSSAR_OK or LSSAR_ERR_CUDA.
  */
 int lssar_device_error_word(unsigned int *word);

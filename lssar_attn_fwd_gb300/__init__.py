@@ -8,8 +8,8 @@ from .inputs import MODE_LSSA, MODE_LSSAR, MODE_SIGMOID_RW, MODE_SOFTMAX, MODE_S
 
 
 def __getattr__(name):
-    if name in ("lssar_attn_fwd", "lssar_attn_fwd_simt", "load_library", "device_error_word",
-                "LssarError"):
+    if name in ("lssar_attn_fwd", "lssar_attn_fwd_simt", "lssar_paged_append", "lssar_paged_decode",
+                "lssar_paged_evict", "load_library", "device_error_word", "LssarError"):
         from . import api
         return getattr(api, name)
     raise AttributeError(name)

@@ -29,10 +29,26 @@ _EXPORTS = (
     "lssar_selftest_stall",
     "lssar_schedule_plan",
     "lssar_decode_plan",
+    "lssar_paged_append",
+    "lssar_paged_decode",
+    "lssar_paged_evict",
     "lssar_status_string",
     "lssar_device_error_word",
     "lssar_abi_version",
 )
+
+
+DTYPE_BF16 = 0
+DTYPE_FP16 = 1
+
+
+class PagedCacheDesc(ctypes.Structure):
+    """lssar_paged_cache_t of the C ABI."""
+
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("page_stride", ctypes.c_longlong), ("n_pages", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("B", ctypes.c_int), ("Hkv", ctypes.c_int),
+                ("d", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
 class LssarError(RuntimeError):
@@ -101,6 +117,13 @@ def _open(path):
     lib.lssar_schedule_plan.restype = ctypes.c_int
     lib.lssar_decode_plan.argtypes = [ctypes.c_int] * 4 + [ctypes.POINTER(ctypes.c_int)] * 4
     lib.lssar_decode_plan.restype = ctypes.c_int
+    cache, strides = ctypes.POINTER(PagedCacheDesc), ctypes.POINTER(ctypes.c_longlong)
+    ptr, num = ctypes.c_void_p, ctypes.c_int
+    lib.lssar_paged_append.argtypes = [cache, ptr, strides, ptr, strides, num] + [ptr] * 6
+    lib.lssar_paged_decode.argtypes = [cache, ptr, strides, ptr, num, num, num, ptr, ptr, ptr]
+    lib.lssar_paged_evict.argtypes = [cache, ptr, ptr, num, num, num, ptr, ptr, ptr, ptr]
+    for name in ("lssar_paged_append", "lssar_paged_decode", "lssar_paged_evict"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.lssar_selftest_stall.argtypes = [ctypes.c_void_p]
     lib.lssar_selftest_stall.restype = ctypes.c_int
     lib.lssar_status_string.argtypes = [ctypes.c_int]
@@ -349,6 +372,183 @@ def lssar_attn_decode(q, k_cache, v_cache, p=3, mode=MODE_LSSAR, out=None, strea
         _check(call_raw("lssar_attn_decode", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                         out.data_ptr(), B, H, L, d, p, mode, s.cuda_stream))
     return out
+
+
+def _longs(values):
+    return (ctypes.c_longlong * len(values))(*values)
+
+
+def _paged_cache(k_pages, v_pages, table, lens):
+    """Checks the tensors of a paged cache; returns its C description."""
+    import torch
+    for t in (k_pages, v_pages, table, lens):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("k_pages, v_pages, table and lens must be torch tensors")
+        if t.device.type != "cuda" or t.device != k_pages.device:
+            raise ValueError("k_pages, v_pages, table and lens must be CUDA tensors on one device")
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages and v_pages must share one [n_pages, Hkv, page_size, d] shape and type")
+    if k_pages.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("k_pages and v_pages must be bfloat16 or float16")
+    n_pages, Hkv, ps, d = k_pages.shape
+    if n_pages < 1 or Hkv < 1 or ps < 1:
+        raise ValueError("k_pages and v_pages must hold at least one page, head and token")
+    for t in (k_pages, v_pages):
+        if not t[0].is_contiguous() or (n_pages > 1 and t.stride(0) != k_pages.stride(0)):
+            raise ValueError("each page must be contiguous, and K and V must share the stride between pages")
+    if table.dim() != 2 or table.dtype != torch.int32 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous int32 [B, max_pages] tensor")
+    B, max_pages = table.shape
+    if tuple(lens.shape) != (B,) or lens.dtype != torch.int32 or not lens.is_contiguous():
+        raise ValueError("lens must be a contiguous int32 [B] tensor")
+    # the stride of a single page is never used
+    stride = k_pages.stride(0) if n_pages > 1 else Hkv * ps * d
+    return PagedCacheDesc(k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(), stride, n_pages,
+                          max_pages, ps, B, Hkv, d, DTYPE_BF16 if k_pages.dtype == torch.bfloat16 else DTYPE_FP16)
+
+
+def _slots(name, t, desc, dtype, device):
+    """The pointer of a [B, Hkv, capacity] tensor of per-slot values, or None."""
+    if t is None:
+        return None
+    if (t.dtype != dtype or tuple(t.shape) != (desc.B, desc.Hkv, desc.max_pages * desc.page_size)
+            or not t.is_contiguous() or t.device != device):
+        raise ValueError(f"{name} must be a contiguous {dtype} [B, Hkv, max_pages * page_size] tensor on the cache's device")
+    return t.data_ptr()
+
+
+def _per_sequence(name, t, desc, device):
+    """The pointer of a [B] int32 tensor, or None."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != (desc.B,) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 [B] tensor on the cache's device")
+    return t.data_ptr()
+
+
+def _stream_of(stream, device, *made):
+    """The stream's handle; tensors that this call made are kept from reuse
+    until the stream is done with them."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+    for t in made:
+        t.record_stream(s)
+    return s.cuda_stream
+
+
+def lssar_paged_append(k_new, v_new, k_pages, v_pages, table, lens, counts=None, first_positions=None, scores=None,
+                       positions=None, lens_out=None, stream=None):
+    """Puts new tokens' keys and values into the pages of their sequences.
+
+    k_new, v_new: [B, Hkv, n, d] (or [B, Hkv, d] for one token) of the cache's
+    type, any strides that are multiples of 8 elements with d contiguous.
+    k_pages, v_pages: [n_pages, Hkv, page_size, d] bf16 or fp16 (page_size a
+    multiple of 8 up to 256, d = 64 or 128); table: [B, max_pages] int32 page
+    numbers; lens: [B] int32 cached tokens.  counts: [B] int32, the first
+    counts[b] of the n tokens are appended (default: all).  first_positions:
+    [B] int32 position of the first of them (default: lens).  scores (float32)
+    and positions (int32), [B, Hkv, max_pages * page_size]: the new slots
+    become 0 and the tokens' positions.  Returns the new lengths (lens_out).
+    """
+    import torch
+    desc = _paged_cache(k_pages, v_pages, table, lens)
+    dev = k_pages.device
+    if k_new.dim() == 3 and v_new.dim() == 3:
+        k_new, v_new = k_new.unsqueeze(2), v_new.unsqueeze(2)
+    for t in (k_new, v_new):
+        if t.dim() != 4 or t.shape != k_new.shape or t.dtype != k_pages.dtype or t.device != dev:
+            raise ValueError("k_new and v_new must share one [B, Hkv, n, d] shape, with the cache's type and device")
+        if t.numel() and t.stride(3) != 1:
+            raise ValueError("the last dimension of k_new and v_new must be contiguous")
+    B, Hkv, n, d = k_new.shape
+    if (B, Hkv, d) != (desc.B, desc.Hkv, desc.d):
+        raise ValueError("k_new and v_new must be [B, Hkv, n, d] with the cache's B, Hkv and d")
+    made = []
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+        made.append(lens_out)
+    with torch.cuda.device(dev):
+        _check(load_library().lssar_paged_append(
+            ctypes.byref(desc), k_new.data_ptr(), _longs(k_new.stride()[:3]), v_new.data_ptr(),
+            _longs(v_new.stride()[:3]), n, _per_sequence("counts", counts, desc, dev),
+            _per_sequence("first_positions", first_positions, desc, dev), _slots("scores", scores, desc, torch.float32, dev),
+            _slots("positions", positions, desc, torch.int32, dev), _per_sequence("lens_out", lens_out, desc, dev),
+            _stream_of(stream, dev, *made)))
+    return lens_out
+
+
+def lssar_paged_decode(q, k_pages, v_pages, table, lens, p=3, mode=MODE_LSSAR, scores=None, scores_out=None, out=None,
+                       stream=None):
+    """One new query row per head against a paged cache, in every mode.
+
+    q: [B, H, d] of the cache's type (d contiguous, other strides multiples of
+    8), H a multiple of Hkv (query head h reads key head h // (H // Hkv)); the
+    cache as in :func:`lssar_paged_append`, the new token already appended.
+    Returns out [B, H, d], row lens[b] of the attention over each sequence's
+    cached tokens (zeros for an empty sequence).  scores: float32
+    [B, Hkv, max_pages * page_size]; each cached token's slot of scores_out
+    (default: scores itself) becomes scores plus the normalised weights that
+    the token gets from the query heads of its key head.
+    """
+    import torch
+    desc = _paged_cache(k_pages, v_pages, table, lens)
+    dev = k_pages.device
+    if q.dim() != 3 or q.shape[0] != desc.B or q.shape[2] != desc.d or q.dtype != k_pages.dtype or q.device != dev:
+        raise ValueError("q must be [B, H, d] with the cache's B, d, type and device")
+    if q.numel() and q.stride(2) != 1:
+        raise ValueError("the last dimension of q must be contiguous")
+    if scores is None and scores_out is not None:
+        raise ValueError("scores_out needs scores")
+    if scores is not None and scores_out is None:
+        scores_out = scores
+    made = []
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        made.append(out)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous [B, H, d] tensor of q's type on the cache's device")
+    with torch.cuda.device(dev):
+        _check(load_library().lssar_paged_decode(
+            ctypes.byref(desc), q.data_ptr(), _longs(q.stride()[:2]), out.data_ptr(), q.shape[1], int(p), int(mode),
+            _slots("scores", scores, desc, torch.float32, dev), _slots("scores_out", scores_out, desc, torch.float32, dev),
+            _stream_of(stream, dev, *made)))
+    return out
+
+
+def lssar_paged_evict(k_pages, v_pages, table, lens, scores, positions, keep, recent=0, sinks=0, scores_out=None,
+                      positions_out=None, lens_out=None, stream=None):
+    """Cuts every sequence with more than ``keep`` cached tokens to ``keep``.
+
+    Per key head the tokens of the highest scores stay (ties: the lower slot),
+    and before them the protected ones: position < sinks or position > newest
+    position - recent (recent + sinks <= keep).  Kept tokens behind slot
+    ``keep`` move into the evicted slots before it, in the pages as in scores
+    and positions ([B, Hkv, max_pages * page_size] float32 and int32); with
+    scores_out and positions_out (both or neither) these are read only.
+    Returns (new lengths, scores_out, positions_out).
+    """
+    import torch
+    desc = _paged_cache(k_pages, v_pages, table, lens)
+    dev = k_pages.device
+    if (scores_out is None) != (positions_out is None):
+        raise ValueError("scores_out and positions_out go together")
+    if scores_out is None:
+        scores_out, positions_out = scores, positions
+    made = []
+    if lens_out is None:
+        lens_out = torch.empty_like(lens)
+        made.append(lens_out)
+    with torch.cuda.device(dev):
+        _check(load_library().lssar_paged_evict(
+            ctypes.byref(desc), _slots("scores", scores, desc, torch.float32, dev),
+            _slots("positions", positions, desc, torch.int32, dev), int(keep), int(recent), int(sinks),
+            _slots("scores_out", scores_out, desc, torch.float32, dev),
+            _slots("positions_out", positions_out, desc, torch.int32, dev),
+            _per_sequence("lens_out", lens_out, desc, dev), _stream_of(stream, dev, *made)))
+    return lens_out, scores_out, positions_out
 
 
 def lssar_attn_fwd_profiled(q, k, v, p, mode, out, stream, ev_start, ev_main, ev_end):

@@ -135,6 +135,12 @@ int lssar::validate_args(const void *q, const void *k, const void *v, void *out,
     return validate(q, k, v, out, B, H, L, d, p, mode, pr);
 }
 
+cudaError_t lssar::scratch_alloc(void **ws, size_t bytes, cudaStream_t stream) {
+    cudaMemPool_t pool;
+    const cudaError_t e = device_pool(&pool);
+    return e != cudaSuccess ? e : cudaMallocFromPoolAsync(ws, bytes, pool, stream);
+}
+
 extern "C" {
 
 int lssar_attn_fwd(const void *q, const void *k, const void *v, void *out, int B, int H, int L,
@@ -351,6 +357,9 @@ const char *lssar_status_string(int status) {
         case LSSAR_ERR_CUDA: return "CUDA error";
         case LSSAR_ERR_ALIAS: return "an output overlaps an input or another output";
         case LSSAR_ERR_SCRATCH: return "problem needs more scratch than the fixed no-alloc array";
+        case LSSAR_ERR_PAGE: return "invalid pages (page_size a multiple of 8 in 8..256, n_pages >= 1, page_stride a multiple of 8 and at least one page)";
+        case LSSAR_ERR_DTYPE: return "unknown cache type (bfloat16 or float16)";
+        case LSSAR_ERR_KEEP: return "keep must be at least 1 and hold recent + sinks (each >= 0)";
         default: return "unknown status";
     }
 }
@@ -360,6 +369,6 @@ int lssar_device_error_word(unsigned int *word) {
     return lssar::read_and_clear_error_word(word) == cudaSuccess ? LSSAR_OK : LSSAR_ERR_CUDA;
 }
 
-int lssar_abi_version(void) { return 10000; }
+int lssar_abi_version(void) { return 10100; }
 
 }  // extern "C"

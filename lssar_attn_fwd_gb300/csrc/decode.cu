@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 
 #include "lssar_internal.cuh"
+#include "row_weights.cuh"
 #include "tc_host.cuh"
 #include "tc_ptx.cuh"
 
@@ -85,33 +86,6 @@ __device__ __forceinline__ float block_reduce(float x, bool is_max, float *red) 
     __syncthreads();
     float r = is_max ? -INFINITY : 0.f;
     for (int w = 0; w < kDecWarps + 1; ++w) r = is_max ? fmaxf(r, red[w]) : r + red[w];
-    return r;
-}
-
-// log2(1 + 2^z) without overflow for any z (MUFU ex2 / lg2, as in the
-// prefill kernel)
-__device__ __forceinline__ float sp2_any(float z) {
-    return fmaxf(z, 0.f) + ptx::lg2(1.f + ptx::ex2(-fabsf(z)));
-}
-
-__device__ __forceinline__ float sigmoid2(float z) {   // 1 / (1 + 2^-z)
-    return ptx::rcp(1.f + ptx::ex2(-z));
-}
-
-// The normaliser value of a score (softmax modes: relative to the max m).
-__device__ __forceinline__ float phi(int mode, float z, float m) {
-    if (mode == kSoftmax || mode == kSoftmaxRw) return ptx::ex2(z - m);
-    if (mode == kSigmoidRw) return sigmoid2(z);
-    return sp2_any(z);
-}
-
-__device__ __forceinline__ float powi(float x, int p) {
-    float r = 1.f;
-    while (p) {
-        if (p & 1) r *= x;
-        x *= x;
-        p >>= 1;
-    }
     return r;
 }
 

@@ -158,6 +158,9 @@ inline cudaError_t device_sms(int *sms) {
 // (-1: none), *tail_base = the first item handed out by the counter.
 int schedule_plan(int BH, int n_qtiles, int grid, int *first, int *tail_base);
 
+// Stream-ordered scratch from the library's memory pool on the current device.
+cudaError_t scratch_alloc(void **ws, size_t bytes, cudaStream_t stream);
+
 // Reads and clears the device error word of the current device.
 cudaError_t read_and_clear_error_word(unsigned int *word);
 
