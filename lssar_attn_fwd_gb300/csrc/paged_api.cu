@@ -136,7 +136,7 @@ int lssar_paged_decode(const lssar_paged_cache_t *cache, const void *q, const lo
     if (st != LSSAR_OK) return st;
     if (!q || !q_strides || !out || !scores != !scores_out) return LSSAR_ERR_NULL;
     if (mode < LSSAR_MODE_SOFTMAX || mode > LSSAR_MODE_SIGMOID_RW) return LSSAR_ERR_MODE;
-    if (H < 1 || H % a.c.Hkv || (unsigned long long)a.c.B * H > (1ULL << 24) ||
+    if (H < 1 || H % a.c.Hkv || H / a.c.Hkv > 128 || (unsigned long long)a.c.B * H > (1ULL << 24) ||
         (unsigned long long)a.c.B * H * a.c.capacity() > kMaxElems)
         return LSSAR_ERR_SHAPE;
     const bool reweight = lssar::is_reweight(mode);

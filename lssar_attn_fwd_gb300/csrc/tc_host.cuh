@@ -24,6 +24,11 @@ inline float score_qmul(int d) { return 1.4426950408889634f * logf((float)d); }
 // 128 rows, 128-byte swizzle, rows past L read as zero.
 bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, int BH, int L, int D);
 
+// TMA map of the pages of a paged cache, [n_pages][rows][d] with page_stride
+// elements between pages: boxes of 64 elements x box_rows, 128-byte swizzle.
+bool make_page_map(CUtensorMap *m, const void *base, bool half, int d, int rows, int n_pages, long long page_stride,
+                   int box_rows);
+
 // Device address of the library's error word on the current device.
 cudaError_t error_word_ptr(unsigned **out);
 
