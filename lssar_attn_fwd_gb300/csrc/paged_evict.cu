@@ -10,20 +10,35 @@
 // and a destination, so all moves are independent.
 //
 // Rank as a 32-bit key: a float's bits in the order of the values (-0 as +0),
-// NaN below every number, all ones for a protected token.  One CTA per row
-// finds the keep-th largest key by its four bytes from the highest down (a
-// 256-bin histogram each), then walks the slots once in order, numbers the
-// holes and the movers and lists them; a second kernel moves the rows.
+// NaN below every number, all ones for a protected token.
+//
+// One thread-block cluster per row, one launch.  Each CTA takes an equal run of
+// the row's slots and keeps their keys in shared memory, so that scores and
+// positions are read once.  The keep-th largest key is found by its four bytes
+// from the highest down: 256-bin histograms whose sums over the cluster meet
+// in distributed shared memory (lanes with equal bytes add once: the leading
+// bytes of accumulated weights are nearly all the same).  Then each thread
+// walks its own consecutive slots, prefix sums over the block and the cluster
+// number the holes and the movers, the lists go to a scratch array, and after a
+// last barrier the cluster's threads move the rows, 16 bytes a lane.
+//
+// Bound by HBM for long rows (8 bytes of each slot, 8d of each moved row), by
+// the eight barriers of the selection (a few us) for short ones.
 #include <climits>
+#include <cstdlib>
 
 #include "paged.cuh"
 #include "tc_host.cuh"
+#include "tc_ptx.cuh"
 
 namespace lssar {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kMoveThreads = 256;
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;            // portable cluster size
+constexpr int kCachedKeys = 16384;        // keys per CTA held in shared memory: two CTAs per SM
+constexpr int kChunk = 4096;              // slots per CTA that are worth another CTA
 
 // Key of one slot (see above).
 __device__ __forceinline__ unsigned rank_key(float s, int pos, int newest, int recent, int sinks) {
@@ -34,144 +49,235 @@ __device__ __forceinline__ unsigned rank_key(float s, int pos, int newest, int r
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix sum of x over the block; *total = the block's sum.
-__device__ int block_scan(int x, int *red, int *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
-    }
-    __syncthreads();
-    if (lane == 31) red[warp] = s;
-    __syncthreads();
-    int before = 0, sum = 0;
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-        if (w < warp) before += red[w];
-        sum += red[w];
-    }
-    *total = sum;
-    return before + s - x;
+// Shared memory that the cluster's other CTAs read.
+struct Shared {
+    int newest;
+    unsigned hist[4][256];
+    int holes, movers;
+};
+
+__device__ __forceinline__ int ld_cluster(const void *p, int rank) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ptx::cluster_map(ptx::smem_u32(p), (uint32_t)rank)) : "memory");
+    return v;
 }
 
-// src / dst: [B * Hkv][keep] lists, count: [B * Hkv].
-__global__ void __launch_bounds__(kSelThreads) paged_select(const PagedEvict a, int *__restrict__ src, int *__restrict__ dst, int *__restrict__ count) {
+// Exclusive prefix sums of x and y over the block, in thread order; *tx, *ty: the block's sums.
+__device__ void block_scan(int &x, int &y, int2 *red, int *tx, int *ty) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int a = x, b = y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, a, o), v = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) {
+            a += u;
+            b += v;
+        }
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = make_int2(a, b);
+    __syncthreads();
+    int2 w = red[lane];   // kWarps == 32
+    int2 s = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s.x, o), v = __shfl_up_sync(0xffffffffu, s.y, o);
+        if (lane >= o) {
+            s.x += u;
+            s.y += v;
+        }
+    }
+    *tx = __shfl_sync(0xffffffffu, s.x, 31);
+    *ty = __shfl_sync(0xffffffffu, s.y, 31);
+    x = a - x + __shfl_sync(0xffffffffu, s.x - w.x, warp);
+    y = b - y + __shfl_sync(0xffffffffu, s.y - w.y, warp);
+}
+
+// src / dst: [B * Hkv][keep] slots of the movers and the holes.  CACHED: the
+// run's keys are in shared memory; else each pass makes them again.
+template <bool CACHED>
+__global__ void __launch_bounds__(kThreads, CACHED ? 2 : 1)
+paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__restrict__ dst, int ctas) {
     const PagedCache &c = a.c;
-    __shared__ int red[kSelThreads / 32];
-    __shared__ unsigned hist[256];
-    __shared__ unsigned s_prefix, s_need;
-    const int bh = blockIdx.x, b = bh / c.Hkv;
+    extern __shared__ unsigned cached[];
+    __shared__ Shared sh;
+    __shared__ int2 red[kWarps];
+    __shared__ int s_newest;
+    __shared__ unsigned s_bin, s_left;
+    const int bh = blockIdx.x / ctas, rank = blockIdx.x % ctas, b = bh / c.Hkv, h = bh % c.Hkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = paged_len(c, b);
     const size_t base = (size_t)bh * c.capacity();
     const float *sc = a.scores + base;
     const int *pos = a.positions + base;
     float *sc_out = a.scores_out + base;
     int *pos_out = a.positions_out + base;
-    const bool in_place = a.scores == a.scores_out;
     // (a length outside the cache stays as it is, and nothing of its rows moves)
-    if (bh % c.Hkv == 0 && threadIdx.x == 0) a.lens_out[b] = c.lens[b] == n ? min(n, a.keep) : c.lens[b];
-    if (n <= a.keep) {
-        if (threadIdx.x == 0) count[bh] = 0;
-        for (int j = threadIdx.x; j < n; j += kSelThreads) {
+    if (h == 0 && rank == 0 && threadIdx.x == 0) a.lens_out[b] = c.lens[b] == n ? min(n, a.keep) : c.lens[b];
+    // slots [lo, hi) are this CTA's; a multiple of 4 per thread
+    const int run = ((n + ctas - 1) / ctas + 3) & ~3, lo = min(n, rank * run), hi = min(n, lo + run);
+    if (a.scores != a.scores_out)   // the holes' values follow below
+        for (int j = lo + threadIdx.x; j < min(hi, a.keep); j += kThreads) {
             sc_out[j] = sc[j];
             pos_out[j] = pos[j];
         }
-        return;
-    }
+    if (n <= a.keep) return;   // the whole cluster
+    // the newest position of the row
     int newest = INT_MIN;
-    for (int j = threadIdx.x; j < n; j += kSelThreads) newest = max(newest, pos[j]);
+    for (int j = lo + threadIdx.x; j < hi; j += kThreads) newest = max(newest, pos[j]);
     newest = __reduce_max_sync(0xffffffffu, newest);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = newest;
+    if (lane == 0) red[warp].x = newest;
+    reinterpret_cast<unsigned *>(sh.hist)[threadIdx.x] = 0;   // 4 * 256 == kThreads
     __syncthreads();
-    for (int w = 0; w < kSelThreads / 32; ++w) newest = max(newest, red[w]);
-    // the keep-th largest key, byte by byte; need: how many keys equal to it stay
-    unsigned prefix = 0, need = a.keep;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        __syncthreads();
-        if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-        __syncthreads();
-        for (int j = threadIdx.x; j < n; j += kSelThreads) {
-            const unsigned key = rank_key(sc[j], pos[j], newest, a.recent, a.sinks);
-            if (shift == 24 || (key >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1u);
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            int bin = 255;
-            unsigned left = need;
-            while (hist[bin] < left) left -= hist[bin--];
-            s_prefix = prefix | ((unsigned)bin << shift);
-            s_need = left;
-        }
-        __syncthreads();
-        prefix = s_prefix;
-        need = s_need;
+    if (warp == 0) {
+        newest = __reduce_max_sync(0xffffffffu, red[lane].x);
+        if (lane == 0) sh.newest = newest;
     }
-    // walk the slots in order
-    int eq_before = 0, holes = 0, movers = 0;
-    for (int j0 = 0; j0 < n; j0 += kSelThreads) {
-        const int j = j0 + threadIdx.x;
-        const float s = j < n ? sc[j] : 0.f;
-        const int ps = j < n ? pos[j] : 0;
-        const unsigned key = j < n ? rank_key(s, ps, newest, a.recent, a.sinks) : 0u;
-        int total;
-        const int eq = j < n && key == prefix;
-        const int rank = eq_before + block_scan(eq, red, &total);
-        eq_before += total;
-        const bool kept = j < n && (key > prefix || (eq && rank < (int)need));
-        const int hole = j < a.keep && !kept, mover = j >= a.keep && kept;
-        const int at = block_scan(hole, red, &total);
-        if (hole) dst[(size_t)bh * a.keep + holes + at] = j;
-        holes += total;
-        const int mat = block_scan(mover, red, &total);
-        if (mover) src[(size_t)bh * a.keep + movers + mat] = j;
-        movers += total;
-        if (!in_place && j < a.keep && kept) {
-            sc_out[j] = s;
-            pos_out[j] = ps;
-        }
+    ptx::cluster_sync();
+    if (warp == 0) {
+        newest = lane < ctas ? ld_cluster(&sh.newest, lane) : INT_MIN;
+        newest = __reduce_max_sync(0xffffffffu, newest);
+        if (lane == 0) s_newest = newest;
     }
-    if (threadIdx.x == 0) count[bh] = movers;
-}
-
-__global__ void __launch_bounds__(kMoveThreads) paged_move(const PagedEvict a, const int *__restrict__ src, const int *__restrict__ dst, const int *__restrict__ count) {
-    const PagedCache &c = a.c;
-    const int bh = blockIdx.x, b = bh / c.Hkv, h = bh % c.Hkv, parts = c.d / 8;
-    const int part = threadIdx.x % parts, per = kMoveThreads / parts, n = count[bh];
-    const size_t base = (size_t)bh * c.capacity();
-    for (int i = blockIdx.y * per + threadIdx.x / parts; i < n; i += gridDim.y * per) {
-        const int from = src[(size_t)bh * a.keep + i], to = dst[(size_t)bh * a.keep + i];
+    __syncthreads();
+    newest = s_newest;
+    auto make = [&](int j) { return rank_key(sc[j], pos[j], newest, a.recent, a.sinks); };
+    auto key_of = [&](int j) { return CACHED ? cached[j - lo] : make(j); };
+    // the keep-th largest key, byte by byte; left: how many of the keys with its
+    // leading bytes are among the highest `keep`
+    unsigned prefix = 0, left = a.keep;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        const int steps = (hi - lo + kThreads - 1) / kThreads;
+        for (int i = 0; i < steps; ++i) {
+            const int j = lo + i * kThreads + threadIdx.x;
+            unsigned key = 0;
+            bool in = j < hi;
+            if (in) {
+                if (pass == 0) {
+                    key = make(j);
+                    if (CACHED) cached[j - lo] = key;
+                } else {
+                    key = key_of(j);
+                    in = (key >> (shift + 8)) == (prefix >> (shift + 8));
+                }
+            }
+            // lanes out of the count share a bin number of their own
+            const unsigned bin = in ? (key >> shift) & 255u : 256u;
+            const unsigned peers = __match_any_sync(0xffffffffu, bin);
+            if (in && lane == __ffs(peers) - 1) atomicAdd(&sh.hist[pass][bin], (unsigned)__popc(peers));
+        }
+        ptx::cluster_sync();
+        // sums over the cluster, then from the highest bin down: thread t has bin 255 - t
+        int cnt = 0, zero = 0, t0, t1;
+        if (threadIdx.x < 256)
+            for (int r = 0; r < ctas; ++r) cnt += ld_cluster(&sh.hist[pass][255 - threadIdx.x], r);
+        int above = cnt;
+        block_scan(above, zero, red, &t0, &t1);
+        if (threadIdx.x < 256 && above < (int)left && above + cnt >= (int)left) {
+            s_bin = 255 - threadIdx.x;
+            s_left = left - above;
+        }
+        __syncthreads();
+        prefix |= s_bin << shift;
+        left = s_left;
+    }
+    // of the keys equal to `prefix` the first `left` stay: those of the CTAs
+    // before this one are in the last histogram
+    int eq_before = 0;
+    for (int r = 0; r < rank; ++r) eq_before += ld_cluster(&sh.hist[3][prefix & 255u], r);
+    // thread t owns consecutive slots
+    const int per = ((hi - lo + kThreads - 1) / kThreads + 3) & ~3;
+    const int j0 = min(hi, lo + (int)threadIdx.x * per), j1 = min(hi, j0 + per);
+    int eq = 0, zero = 0, t0, t1;
+    for (int j = j0; j < j1; ++j) eq += key_of(j) == prefix;
+    block_scan(eq, zero, red, &t0, &t1);
+    const int rank0 = eq_before + eq;
+    int holes = 0, movers = 0, seen = rank0;
+    auto stays = [&](unsigned key) { return key > prefix || (key == prefix && seen++ < (int)left); };
+    for (int j = j0; j < j1; ++j) {
+        const bool s = stays(key_of(j));
+        holes += j < a.keep && !s;
+        movers += j >= a.keep && s;
+    }
+    block_scan(holes, movers, red, &t0, &t1);
+    if (threadIdx.x == 0) {
+        sh.holes = t0;
+        sh.movers = t1;
+    }
+    ptx::cluster_sync();
+    int total = 0;
+    for (int r = 0; r < ctas; ++r) {
+        const int x = ld_cluster(&sh.holes, r), y = ld_cluster(&sh.movers, r);
+        if (r < rank) {
+            holes += x;
+            movers += y;
+        }
+        total += x;
+    }
+    int *to_list = dst + (size_t)bh * a.keep, *from_list = src + (size_t)bh * a.keep;
+    seen = rank0;
+    for (int j = j0; j < j1; ++j) {
+        const bool s = stays(key_of(j));
+        if (j < a.keep && !s) to_list[holes++] = j;
+        if (j >= a.keep && s) from_list[movers++] = j;
+    }
+    ptx::cluster_sync();   // the lists are complete; no CTA's shared memory is read after this
+    const int parts = c.d / 8, part = threadIdx.x % parts, per_cta = kThreads / parts;
+    auto *k = static_cast<uint16_t *>(c.k), *v = static_cast<uint16_t *>(c.v);
+    for (int i = rank * per_cta + threadIdx.x / parts; i < total; i += ctas * per_cta) {
+        const int from = __ldcg(from_list + i), to = __ldcg(to_list + i);
         if (part == 0) {
-            a.scores_out[base + to] = a.scores[base + from];
-            a.positions_out[base + to] = a.positions[base + from];
+            sc_out[to] = sc[from];
+            pos_out[to] = pos[from];
         }
         const int pf = paged_page(c, b, from / c.page_size), pt = paged_page(c, b, to / c.page_size);
         if (pf < 0 || pt < 0) continue;
         const size_t of = pf * c.page_stride + ((size_t)h * c.page_size + from % c.page_size) * c.d + part * 8;
         const size_t ot = pt * c.page_stride + ((size_t)h * c.page_size + to % c.page_size) * c.d + part * 8;
-        auto *k = static_cast<uint16_t *>(c.k), *v = static_cast<uint16_t *>(c.v);
         const uint4 kx = *reinterpret_cast<const uint4 *>(k + of), vx = *reinterpret_cast<const uint4 *>(v + of);
         *reinterpret_cast<uint4 *>(k + ot) = kx;
         *reinterpret_cast<uint4 *>(v + ot) = vx;
     }
 }
 
+template <bool CACHED>
+cudaError_t launch(const PagedEvict &a, int *src, int *dst, int ctas, int run, cudaStream_t stream) {
+    const int rows = a.c.B * a.c.Hkv, smem = CACHED ? run * 4 : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)rows * ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    static PerDeviceOnce once;
+    const cudaError_t e = per_device_once(once, nullptr, [](int &) {
+        return cudaFuncSetAttribute(paged_evict<CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCachedKeys * 4);
+    });
+    if (e != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&cfg, paged_evict<CACHED>, a, src, dst, ctas);
+}
+
 }  // namespace
 
-size_t paged_evict_workspace_bytes(const PagedEvict &pr) {
-    const size_t rows = (size_t)pr.c.B * pr.c.Hkv;
-    return rows * pr.keep * 8 + rows * 4;
-}
+size_t paged_evict_workspace_bytes(const PagedEvict &pr) { return (size_t)pr.c.B * pr.c.Hkv * pr.keep * 8; }
 
 cudaError_t launch_paged_evict(const PagedEvict &pr, void *ws, cudaStream_t stream) {
     PagedEvict a = pr;
     cudaError_t e = error_word_ptr(&a.c.err);
     if (e != cudaSuccess) return e;
-    const int rows = a.c.B * a.c.Hkv;
-    int *src = static_cast<int *>(ws), *dst = src + (size_t)rows * a.keep, *count = dst + (size_t)rows * a.keep;
-    paged_select<<<rows, kSelThreads, 0, stream>>>(a, src, dst, count);
-    paged_move<<<dim3(rows, 16), kMoveThreads, 0, stream>>>(a, src, dst, count);
-    return cudaGetLastError();
+    int *src = static_cast<int *>(ws), *dst = src + (size_t)a.c.B * a.c.Hkv * a.keep;
+    // CTAs per row by the longest row that the table has room for
+    const int cap = a.c.capacity();
+    int ctas = 1;
+    while (ctas < kMaxCluster && cap > ctas * kChunk) ctas *= 2;
+    const int run = ((cap + ctas - 1) / ctas + 3) & ~3;
+    return run <= kCachedKeys ? launch<true>(a, src, dst, ctas, run, stream) : launch<false>(a, src, dst, ctas, run, stream);
 }
 
 }  // namespace lssar
