@@ -38,6 +38,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "paged.cuh"
 #include "row_weights.cuh"
 #include "tc_host.cuh"
@@ -628,64 +630,98 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 
-// Blocks [0, join_blocks): the output rows, `warps_per` warps for each;
-// the others: the scores, by equal runs of tiles of the key heads.
+__device__ __forceinline__ float2 shuffle_xor(float2 x, int o) {
+    return make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o));
+}
+
+// (reference, sum of w) over the row's segments i = first, first + step, ...
+// of the head whose entries start at `at` (the whole warp calls it).
+__device__ float2 join_sums(const float2 *at, int zg, long long first, long long count, long long step) {
+    float2 x = make_float2(kLowest, 0.f);
+    for (long long i = first; i < count; i += step) x = join_pair(x, __ldcg(at + i * zg));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = join_pair(x, shuffle_xor(x, o));
+    return x;
+}
+
+// Blocks [0, join_blocks): the output rows, `warps_per` warps for each; the
+// others: the scores, by equal runs of tiles of the key heads.  Everything
+// that the lengths alone decide is done before the wait for the kernel that
+// this one depends on; after it come two rounds of loads for an output row (the
+// segments' sums, then their value sums) and two for the scores (the row
+// constants, then z and the scores, 16 bytes a thread).
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_join(const __grid_constant__ Args g, int join_blocks, int warps_per) {
     const PagedCache &c = g.a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = g.a.H / c.Hkv, mode = g.a.mode;
-    __shared__ float4 part[kJoinWarps][32];
-    __shared__ float2 ms[kJoinWarps];
     const long long per_row = tiles_before(c, c.B), total = per_row * g.sp.heads_rows;
     const int run = run_length(g.sp, total);
-    ptx::grid_dependency_wait();
     if ((int)blockIdx.x < join_blocks) {
         constexpr int kPerLane = D / 32;
-        const int per_block = kJoinWarps / warps_per;
+        using Vec = typename std::conditional<kPerLane == 4, float4, float2>::type;
+        __shared__ Vec part[kJoinWarps][32];
+        __shared__ float2 ms[kJoinWarps];
+        const int per_block = kJoinWarps / warps_per, sub = warp % warps_per;
         const long long r = (long long)blockIdx.x * per_block + warp / warps_per;
         const bool live = r < (long long)c.B * g.a.H;
         const int b = live ? (int)(r / g.a.H) : 0, hq = (int)(r % g.a.H), h = hq / G, gq = hq % G;
         const int n = live ? paged_len(c, b) : 0, nt = (n + kTile - 1) / kTile;
+        const bool usable = live && c.lens[b] == n;
+        const long long before = tiles_before(c, b);
+        const int hr = h * g.sp.blocks + gq / kHeads;
+        Segments sg = {0, 0};
+        if (n > 0) sg = segments_of((long long)b * g.sp.heads_rows + hr, before * g.sp.heads_rows + (long long)hr * nt, nt, run);
+        const float2 *sums = g.s.sums + sg.first * g.sp.zg + gq % kHeads;
+        const float *o = g.s.o + (sg.first * g.sp.zg + gq % kHeads) * D + lane * kPerLane;
+        ptx::grid_dependency_wait();
         float acc[kPerLane];
 #pragma unroll
         for (int e = 0; e < kPerLane; ++e) acc[e] = 0.f;
-        float m = kLowest, sum = 0.f;
-        const long long before = tiles_before(c, b);
-        if (n > 0) {
-            const int hr = h * g.sp.blocks + gq / kHeads, hh = gq % kHeads;
-            const long long row = (long long)b * g.sp.heads_rows + hr, start = before * g.sp.heads_rows + (long long)hr * nt;
-            const Segments sg = segments_of(row, start, nt, run);
-            for (long long i = warp % warps_per; i < sg.count; i += warps_per) {
-                const long long at = (sg.first + i) * g.sp.zg + hh;
-                const float2 y = __ldcg(&g.s.sums[at]);
-                const float mn = isnan(m) || isnan(y.x) ? NAN : fmaxf(m, y.x), fa = ptx::ex2(m - mn), fb = ptx::ex2(y.x - mn);
-                m = mn;
-                sum = sum * fa + y.y * fb;
-                const float *o = g.s.o + at * D + lane * kPerLane;
-#pragma unroll
-                for (int e = 0; e < kPerLane; ++e) acc[e] = acc[e] * fa + __ldcg(o + e) * fb;
+        // this warp's segments sub, sub + warps_per, ...
+        const float2 x = join_sums(sums, g.sp.zg, sub + (long long)lane * warps_per, sg.count, 32LL * warps_per);
+        float m = x.x, sum = x.y;
+        for (long long i0 = sub; i0 < sg.count; i0 += 32LL * warps_per) {
+            const long long mine = i0 + (long long)lane * warps_per;
+            const float f = mine < sg.count ? ptx::ex2(__ldcg(sums + mine * g.sp.zg).x - m) : 0.f;
+            const int cnt = (int)min(32LL, (sg.count - i0 + warps_per - 1) / warps_per);
+#pragma unroll 8
+            for (int i = 0; i < cnt; ++i) {
+                const Vec v = __ldcg(reinterpret_cast<const Vec *>(o + (i0 + (long long)i * warps_per) * g.sp.zg * D));
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                acc[0] = fmaf(v.x, fi, acc[0]);
+                acc[1] = fmaf(v.y, fi, acc[1]);
+                if constexpr (kPerLane == 4) {
+                    acc[2] = fmaf(v.z, fi, acc[2]);
+                    acc[3] = fmaf(v.w, fi, acc[3]);
+                }
             }
         }
         if (warps_per > 1) {
-            float4 x = make_float4(acc[0], acc[1], kPerLane > 2 ? acc[kPerLane - 2] : 0.f, kPerLane > 2 ? acc[kPerLane - 1] : 0.f);
-            part[warp][lane] = x;
+            if constexpr (kPerLane == 4) part[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            else part[warp][lane] = make_float2(acc[0], acc[1]);
             if (lane == 0) ms[warp] = make_float2(m, sum);
             __syncthreads();
-            if (warp % warps_per) return;
-            for (int w = warp + 1; w < warp + warps_per; ++w) {
-                const float2 y = ms[w];
-                const float mn = isnan(m) || isnan(y.x) ? NAN : fmaxf(m, y.x), fa = ptx::ex2(m - mn), fb = ptx::ex2(y.x - mn);
-                m = mn;
-                sum = sum * fa + y.y * fb;
-                const float4 v = part[w][lane];
-                const float vv[4] = {v.x, v.y, v.z, v.w};
+            if (sub) return;
+            float2 all = ms[warp];
+            for (int w = 1; w < warps_per; ++w) all = join_pair(all, ms[warp + w]);
 #pragma unroll
-                for (int e = 0; e < kPerLane; ++e) acc[e] = acc[e] * fa + vv[e] * fb;
+            for (int e = 0; e < kPerLane; ++e) acc[e] = 0.f;
+            for (int w = 0; w < warps_per; ++w) {
+                const float f = ptx::ex2(ms[warp + w].x - all.x);
+                const Vec v = part[warp + w][lane];
+                acc[0] = fmaf(v.x, f, acc[0]);
+                acc[1] = fmaf(v.y, f, acc[1]);
+                if constexpr (kPerLane == 4) {
+                    acc[2] = fmaf(v.z, f, acc[2]);
+                    acc[3] = fmaf(v.w, f, acc[3]);
+                }
             }
+            m = all.x;
+            sum = all.y;
         }
         if (!live) return;
         // a length outside the cache: NaN; an empty sequence: zeros
-        const float inv = c.lens[b] != n || isnan(m) ? NAN : n == 0 ? 0.f : 1.f / sum;
+        const float inv = !usable || isnan(m) ? NAN : n == 0 ? 0.f : 1.f / sum;
         uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(g.a.out) + r * D + lane * kPerLane);
 #pragma unroll
         for (int e = 0; e < kPerLane; e += 2) out[e / 2] = Elem<T>::pack(acc[e] * inv, acc[e + 1] * inv);
@@ -696,8 +732,11 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join(const __grid_constant
     const long long keys_total = per_row * c.Hkv, cta = (long long)blockIdx.x - join_blocks, ctas = (long long)gridDim.x - join_blocks;
     const long long srun = (keys_total + ctas - 1) / ctas;
     const long long t0 = cta * srun, t1 = t0 + srun < keys_total ? t0 + srun : keys_total;
-    if (t0 >= t1) return;
-    Place p = locate(c, c.Hkv, t0);
+    Place p = {};
+    if (t0 < t1) p = locate(c, c.Hkv, t0);
+    p.t = t0;
+    const bool vec = ((reinterpret_cast<uintptr_t>(g.a.scores) | reinterpret_cast<uintptr_t>(g.a.scores_out)) & 15) == 0;
+    ptx::grid_dependency_wait();
     while (p.t < t1) {
         const int cnt = (int)(t1 - p.t < p.nt - p.tile ? t1 - p.t : p.nt - p.tile);
         // number of the row's first tile among the stream's: the rows before it, each `blocks` times
@@ -707,30 +746,55 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join(const __grid_constant
         for (int gq = warp; gq < G; gq += kJoinWarps) {
             const long long row = (long long)p.b * g.sp.heads_rows + p.hr * g.sp.blocks + gq / kHeads;
             const Segments sg = segments_of(row, start + (long long)(gq / kHeads) * p.nt, p.nt, run);
-            float2 x = make_float2(kLowest, 0.f);
-            for (long long i = lane; i < sg.count; i += 32) x = join_pair(x, __ldcg(&g.s.sums[(sg.first + i) * g.sp.zg + gq % kHeads]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                x = join_pair(x, make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o)));
-            if (lane == 0) {
-                float4 r = is_reweight(mode) ? __ldcg(&g.s.rowc[row * g.sp.zg + gq % kHeads]) : make_float4(x.x, 1.f, 0.f, 0.f);
-                r.w = isnan(x.x) ? NAN : 1.f / x.y;
-                rowc[gq] = r;
-            }
+            float4 r = make_float4(0.f, 1.f, 0.f, 0.f);
+            if (is_reweight(mode)) r = __ldcg(&g.s.rowc[row * g.sp.zg + gq % kHeads]);
+            const float2 x = join_sums(g.s.sums + sg.first * g.sp.zg + gq % kHeads, g.sp.zg, lane, sg.count, 32);
+            if (!is_reweight(mode)) r.x = x.x;
+            r.w = isnan(x.x) ? NAN : 1.f / x.y;
+            if (lane == 0) rowc[gq] = r;
         }
         __syncthreads();
-        const int slot0 = threadIdx.x % kTile;
-        for (int i = threadIdx.x / kTile; i < cnt; i += kJoinThreads / kTile) {
-            const int slot = (p.tile + i) * kTile + slot0;
-            if (slot >= p.n) continue;
-            float s = 0.f;
+        // 16 threads per tile, four slots each
+        constexpr int kGroups = kJoinThreads / 16;
+        const int slot0 = (threadIdx.x % 16) * 4;
+        const size_t base = ((size_t)p.b * c.Hkv + p.hr) * c.capacity();
+        for (int i = threadIdx.x / 16; i < cnt; i += kGroups) {
+            const int slot = (p.tile + i) * kTile + slot0, have = p.n - slot;
+            if (have <= 0) continue;
+            const float *from = g.a.scores + base + slot;
+            float *to = g.a.scores_out + base + slot;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (vec && have >= 4) {
+                s = __ldcg(reinterpret_cast<const float4 *>(from));
+            } else {
+                s.x = from[0];
+                if (have > 1) s.y = from[1];
+                if (have > 2) s.z = from[2];
+                if (have > 3) s.w = from[3];
+            }
+            float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
             for (int gq = 0; gq < G; ++gq) {
                 const long long tile = start + (long long)(gq / kHeads) * p.nt + p.tile + i;
-                const float z = __ldcg(&g.s.z[(tile * g.sp.zg + gq % kHeads) * kTile + slot0]);
-                s += weight(mode, g.a.p, z, rowc[gq]) * rowc[gq].w;
+                const float4 z = __ldcg(reinterpret_cast<const float4 *>(&g.s.z[(tile * g.sp.zg + gq % kHeads) * kTile + slot0]));
+                const float4 rc = rowc[gq];
+                add.x = fmaf(weight(mode, g.a.p, z.x, rc), rc.w, add.x);
+                add.y = fmaf(weight(mode, g.a.p, z.y, rc), rc.w, add.y);
+                add.z = fmaf(weight(mode, g.a.p, z.z, rc), rc.w, add.z);
+                add.w = fmaf(weight(mode, g.a.p, z.w, rc), rc.w, add.w);
             }
-            const size_t at = ((size_t)p.b * c.Hkv + p.hr) * c.capacity() + slot;
-            g.a.scores_out[at] = g.a.scores[at] + s;
+            s.x += add.x;
+            s.y += add.y;
+            s.z += add.z;
+            s.w += add.w;
+            if (vec && have >= 4) {
+                *reinterpret_cast<float4 *>(to) = s;
+            } else {
+                to[0] = s.x;
+                if (have > 1) to[1] = s.y;
+                if (have > 2) to[2] = s.z;
+                if (have > 3) to[3] = s.w;
+            }
         }
         p.t += cnt;
         if (p.t < t1) next_row(c, c.Hkv, p);
