@@ -1,0 +1,10 @@
+// Instances of the paged decode kernel: bf16 cache, d = 128, every mode.
+#include "paged_decode.cuh"
+
+namespace lssar {
+namespace paged {
+
+LSSAR_PAGED_DECODE_INSTANCES(__nv_bfloat16, 128, bf16_d128)
+
+}  // namespace paged
+}  // namespace lssar
