@@ -47,8 +47,8 @@ struct PagedDecode {
     const float *scores;      // [B, Hkv, capacity] or null
     float *scores_out;
 };
-cudaError_t paged_decode_workspace_bytes(const PagedDecode &pr, size_t *bytes);
-cudaError_t launch_paged_decode(const PagedDecode &pr, void *ws, cudaStream_t stream);
+size_t paged_decode_workspace_bytes(const PagedDecode &pr, int sms);
+cudaError_t launch_paged_decode(const PagedDecode &pr, void *ws, int sms, cudaStream_t stream);
 
 struct PagedEvict {
     PagedCache c;

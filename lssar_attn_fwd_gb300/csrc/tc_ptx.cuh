@@ -380,6 +380,12 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
+__device__ __forceinline__ float rsqrt(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // a * b + c clamped to [0, 1] (one saturating FMA), two lanes.
 __device__ __forceinline__ float2 fma_sat2(float2 a, float2 b, float2 c) {
     float2 d;
