@@ -3,9 +3,10 @@
 // Token t of sequence b (t < counts[b]) has slot lens[b] + t; its rows of
 // every key head are copied to the slot's page, its added-up weight starts at
 // 0 and its position is first[b] + t.  A copy: 4d bytes of each (token, head)
-// are read and written once, so HBM bounds it.  Consecutive threads take
-// consecutive 16-byte vectors of consecutive tokens of one head, which fill a
-// page's rows of that head from front to back.
+// are read and written once, so HBM bounds it.  A block takes a stretch of
+// tokens of one (sequence, head), which fills the rows of that head in its pages
+// from front to back; d / 8 threads take a row, four rows of a group at once, so
+// that their loads are in flight together.
 #include "paged.cuh"
 #include "tc_host.cuh"
 
@@ -13,37 +14,52 @@ namespace lssar {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr int kRowsAtOnce = 4;
 
-__global__ void __launch_bounds__(kAppendThreads) paged_append(const PagedAppend a) {
+// `stretch`: tokens per block.
+__global__ void __launch_bounds__(kAppendThreads) paged_append(const __grid_constant__ PagedAppend a, int stretch, int stretches) {
     const PagedCache &c = a.c;
-    const long long idx = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
-    if (idx < c.B) {   // the new lengths, by the first B threads
-        const int b = (int)idx, cnt = a.counts ? a.counts[b] : a.n, len = c.lens[b];
-        const bool ok = len >= 0 && cnt >= 0 && cnt <= a.n && (long long)len + cnt <= c.capacity();
+    const int bh = blockIdx.x / stretches, b = bh / c.Hkv, h = bh - b * c.Hkv, t0 = (blockIdx.x - bh * stretches) * stretch;
+    const int cnt = a.counts ? a.counts[b] : a.n, len = c.lens[b];
+    const bool ok = len >= 0 && cnt >= 0 && cnt <= a.n && (long long)len + cnt <= c.capacity();
+    if (h == 0 && t0 == 0 && threadIdx.x == 0) {
         if (!ok) atomicCAS(c.err, 0u, (unsigned)kErrPagedLength);
         a.lens_out[b] = ok ? len + cnt : len;
     }
-    const int parts = c.d / 8;
-    const long long row = idx / parts;
-    if (row >= (long long)c.B * c.Hkv * a.n) return;
-    const int part = (int)(idx % parts);
-    const int t = (int)(row % a.n), bh = (int)(row / a.n), b = bh / c.Hkv, h = bh % c.Hkv;
-    const int cnt = a.counts ? a.counts[b] : a.n, len = c.lens[b];
-    if (len < 0 || cnt < 0 || cnt > a.n || (long long)len + cnt > c.capacity() || t >= cnt) return;
-    const int slot = len + t;
-    if (part == 0) {
-        const size_t at = (size_t)bh * c.capacity() + slot;
-        if (a.scores) a.scores[at] = 0.f;
-        if (a.positions) a.positions[at] = (a.first ? a.first[b] : len) + t;
+    const int t1 = ok ? min(cnt, t0 + stretch) : 0;
+    if (t0 >= t1) return;
+    const size_t at = (size_t)bh * c.capacity() + len;
+    if (a.scores)
+        for (int t = t0 + threadIdx.x; t < t1; t += kAppendThreads) a.scores[at + t] = 0.f;
+    if (a.positions) {
+        const int first = a.first ? a.first[b] : len;
+        for (int t = t0 + threadIdx.x; t < t1; t += kAppendThreads) a.positions[at + t] = first + t;
     }
-    const int pg = paged_page(c, b, slot / c.page_size);
-    if (pg < 0) return;
-    const auto *k = static_cast<const uint16_t *>(a.k_new) + b * a.ks[0] + h * a.ks[1] + t * a.ks[2] + part * 8;
-    const auto *v = static_cast<const uint16_t *>(a.v_new) + b * a.vs[0] + h * a.vs[1] + t * a.vs[2] + part * 8;
-    const uint4 kx = *reinterpret_cast<const uint4 *>(k), vx = *reinterpret_cast<const uint4 *>(v);
-    const size_t to = pg * c.page_stride + ((size_t)h * c.page_size + slot % c.page_size) * c.d + part * 8;
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(c.k) + to) = kx;
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(c.v) + to) = vx;
+    const int parts = c.d / 8, part = threadIdx.x % parts, groups = kAppendThreads / parts;
+    const uint16_t *k = static_cast<const uint16_t *>(a.k_new) + b * a.ks[0] + h * a.ks[1] + part * 8;
+    const uint16_t *v = static_cast<const uint16_t *>(a.v_new) + b * a.vs[0] + h * a.vs[1] + part * 8;
+#pragma unroll 1
+    for (int t = t0 + threadIdx.x / parts; t < t1; t += kRowsAtOnce * groups) {
+        uint4 kx[kRowsAtOnce], vx[kRowsAtOnce];
+        int pg[kRowsAtOnce];
+#pragma unroll
+        for (int e = 0; e < kRowsAtOnce; ++e) {
+            const int te = t + e * groups;
+            pg[e] = -1;
+            if (te >= t1) continue;
+            kx[e] = __ldcs(reinterpret_cast<const uint4 *>(k + te * a.ks[2]));
+            vx[e] = __ldcs(reinterpret_cast<const uint4 *>(v + te * a.vs[2]));
+            pg[e] = paged_page(c, b, (len + te) / c.page_size);
+        }
+#pragma unroll
+        for (int e = 0; e < kRowsAtOnce; ++e) {
+            if (pg[e] < 0) continue;
+            const int slot = len + t + e * groups;
+            const size_t to = pg[e] * c.page_stride + ((size_t)h * c.page_size + slot % c.page_size) * c.d + part * 8;
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(c.k) + to) = kx[e];
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(c.v) + to) = vx[e];
+        }
+    }
 }
 
 }  // namespace
@@ -52,11 +68,17 @@ cudaError_t launch_paged_append(const PagedAppend &pr, cudaStream_t stream) {
     PagedAppend a = pr;
     cudaError_t e = error_word_ptr(&a.c.err);
     if (e != cudaSuccess) return e;
-    long long threads = (long long)a.c.B * a.c.Hkv * a.n * (a.c.d / 8);
-    if (threads < a.c.B) threads = a.c.B;
-    const long long blocks = (threads + kAppendThreads - 1) / kAppendThreads;
+    // one round of a block's threads, or several while that leaves enough blocks to
+    // fill the GPU (blocks past a sequence's count end at once, but each costs a launch)
+    const int round = kRowsAtOnce * kAppendThreads / (a.c.d / 8);
+    const long long rows = (long long)a.c.B * a.c.Hkv;
+    int sms = 0, stretch = round;
+    if ((e = device_sms(&sms)) != cudaSuccess) return e;
+    while (stretch < 4 * round && rows * ((a.n + 2LL * stretch - 1) / (2 * stretch)) >= 16LL * sms) stretch *= 2;
+    const int stretches = a.n > stretch ? (a.n + stretch - 1) / stretch : 1;
+    const long long blocks = rows * stretches;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    paged_append<<<(unsigned)blocks, kAppendThreads, 0, stream>>>(a);
+    paged_append<<<(unsigned)blocks, kAppendThreads, 0, stream>>>(a, stretch, stretches);
     return cudaGetLastError();
 }
 

@@ -19,7 +19,7 @@ Layout layout(const PagedDecode &pr, int sms) {
     sp.zg = sp.G < paged::kHeads ? sp.G : paged::kHeads;
     const int keys = paged::tile_keys(c.d);
     const size_t rows = (size_t)c.B * sp.heads_rows, tiles = rows * ((c.capacity() + keys - 1) / keys);
-    const size_t wave = (size_t)sms * paged::Config<64, paged::kValues>::kPerSm;
+    const size_t wave = (size_t)sms * (c.d == 64 ? paged::Config<64, paged::kValues>::kPerSm : paged::Config<128, paged::kValues>::kPerSm);
     sp.ctas = (int)(tiles < wave ? tiles : wave);
     const size_t segments = (rows + sp.ctas) * sp.zg;
     const bool reweight = is_reweight(pr.mode);

@@ -72,8 +72,12 @@ struct Config {
     static constexpr int kPairs = kKeys / 2;           // pairs of keys per warp and tile
     static constexpr int kBatch = 32 / kPairs;         // tiles whose weights are formed together (32 pairs)
     static constexpr int kStageBytes = kTile * D * 2;
-    static constexpr int kStages = 3;
-    static constexpr int kPerSm = 3;
+    // CTAs per SM and stages of each.  d = 64: 3 x 3 (3 x 2 as fast, 2 x 5 4 % slower on
+    // 8 x 16K).  d = 128: 2 x 4; three CTAs leave 128 registers a thread, too few for the
+    // one-pass kernel: 104 against 91 us on a ragged batch of 480 MB, 43 against 39 us on
+    // 64 short sequences.
+    static constexpr int kStages = D == 64 ? 3 : 4;
+    static constexpr int kPerSm = D == 64 ? 3 : 2;
     static constexpr int kMerge = PHASE == kScores ? 0 : kWarps * kHeads * D * 4;   // the warps' sums of w v
     static constexpr int kSmem = 1024 + kStages * kStageBytes + kMerge;
 };
@@ -218,8 +222,8 @@ __device__ __forceinline__ uint32_t piece(uint32_t tile, int row, int chunk) {
 __device__ __forceinline__ void compute_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kCompute) : "memory"); }
 
 struct Shared {
-    uint64_t full[3], empty[3];
-    int bad[3];                     // the stage's tile names a page that is none
+    uint64_t full[4], empty[4];
+    int bad[4];                     // the stage's tile names a page that is none
     float2 red[kWarps][kHeads];
     float4 rowc[kHeads];
     int abort_flag;
@@ -545,20 +549,8 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
                         const float4 rc = sh.rowc[x0 + x];
                         y[2 * x] = have > 0 ? fmaxf(fmaf(phi(MODE, zn[x].x, rc.x), rc.y, rc.z), 0.f) : 0.f;
                         y[2 * x + 1] = have > 1 ? fmaxf(fmaf(phi(MODE, zn[x].y, rc.x), rc.y, rc.z), 0.f) : 0.f;
-                        if (x0 + x + 1 >= heads && x < 3) {   // one or two heads: no more than theirs
-#pragma unroll
-                            for (int e = 2 * x + 2; e < 8; ++e) y[e] = 0.f;
-                            break;
-                        }
                     }
-                    if (heads - x0 == 1) {
-                        float one[2] = {y[0], y[1]};
-                        powers(one, g.a.p);
-                        y[0] = one[0];
-                        y[1] = one[1];
-                    } else {
-                        powers(y, g.a.p);
-                    }
+                    powers(y, g.a.p);
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
                         if (x0 + x < heads) {
@@ -739,14 +731,14 @@ __device__ __forceinline__ float2 join_sums(const float2 *at, int zg, int count)
 // query head; the others: the scores, each block an equal run of the tiles
 // numbered through (sequence, key head, tile).  Everything that the lengths alone
 // decide is done before the wait for the kernel that this one depends on.
-template <typename T, int D, int MODE>
+template <typename T, int D, int MODE, bool SCORES>
 __global__ void __launch_bounds__(kJoinThreads, 4) paged_join(const __grid_constant__ Args g, int join_blocks, int warps_per) {
     constexpr int kPerLane = D / 32, kTile = tile_keys(D);
     constexpr bool kRelative = MODE == kSoftmax;
     const PagedCache &c = g.a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = g.sp.G;
     const int per_row = tiles_before<D>(c, c.B), total = per_row * g.sp.heads_rows, run = max(1, (total + g.sp.ctas - 1) / g.sp.ctas);
-    if ((int)blockIdx.x < join_blocks) {
+    if (!SCORES || (int)blockIdx.x < join_blocks) {
         __shared__ float part[kJoinWarps][D];
         const int sub = warp % warps_per, r = blockIdx.x * (kJoinWarps / warps_per) + warp / warps_per;
         const bool live = r < c.B * g.a.H;
@@ -800,6 +792,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join(const __grid_const
         for (int e = 0; e < kPerLane; e += 2) out[e / 2] = Elem<T>::pack(acc[e], acc[e + 1]);
         return;
     }
+    if constexpr (SCORES) {
     // four slots per thread
     __shared__ float2 rowf[kMaxGroup];   // the sums' joint reference, 1 / sum of w
     constexpr int kThreads = kTile / 4, kStep = kJoinThreads / kThreads;
@@ -825,7 +818,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join(const __grid_const
             if (lane == 0) rowf[x] = make_float2(all.x, ptx::rcp(all.y));
         }
         __syncthreads();
-#pragma unroll 2
+#pragma unroll 1
         for (int i = threadIdx.x / kThreads; i < cnt; i += kStep) {
             const int have = p.n - (p.tile + i) * kTile - in;
             if (have <= 0) continue;
@@ -850,6 +843,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join(const __grid_const
         }
         p.t += cnt;
         if (p.t < t1) next_row<D>(c, 1, p);
+    }
     }
 }
 
@@ -893,7 +887,8 @@ cudaError_t launch_mode(const CUtensorMap &km, const CUtensorMap &vm, const Args
     int warps_per = rows <= sms ? kJoinWarps : 1, join_blocks = (rows * warps_per + kJoinWarps - 1) / kJoinWarps;
     const int blocks = join_blocks + (g.a.scores ? (g.sp.ctas < 3 * sms ? g.sp.ctas : 3 * sms) : 0);
     void *args[] = {(void *)&g, (void *)&join_blocks, (void *)&warps_per};
-    return launch_kernel((const void *)paged_join<T, D, MODE>, blocks, kJoinThreads, 0, true, args, stream);
+    const void *fn = g.a.scores ? (const void *)paged_join<T, D, MODE, true> : (const void *)paged_join<T, D, MODE, false>;
+    return launch_kernel(fn, blocks, kJoinThreads, 0, true, args, stream);
 }
 
 // One call per (type, d) and file, so that the instances compile in parallel.

@@ -34,11 +34,12 @@
 namespace lssar {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;             // two CTAs per SM with 64 registers a thread, for the moves' loads in flight
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;            // portable cluster size
-constexpr int kCachedKeys = 16384;        // keys per CTA held in shared memory: two CTAs per SM
-constexpr int kChunk = 4096;              // slots per CTA that are worth another CTA
+constexpr int kCachedKeys = 24576;        // keys per CTA held in shared memory: two CTAs per SM
+constexpr int kChunk = 2048;              // slots per CTA that are worth another CTA
+constexpr int kMoves = 4;                 // rows that a group of threads moves at once
 
 // Key of one slot (see above).
 __device__ __forceinline__ unsigned rank_key(float s, int pos, int newest, int recent, int sinks) {
@@ -77,7 +78,7 @@ __device__ void block_scan(int &x, int &y, int2 *red, int *tx, int *ty) {
     __syncthreads();
     if (lane == 31) red[warp] = make_int2(a, b);
     __syncthreads();
-    int2 w = red[lane];   // kWarps == 32
+    int2 w = lane < kWarps ? red[lane] : make_int2(0, 0);
     int2 s = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -96,7 +97,7 @@ __device__ void block_scan(int &x, int &y, int2 *red, int *tx, int *ty) {
 // src / dst: [B * Hkv][keep] slots of the movers and the holes.  CACHED: the
 // run's keys are in shared memory; else each pass makes them again.
 template <bool CACHED>
-__global__ void __launch_bounds__(kThreads, CACHED ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 2)
 paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__restrict__ dst, int ctas) {
     const PagedCache &c = a.c;
     extern __shared__ unsigned cached[];
@@ -127,10 +128,10 @@ paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__
     for (int j = lo + threadIdx.x; j < hi; j += kThreads) newest = max(newest, pos[j]);
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) red[warp].x = newest;
-    reinterpret_cast<unsigned *>(sh.hist)[threadIdx.x] = 0;   // 4 * 256 == kThreads
+    for (int i = threadIdx.x; i < 4 * 256; i += kThreads) reinterpret_cast<unsigned *>(sh.hist)[i] = 0;
     __syncthreads();
     if (warp == 0) {
-        newest = __reduce_max_sync(0xffffffffu, red[lane].x);
+        newest = __reduce_max_sync(0xffffffffu, lane < kWarps ? red[lane].x : INT_MIN);
         if (lane == 0) sh.newest = newest;
     }
     ptx::cluster_sync();
@@ -223,21 +224,46 @@ paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__
         if (j >= a.keep && s) from_list[movers++] = j;
     }
     ptx::cluster_sync();   // the lists are complete; no CTA's shared memory is read after this
-    const int parts = c.d / 8, part = threadIdx.x % parts, per_cta = kThreads / parts;
+    // d / 8 threads per row, kMoves rows of a group at once: the places, the pages, then
+    // the rows' loads are in flight together
+    const int parts = c.d / 8, part = threadIdx.x % parts, groups = ctas * (kThreads / parts);
     auto *k = static_cast<uint16_t *>(c.k), *v = static_cast<uint16_t *>(c.v);
-    for (int i = rank * per_cta + threadIdx.x / parts; i < total; i += ctas * per_cta) {
-        const int from = __ldcg(from_list + i), to = __ldcg(to_list + i);
-        if (part == 0) {
-            sc_out[to] = sc[from];
-            pos_out[to] = pos[from];
+#pragma unroll 1
+    for (int i0 = rank * (kThreads / parts) + threadIdx.x / parts; i0 < total; i0 += kMoves * groups) {
+        int from[kMoves], to[kMoves];
+#pragma unroll
+        for (int e = 0; e < kMoves; ++e) {
+            const int i = i0 + e * groups;
+            from[e] = i < total ? __ldcg(from_list + i) : -1;
+            to[e] = i < total ? __ldcg(to_list + i) : 0;
         }
-        const int pf = paged_page(c, b, from / c.page_size), pt = paged_page(c, b, to / c.page_size);
-        if (pf < 0 || pt < 0) continue;
-        const size_t of = pf * c.page_stride + ((size_t)h * c.page_size + from % c.page_size) * c.d + part * 8;
-        const size_t ot = pt * c.page_stride + ((size_t)h * c.page_size + to % c.page_size) * c.d + part * 8;
-        const uint4 kx = *reinterpret_cast<const uint4 *>(k + of), vx = *reinterpret_cast<const uint4 *>(v + of);
-        *reinterpret_cast<uint4 *>(k + ot) = kx;
-        *reinterpret_cast<uint4 *>(v + ot) = vx;
+        long long of[kMoves], ot[kMoves];
+#pragma unroll
+        for (int e = 0; e < kMoves; ++e) {
+            of[e] = -1;
+            if (from[e] < 0) continue;
+            if (part == 0) {
+                sc_out[to[e]] = sc[from[e]];
+                pos_out[to[e]] = pos[from[e]];
+            }
+            const int fi = from[e] / c.page_size, ti = to[e] / c.page_size, pf = paged_page(c, b, fi), pt = paged_page(c, b, ti);
+            if (pf < 0 || pt < 0) continue;
+            of[e] = pf * c.page_stride + ((long long)h * c.page_size + from[e] - fi * c.page_size) * c.d + part * 8;
+            ot[e] = pt * c.page_stride + ((long long)h * c.page_size + to[e] - ti * c.page_size) * c.d + part * 8;
+        }
+        uint4 kx[kMoves], vx[kMoves];
+#pragma unroll
+        for (int e = 0; e < kMoves; ++e)
+            if (of[e] >= 0) {
+                kx[e] = __ldcs(reinterpret_cast<const uint4 *>(k + of[e]));
+                vx[e] = __ldcs(reinterpret_cast<const uint4 *>(v + of[e]));
+            }
+#pragma unroll
+        for (int e = 0; e < kMoves; ++e)
+            if (of[e] >= 0) {
+                *reinterpret_cast<uint4 *>(k + ot[e]) = kx[e];
+                *reinterpret_cast<uint4 *>(v + ot[e]) = vx[e];
+            }
     }
 }
 
@@ -272,10 +298,13 @@ cudaError_t launch_paged_evict(const PagedEvict &pr, void *ws, cudaStream_t stre
     cudaError_t e = error_word_ptr(&a.c.err);
     if (e != cudaSuccess) return e;
     int *src = static_cast<int *>(ws), *dst = src + (size_t)a.c.B * a.c.Hkv * a.keep;
-    // CTAs per row by the longest row that the table has room for
+    // CTAs per row by the longest row that the table has room for, in one wave of two per
+    // SM (96 rows of 16K tokens: 768 CTAs in 2.5 waves took 82 us)
     const int cap = a.c.capacity();
-    int ctas = 1;
-    while (ctas < kMaxCluster && cap > ctas * kChunk) ctas *= 2;
+    const long long rows = (long long)a.c.B * a.c.Hkv;
+    int sms = 0, ctas = 1;
+    if ((e = device_sms(&sms)) != cudaSuccess) return e;
+    while (ctas < kMaxCluster && cap > ctas * kChunk && 2 * ctas * rows <= 2 * sms) ctas *= 2;
     const int run = ((cap + ctas - 1) / ctas + 3) & ~3;
     return run <= kCachedKeys ? launch<true>(a, src, dst, ctas, run, stream) : launch<false>(a, src, dst, ctas, run, stream);
 }
