@@ -38,28 +38,35 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append(const __grid_cons
     const int parts = c.d / 8, part = threadIdx.x % parts, groups = kAppendThreads / parts;
     const uint16_t *k = static_cast<const uint16_t *>(a.k_new) + b * a.ks[0] + h * a.ks[1] + part * 8;
     const uint16_t *v = static_cast<const uint16_t *>(a.v_new) + b * a.vs[0] + h * a.vs[1] + part * 8;
+    const int *table = c.table + (size_t)b * c.max_pages;
+    bool bad = false;
 #pragma unroll 1
     for (int t = t0 + threadIdx.x / parts; t < t1; t += kRowsAtOnce * groups) {
         uint4 kx[kRowsAtOnce], vx[kRowsAtOnce];
-        int pg[kRowsAtOnce];
+        int pg[kRowsAtOnce], row[kRowsAtOnce];
 #pragma unroll
         for (int e = 0; e < kRowsAtOnce; ++e) {
-            const int te = t + e * groups;
-            pg[e] = -1;
+            const int te = t + e * groups, i = (len + te) / c.page_size;
+            pg[e] = 0;
+            row[e] = len + te - i * c.page_size;
             if (te >= t1) continue;
             kx[e] = __ldcs(reinterpret_cast<const uint4 *>(k + te * a.ks[2]));
             vx[e] = __ldcs(reinterpret_cast<const uint4 *>(v + te * a.vs[2]));
-            pg[e] = paged_page(c, b, (len + te) / c.page_size);
+            pg[e] = table[i];
         }
 #pragma unroll
         for (int e = 0; e < kRowsAtOnce; ++e) {
-            if (pg[e] < 0) continue;
-            const int slot = len + t + e * groups;
-            const size_t to = pg[e] * c.page_stride + ((size_t)h * c.page_size + slot % c.page_size) * c.d + part * 8;
+            if (t + e * groups >= t1) continue;
+            if ((unsigned)pg[e] >= (unsigned)c.n_pages) {
+                bad = true;
+                continue;
+            }
+            const size_t to = pg[e] * c.page_stride + ((size_t)h * c.page_size + row[e]) * c.d + part * 8;
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(c.k) + to) = kx[e];
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(c.v) + to) = vx[e];
         }
     }
+    if (bad) atomicCAS(c.err, 0u, (unsigned)kErrPagedPage);
 }
 
 }  // namespace

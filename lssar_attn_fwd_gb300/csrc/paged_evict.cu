@@ -12,18 +12,20 @@
 // Rank as a 32-bit key: a float's bits in the order of the values (-0 as +0),
 // NaN below every number, all ones for a protected token.
 //
-// One thread-block cluster per row, one launch.  Each CTA takes an equal run of
-// the row's slots and keeps their keys in shared memory, so that scores and
-// positions are read once.  The keep-th largest key is found by its four bytes
+// paged_select: one thread-block cluster per row.  Each CTA takes an equal run of
+// the row's slots and keeps their keys in shared memory, so that scores are read
+// once and positions twice.  The keep-th largest key is found by its four bytes
 // from the highest down: 256-bin histograms whose sums over the cluster meet
 // in distributed shared memory (lanes with equal bytes add once: the leading
 // bytes of accumulated weights are nearly all the same).  Then each thread
-// walks its own consecutive slots, prefix sums over the block and the cluster
-// number the holes and the movers, the lists go to a scratch array, and after a
-// last barrier the cluster's threads move the rows, 16 bytes a lane.
+// walks its own consecutive slots, and prefix sums over the block and the cluster
+// number the holes and the movers, whose lists go to scratch.
+// paged_move: all SMs move the rows, 16 bytes a lane, two rows of a group of
+// threads at once.  (Moved by the selecting clusters, which leave SMs idle and
+// have few loads in flight, 32 rows of 128K tokens took 226 us.)
 //
 // Bound by HBM for long rows (8 bytes of each slot, 8d of each moved row), by
-// the eight barriers of the selection (a few us) for short ones.
+// the eight barriers of the selection (a few us each with their code) for short ones.
 #include <climits>
 #include <cstdlib>
 
@@ -34,20 +36,23 @@
 namespace lssar {
 namespace {
 
-constexpr int kThreads = 512;             // two CTAs per SM with 64 registers a thread, for the moves' loads in flight
+constexpr int kThreads = 512;
+constexpr int kMoveThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;            // portable cluster size
-constexpr int kCachedKeys = 24576;        // keys per CTA held in shared memory: two CTAs per SM
+constexpr int kCachedKeys = 18432;        // keys per CTA held in shared memory: three CTAs per SM
 constexpr int kChunk = 2048;              // slots per CTA that are worth another CTA
-constexpr int kMoves = 4;                 // rows that a group of threads moves at once
+constexpr int kMoves = 2;                 // rows that a group of threads moves at once
 
-// Key of one slot (see above).
-__device__ __forceinline__ unsigned rank_key(float s, int pos, int newest, int recent, int sinks) {
-    // 64 bits: newest - recent may lie below the least int
-    if (pos < sinks || (long long)pos > (long long)newest - recent) return 0xffffffffu;
+// Key of a score (see above), and whether its token is protected.
+__device__ __forceinline__ unsigned score_key(float s) {
     if (isnan(s)) return 0u;
     const unsigned u = __float_as_uint(s == 0.f ? 0.f : s);
     return (u >> 31) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ bool is_protected(int pos, int newest, int recent, int sinks) {
+    // 64 bits: newest - recent may lie below the least int
+    return pos < sinks || (long long)pos > (long long)newest - recent;
 }
 
 // Shared memory that the cluster's other CTAs read.
@@ -97,13 +102,13 @@ __device__ void block_scan(int &x, int &y, int2 *red, int *tx, int *ty) {
 // src / dst: [B * Hkv][keep] slots of the movers and the holes.  CACHED: the
 // run's keys are in shared memory; else each pass makes them again.
 template <bool CACHED>
-__global__ void __launch_bounds__(kThreads, 2)
-paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__restrict__ dst, int ctas) {
+__global__ void __launch_bounds__(kThreads, 3)
+paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__restrict__ dst, int *__restrict__ count, int ctas) {
+    ptx::launch_dependents();
     const PagedCache &c = a.c;
     extern __shared__ unsigned cached[];
     __shared__ Shared sh;
     __shared__ int2 red[kWarps];
-    __shared__ int s_newest;
     __shared__ unsigned s_bin, s_left;
     const int bh = blockIdx.x / ctas, rank = blockIdx.x % ctas, b = bh / c.Hkv, h = bh % c.Hkv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -115,17 +120,24 @@ paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__
     int *pos_out = a.positions_out + base;
     // (a length outside the cache stays as it is, and nothing of its rows moves)
     if (h == 0 && rank == 0 && threadIdx.x == 0) a.lens_out[b] = c.lens[b] == n ? min(n, a.keep) : c.lens[b];
-    // slots [lo, hi) are this CTA's; a multiple of 4 per thread
+    // slots [lo, hi) are this CTA's
     const int run = ((n + ctas - 1) / ctas + 3) & ~3, lo = min(n, rank * run), hi = min(n, lo + run);
     if (a.scores != a.scores_out)   // the holes' values follow below
         for (int j = lo + threadIdx.x; j < min(hi, a.keep); j += kThreads) {
             sc_out[j] = sc[j];
             pos_out[j] = pos[j];
         }
-    if (n <= a.keep) return;   // the whole cluster
-    // the newest position of the row
+    if (n <= a.keep) {   // the whole cluster
+        if (rank == 0 && threadIdx.x == 0) count[bh] = 0;
+        return;
+    }
+    // the newest position of the row; the scores' keys
     int newest = INT_MIN;
-    for (int j = lo + threadIdx.x; j < hi; j += kThreads) newest = max(newest, pos[j]);
+#pragma unroll 8
+    for (int j = lo + threadIdx.x; j < hi; j += kThreads) {
+        newest = max(newest, pos[j]);
+        if (CACHED) cached[j - lo] = score_key(sc[j]);
+    }
     newest = __reduce_max_sync(0xffffffffu, newest);
     if (lane == 0) red[warp].x = newest;
     for (int i = threadIdx.x; i < 4 * 256; i += kThreads) reinterpret_cast<unsigned *>(sh.hist)[i] = 0;
@@ -135,44 +147,41 @@ paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__
         if (lane == 0) sh.newest = newest;
     }
     ptx::cluster_sync();
-    if (warp == 0) {
-        newest = lane < ctas ? ld_cluster(&sh.newest, lane) : INT_MIN;
-        newest = __reduce_max_sync(0xffffffffu, newest);
-        if (lane == 0) s_newest = newest;
+    newest = __reduce_max_sync(0xffffffffu, lane < ctas ? ld_cluster(&sh.newest, lane) : INT_MIN);
+    if (CACHED) {
+#pragma unroll 8
+        for (int j = lo + threadIdx.x; j < hi; j += kThreads)
+            if (is_protected(pos[j], newest, a.recent, a.sinks)) cached[j - lo] = 0xffffffffu;
     }
-    __syncthreads();
-    newest = s_newest;
-    auto make = [&](int j) { return rank_key(sc[j], pos[j], newest, a.recent, a.sinks); };
-    auto key_of = [&](int j) { return CACHED ? cached[j - lo] : make(j); };
+    auto key_of = [&](int j) {
+        if (CACHED) return cached[j - lo];
+        return is_protected(pos[j], newest, a.recent, a.sinks) ? 0xffffffffu : score_key(sc[j]);
+    };
     // the keep-th largest key, byte by byte; left: how many of the keys with its
     // leading bytes are among the highest `keep`
     unsigned prefix = 0, left = a.keep;
+    const int steps = (hi - lo + kThreads - 1) / kThreads;
+#pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
-        const int steps = (hi - lo + kThreads - 1) / kThreads;
-        for (int i = 0; i < steps; ++i) {
+#pragma unroll 2
+        for (int i = 0; i < steps; ++i) {   // (a thread meets the keys that it made)
             const int j = lo + i * kThreads + threadIdx.x;
-            unsigned key = 0;
-            bool in = j < hi;
-            if (in) {
-                if (pass == 0) {
-                    key = make(j);
-                    if (CACHED) cached[j - lo] = key;
-                } else {
-                    key = key_of(j);
-                    in = (key >> (shift + 8)) == (prefix >> (shift + 8));
-                }
-            }
+            const unsigned key = j < hi ? key_of(j) : 0u;
             // lanes out of the count share a bin number of their own
-            const unsigned bin = in ? (key >> shift) & 255u : 256u;
-            const unsigned peers = __match_any_sync(0xffffffffu, bin);
+            const bool in = j < hi && (pass == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)));
+            const unsigned bin = in ? (key >> shift) & 255u : 256u, peers = __match_any_sync(0xffffffffu, bin);
             if (in && lane == __ffs(peers) - 1) atomicAdd(&sh.hist[pass][bin], (unsigned)__popc(peers));
         }
         ptx::cluster_sync();
         // sums over the cluster, then from the highest bin down: thread t has bin 255 - t
         int cnt = 0, zero = 0, t0, t1;
         if (threadIdx.x < 256)
-            for (int r = 0; r < ctas; ++r) cnt += ld_cluster(&sh.hist[pass][255 - threadIdx.x], r);
+#pragma unroll 1
+            for (int r = 0; r < ctas; r += 2) {   // (a cluster of one reads itself)
+                const int x = ld_cluster(&sh.hist[pass][255 - threadIdx.x], r), y = r + 1 < ctas ? ld_cluster(&sh.hist[pass][255 - threadIdx.x], r + 1) : 0;
+                cnt += x + y;
+            }
         int above = cnt;
         block_scan(above, zero, red, &t0, &t1);
         if (threadIdx.x < 256 && above < (int)left && above + cnt >= (int)left) {
@@ -186,9 +195,11 @@ paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__
     // of the keys equal to `prefix` the first `left` stay: those of the CTAs
     // before this one are in the last histogram
     int eq_before = 0;
+#pragma unroll 1
     for (int r = 0; r < rank; ++r) eq_before += ld_cluster(&sh.hist[3][prefix & 255u], r);
-    // thread t owns consecutive slots
-    const int per = ((hi - lo + kThreads - 1) / kThreads + 3) & ~3;
+    // thread t owns consecutive slots, an odd number of them: no two lanes of a read meet
+    // in a bank of shared memory
+    const int per = ((hi - lo + kThreads - 1) / kThreads) | 1;
     const int j0 = min(hi, lo + (int)threadIdx.x * per), j1 = min(hi, j0 + per);
     int eq = 0, zero = 0, t0, t1;
     for (int j = j0; j < j1; ++j) eq += key_of(j) == prefix;
@@ -223,13 +234,36 @@ paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__
         if (j < a.keep && !s) to_list[holes++] = j;
         if (j >= a.keep && s) from_list[movers++] = j;
     }
-    ptx::cluster_sync();   // the lists are complete; no CTA's shared memory is read after this
+    if (rank == 0 && threadIdx.x == 0) count[bh] = total;
+    ptx::cluster_sync();   // no CTA's shared memory is read after this
+}
+
+// Moves the rows of the lists: `splits` blocks per (sequence, key head).
+__global__ void __launch_bounds__(kMoveThreads, 4) paged_move(const __grid_constant__ PagedEvict a, const int *__restrict__ src, const int *__restrict__ dst, const int *__restrict__ count, int splits) {
+    const PagedCache &c = a.c;
+    const int bh = blockIdx.x / splits, rank = blockIdx.x - bh * splits, b = bh / c.Hkv, h = bh - b * c.Hkv;
+    const int *from_list = src + (size_t)bh * a.keep, *to_list = dst + (size_t)bh * a.keep;
+    const size_t base = (size_t)bh * c.capacity();
+    const float *sc = a.scores + base;
+    const int *pos = a.positions + base;
+    float *sc_out = a.scores_out + base;
+    int *pos_out = a.positions_out + base;
+    ptx::grid_dependency_wait();
+    const int total = __ldcg(count + bh);
+    // scores and positions, a thread each
+    for (int i = rank * kMoveThreads + threadIdx.x; i < total; i += splits * kMoveThreads) {
+        const int from = __ldcg(from_list + i), to = __ldcg(to_list + i);
+        sc_out[to] = sc[from];
+        pos_out[to] = pos[from];
+    }
     // d / 8 threads per row, kMoves rows of a group at once: the places, the pages, then
     // the rows' loads are in flight together
-    const int parts = c.d / 8, part = threadIdx.x % parts, groups = ctas * (kThreads / parts);
+    const int parts = c.d / 8, part = threadIdx.x % parts, groups = splits * (kMoveThreads / parts);
     auto *k = static_cast<uint16_t *>(c.k), *v = static_cast<uint16_t *>(c.v);
+    const int *table = c.table + (size_t)b * c.max_pages;
+    bool bad = false;
 #pragma unroll 1
-    for (int i0 = rank * (kThreads / parts) + threadIdx.x / parts; i0 < total; i0 += kMoves * groups) {
+    for (int i0 = rank * (kMoveThreads / parts) + threadIdx.x / parts; i0 < total; i0 += kMoves * groups) {
         int from[kMoves], to[kMoves];
 #pragma unroll
         for (int e = 0; e < kMoves; ++e) {
@@ -237,26 +271,29 @@ paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__
             from[e] = i < total ? __ldcg(from_list + i) : -1;
             to[e] = i < total ? __ldcg(to_list + i) : 0;
         }
+        int pf[kMoves], pt[kMoves], fr[kMoves], tr[kMoves];
+#pragma unroll
+        for (int e = 0; e < kMoves; ++e) {
+            const int fi = max(from[e], 0) / c.page_size, ti = to[e] / c.page_size;
+            fr[e] = from[e] - fi * c.page_size;
+            tr[e] = to[e] - ti * c.page_size;
+            pf[e] = table[fi];
+            pt[e] = table[ti];
+        }
         long long of[kMoves], ot[kMoves];
 #pragma unroll
         for (int e = 0; e < kMoves; ++e) {
-            of[e] = -1;
-            if (from[e] < 0) continue;
-            if (part == 0) {
-                sc_out[to[e]] = sc[from[e]];
-                pos_out[to[e]] = pos[from[e]];
-            }
-            const int fi = from[e] / c.page_size, ti = to[e] / c.page_size, pf = paged_page(c, b, fi), pt = paged_page(c, b, ti);
-            if (pf < 0 || pt < 0) continue;
-            of[e] = pf * c.page_stride + ((long long)h * c.page_size + from[e] - fi * c.page_size) * c.d + part * 8;
-            ot[e] = pt * c.page_stride + ((long long)h * c.page_size + to[e] - ti * c.page_size) * c.d + part * 8;
+            const bool page = (unsigned)pf[e] < (unsigned)c.n_pages && (unsigned)pt[e] < (unsigned)c.n_pages;
+            of[e] = from[e] >= 0 && page ? pf[e] * c.page_stride + ((long long)h * c.page_size + fr[e]) * c.d + part * 8 : -1;
+            ot[e] = pt[e] * c.page_stride + ((long long)h * c.page_size + tr[e]) * c.d + part * 8;
+            bad |= from[e] >= 0 && !page;
         }
         uint4 kx[kMoves], vx[kMoves];
 #pragma unroll
         for (int e = 0; e < kMoves; ++e)
             if (of[e] >= 0) {
-                kx[e] = __ldcs(reinterpret_cast<const uint4 *>(k + of[e]));
-                vx[e] = __ldcs(reinterpret_cast<const uint4 *>(v + of[e]));
+                kx[e] = *reinterpret_cast<const uint4 *>(k + of[e]);
+                vx[e] = *reinterpret_cast<const uint4 *>(v + of[e]);
             }
 #pragma unroll
         for (int e = 0; e < kMoves; ++e)
@@ -265,10 +302,11 @@ paged_evict(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *__
                 *reinterpret_cast<uint4 *>(v + ot[e]) = vx[e];
             }
     }
+    if (bad) atomicCAS(c.err, 0u, (unsigned)kErrPagedPage);
 }
 
 template <bool CACHED>
-cudaError_t launch(const PagedEvict &a, int *src, int *dst, int ctas, int run, cudaStream_t stream) {
+cudaError_t launch_select(const PagedEvict &a, int *src, int *dst, int *count, int ctas, int run, cudaStream_t stream) {
     const int rows = a.c.B * a.c.Hkv, smem = CACHED ? run * 4 : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)rows * ctas);
@@ -283,30 +321,47 @@ cudaError_t launch(const PagedEvict &a, int *src, int *dst, int ctas, int run, c
     cfg.numAttrs = 1;
     static PerDeviceOnce once;
     const cudaError_t e = per_device_once(once, nullptr, [](int &) {
-        return cudaFuncSetAttribute(paged_evict<CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCachedKeys * 4);
+        return cudaFuncSetAttribute(paged_select<CACHED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCachedKeys * 4);
     });
     if (e != cudaSuccess) return e;
-    return cudaLaunchKernelEx(&cfg, paged_evict<CACHED>, a, src, dst, ctas);
+    return cudaLaunchKernelEx(&cfg, paged_select<CACHED>, a, src, dst, count, ctas);
 }
 
 }  // namespace
 
-size_t paged_evict_workspace_bytes(const PagedEvict &pr) { return (size_t)pr.c.B * pr.c.Hkv * pr.keep * 8; }
+size_t paged_evict_workspace_bytes(const PagedEvict &pr) { return (size_t)pr.c.B * pr.c.Hkv * (pr.keep * 8 + 4); }
 
 cudaError_t launch_paged_evict(const PagedEvict &pr, void *ws, cudaStream_t stream) {
     PagedEvict a = pr;
     cudaError_t e = error_word_ptr(&a.c.err);
     if (e != cudaSuccess) return e;
-    int *src = static_cast<int *>(ws), *dst = src + (size_t)a.c.B * a.c.Hkv * a.keep;
-    // CTAs per row by the longest row that the table has room for, in one wave of two per
-    // SM (96 rows of 16K tokens: 768 CTAs in 2.5 waves took 82 us)
+    int *src = static_cast<int *>(ws), *dst = src + (size_t)a.c.B * a.c.Hkv * a.keep, *count = dst + (size_t)a.c.B * a.c.Hkv * a.keep;
+    // CTAs per row by the longest row that the table has room for, in one wave of three
+    // per SM (96 rows of 16K tokens: 2, 4 and 8 CTAs each took 77, 68 and 82 us)
     const int cap = a.c.capacity();
     const long long rows = (long long)a.c.B * a.c.Hkv;
     int sms = 0, ctas = 1;
     if ((e = device_sms(&sms)) != cudaSuccess) return e;
-    while (ctas < kMaxCluster && cap > ctas * kChunk && 2 * ctas * rows <= 2 * sms) ctas *= 2;
+    while (ctas < kMaxCluster && cap > ctas * kChunk && 2 * ctas * rows <= 3 * sms) ctas *= 2;
     const int run = ((cap + ctas - 1) / ctas + 3) & ~3;
-    return run <= kCachedKeys ? launch<true>(a, src, dst, ctas, run, stream) : launch<false>(a, src, dst, ctas, run, stream);
+    e = run <= kCachedKeys ? launch_select<true>(a, src, dst, count, ctas, run, stream) : launch_select<false>(a, src, dst, count, ctas, run, stream);
+    if (e != cudaSuccess) return e;
+    // two waves of four blocks per SM, more where there are more rows, but not more
+    // than the moves of a full row give work to
+    const int at_once = kMoves * kMoveThreads / (a.c.d / 8), most = (a.keep + at_once - 1) / at_once;
+    long long splits = (8LL * sms + rows - 1) / rows;
+    if (splits > most) splits = most;
+    if (rows * splits > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * splits));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_move, a, (const int *)src, (const int *)dst, (const int *)count, (int)splits);
 }
 
 }  // namespace lssar
