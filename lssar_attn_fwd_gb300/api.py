@@ -9,6 +9,7 @@ built, or a call fails, an exception is raised.
 
 import ctypes
 import os
+import struct
 
 from .inputs import MODE_LSSA, MODE_LSSAR, MODE_SIGMOID_RW, MODE_SOFTMAX, MODE_SOFTMAX_RW  # noqa: F401
 
@@ -117,11 +118,12 @@ def _open(path):
     lib.lssar_schedule_plan.restype = ctypes.c_int
     lib.lssar_decode_plan.argtypes = [ctypes.c_int] * 4 + [ctypes.POINTER(ctypes.c_int)] * 4
     lib.lssar_decode_plan.restype = ctypes.c_int
-    cache, strides = ctypes.POINTER(PagedCacheDesc), ctypes.POINTER(ctypes.c_longlong)
+    # (the cache description and the stride arrays by address: a PagedCacheDesc by
+    # reference, or bytes)
     ptr, num = ctypes.c_void_p, ctypes.c_int
-    lib.lssar_paged_append.argtypes = [cache, ptr, strides, ptr, strides, num] + [ptr] * 6
-    lib.lssar_paged_decode.argtypes = [cache, ptr, strides, ptr, num, num, num, ptr, ptr, ptr]
-    lib.lssar_paged_evict.argtypes = [cache, ptr, ptr, num, num, num, ptr, ptr, ptr, ptr]
+    lib.lssar_paged_append.argtypes = [ptr] * 5 + [num] + [ptr] * 6
+    lib.lssar_paged_decode.argtypes = [ptr] * 4 + [num] * 3 + [ptr] * 3
+    lib.lssar_paged_evict.argtypes = [ptr] * 3 + [num] * 3 + [ptr] * 4
     for name in ("lssar_paged_append", "lssar_paged_decode", "lssar_paged_evict"):
         getattr(lib, name).restype = ctypes.c_int
     lib.lssar_selftest_stall.argtypes = [ctypes.c_void_p]
@@ -374,69 +376,95 @@ def lssar_attn_decode(q, k_cache, v_cache, p=3, mode=MODE_LSSAR, out=None, strea
     return out
 
 
-def _longs(values):
-    return (ctypes.c_longlong * len(values))(*values)
+# lssar_paged_cache_t and stride arrays as bytes: the paged calls are small
+# enough that marshalling is a good part of their time (a ctypes structure and
+# two arrays cost as much as a launch).
+_CACHE = struct.Struct("@PPPPqiiiiiii")
+_pack_2 = struct.Struct("@2q").pack
+_pack_3 = struct.Struct("@3q").pack
 
 
 def _paged_cache(k_pages, v_pages, table, lens):
-    """Checks the tensors of a paged cache; returns its C description."""
+    """Checks the tensors of a paged cache; returns (its C description, B, Hkv,
+    capacity, d, device index)."""
     import torch
     for t in (k_pages, v_pages, table, lens):
         if not isinstance(t, torch.Tensor):
             raise TypeError("k_pages, v_pages, table and lens must be torch tensors")
-        if t.device.type != "cuda" or t.device != k_pages.device:
-            raise ValueError("k_pages, v_pages, table and lens must be CUDA tensors on one device")
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+    dev = k_pages.get_device() if k_pages.is_cuda else -1
+    if dev < 0 or v_pages.get_device() != dev or table.get_device() != dev or lens.get_device() != dev:
+        raise ValueError("k_pages, v_pages, table and lens must be CUDA tensors on one device")
+    shape, dtype = k_pages.shape, k_pages.dtype
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not dtype:
         raise ValueError("k_pages and v_pages must share one [n_pages, Hkv, page_size, d] shape and type")
-    if k_pages.dtype not in (torch.bfloat16, torch.float16):
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError("k_pages and v_pages must be bfloat16 or float16")
-    n_pages, Hkv, ps, d = k_pages.shape
+    n_pages, Hkv, ps, d = shape
     if n_pages < 1 or Hkv < 1 or ps < 1:
         raise ValueError("k_pages and v_pages must hold at least one page, head and token")
-    for t in (k_pages, v_pages):
-        if not t[0].is_contiguous() or (n_pages > 1 and t.stride(0) != k_pages.stride(0)):
-            raise ValueError("each page must be contiguous, and K and V must share the stride between pages")
-    if table.dim() != 2 or table.dtype != torch.int32 or not table.is_contiguous():
+    kst, vst = k_pages.stride(), v_pages.stride()
+    inner = (ps * d, d, 1)
+    if (kst[1:] != inner or vst[1:] != inner or kst[0] != vst[0]) and (
+            not k_pages[0].is_contiguous() or not v_pages[0].is_contiguous() or (n_pages > 1 and kst[0] != vst[0])):
+        raise ValueError("each page must be contiguous, and K and V must share the stride between pages")
+    if table.dtype is not torch.int32 or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table must be a contiguous int32 [B, max_pages] tensor")
     B, max_pages = table.shape
-    if tuple(lens.shape) != (B,) or lens.dtype != torch.int32 or not lens.is_contiguous():
+    if lens.dtype is not torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
         raise ValueError("lens must be a contiguous int32 [B] tensor")
     # the stride of a single page is never used
-    stride = k_pages.stride(0) if n_pages > 1 else Hkv * ps * d
-    return PagedCacheDesc(k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(), stride, n_pages,
-                          max_pages, ps, B, Hkv, d, DTYPE_BF16 if k_pages.dtype == torch.bfloat16 else DTYPE_FP16)
+    desc = _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                       kst[0] if n_pages > 1 else Hkv * ps * d, n_pages, max_pages, ps, B, Hkv, d,
+                       DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP16)
+    return desc, B, Hkv, max_pages * ps, d, dev
 
 
-def _slots(name, t, desc, dtype, device):
+def _slots(name, t, shape, dtype, dev):
     """The pointer of a [B, Hkv, capacity] tensor of per-slot values, or None."""
     if t is None:
         return None
-    if (t.dtype != dtype or tuple(t.shape) != (desc.B, desc.Hkv, desc.max_pages * desc.page_size)
-            or not t.is_contiguous() or t.device != device):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous {dtype} [B, Hkv, max_pages * page_size] tensor on the cache's device")
     return t.data_ptr()
 
 
-def _per_sequence(name, t, desc, device):
+def _per_sequence(name, t, B, dev):
     """The pointer of a [B] int32 tensor, or None."""
     import torch
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != (desc.B,) or not t.is_contiguous() or t.device != device:
+    if t.dtype is not torch.int32 or t.shape != (B,) or not t.is_contiguous() or not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous int32 [B] tensor on the cache's device")
     return t.data_ptr()
 
 
-def _stream_of(stream, device, *made):
-    """The stream's handle; tensors that this call made are kept from reuse
-    until the stream is done with them."""
+def _int32(name, value):
+    value = int(value)
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} does not fit 32 bits")
+    return value
+
+
+def _paged_call(name, dev, stream, made, *args):
+    """Calls an entry point on the cache's device and the given (default: the
+    current) stream; tensors that this call made are kept from reuse until
+    another stream than the current one is done with them."""
     import torch
+    fn = getattr(_LIB or load_library(), name)
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
-    for t in made:
-        t.record_stream(s)
-    return s.cuda_stream
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev)
+        for t in made:
+            t.record_stream(s)
+        handle = s.cuda_stream
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != 0:
+        _check(status)
 
 
 def lssar_paged_append(k_new, v_new, k_pages, v_pages, table, lens, counts=None, first_positions=None, scores=None,
@@ -452,31 +480,32 @@ def lssar_paged_append(k_new, v_new, k_pages, v_pages, table, lens, counts=None,
     [B] int32 position of the first of them (default: lens).  scores (float32)
     and positions (int32), [B, Hkv, max_pages * page_size]: the new slots
     become 0 and the tokens' positions.  Returns the new lengths (lens_out).
+    Runs asynchronously on ``stream`` (default: the current stream).
     """
     import torch
-    desc = _paged_cache(k_pages, v_pages, table, lens)
-    dev = k_pages.device
+    desc, B, Hkv, cap, d, dev = _paged_cache(k_pages, v_pages, table, lens)
     if k_new.dim() == 3 and v_new.dim() == 3:
         k_new, v_new = k_new.unsqueeze(2), v_new.unsqueeze(2)
-    for t in (k_new, v_new):
-        if t.dim() != 4 or t.shape != k_new.shape or t.dtype != k_pages.dtype or t.device != dev:
-            raise ValueError("k_new and v_new must share one [B, Hkv, n, d] shape, with the cache's type and device")
-        if t.numel() and t.stride(3) != 1:
-            raise ValueError("the last dimension of k_new and v_new must be contiguous")
-    B, Hkv, n, d = k_new.shape
-    if (B, Hkv, d) != (desc.B, desc.Hkv, desc.d):
+    shape, dtype = k_new.shape, k_pages.dtype
+    if (len(shape) != 4 or v_new.shape != shape or k_new.dtype is not dtype or v_new.dtype is not dtype
+            or not k_new.is_cuda or not v_new.is_cuda or k_new.get_device() != dev or v_new.get_device() != dev):
+        raise ValueError("k_new and v_new must share one [B, Hkv, n, d] shape, with the cache's type and device")
+    n = shape[2]
+    if (shape[0], shape[1], shape[3]) != (B, Hkv, d):
         raise ValueError("k_new and v_new must be [B, Hkv, n, d] with the cache's B, Hkv and d")
-    made = []
+    kst, vst = k_new.stride(), v_new.stride()
+    if n and (kst[3] != 1 or vst[3] != 1):
+        raise ValueError("the last dimension of k_new and v_new must be contiguous")
+    made = ()
     if lens_out is None:
         lens_out = torch.empty_like(lens)
-        made.append(lens_out)
-    with torch.cuda.device(dev):
-        _check(load_library().lssar_paged_append(
-            ctypes.byref(desc), k_new.data_ptr(), _longs(k_new.stride()[:3]), v_new.data_ptr(),
-            _longs(v_new.stride()[:3]), n, _per_sequence("counts", counts, desc, dev),
-            _per_sequence("first_positions", first_positions, desc, dev), _slots("scores", scores, desc, torch.float32, dev),
-            _slots("positions", positions, desc, torch.int32, dev), _per_sequence("lens_out", lens_out, desc, dev),
-            _stream_of(stream, dev, *made)))
+        made = (lens_out,)
+    slots = (B, Hkv, cap)
+    _paged_call("lssar_paged_append", dev, stream, made, desc, k_new.data_ptr(), _pack_3(*kst[:3]), v_new.data_ptr(),
+                _pack_3(*vst[:3]), n, _per_sequence("counts", counts, B, dev),
+                _per_sequence("first_positions", first_positions, B, dev),
+                _slots("scores", scores, slots, torch.float32, dev), _slots("positions", positions, slots, torch.int32, dev),
+                _per_sequence("lens_out", lens_out, B, dev))
     return lens_out
 
 
@@ -485,36 +514,39 @@ def lssar_paged_decode(q, k_pages, v_pages, table, lens, p=3, mode=MODE_LSSAR, s
     """One new query row per head against a paged cache, in every mode.
 
     q: [B, H, d] of the cache's type (d contiguous, other strides multiples of
-    8), H a multiple of Hkv (query head h reads key head h // (H // Hkv)); the
-    cache as in :func:`lssar_paged_append`, the new token already appended.
-    Returns out [B, H, d], row lens[b] of the attention over each sequence's
-    cached tokens (zeros for an empty sequence).  scores: float32
-    [B, Hkv, max_pages * page_size]; each cached token's slot of scores_out
-    (default: scores itself) becomes scores plus the normalised weights that
-    the token gets from the query heads of its key head.
+    8), H a multiple of Hkv, at most 128 * Hkv (query head h reads key head
+    h // (H // Hkv)); the cache as in :func:`lssar_paged_append`, the new token
+    already appended.  Returns out [B, H, d], row lens[b] of the attention over
+    each sequence's cached tokens (zeros for an empty sequence).  scores:
+    float32 [B, Hkv, max_pages * page_size]; each cached token's slot of
+    scores_out (default: scores itself) becomes scores plus the normalised
+    weights that the token gets from the query heads of its key head.
+    Runs asynchronously on ``stream`` (default: the current stream).
     """
     import torch
-    desc = _paged_cache(k_pages, v_pages, table, lens)
-    dev = k_pages.device
-    if q.dim() != 3 or q.shape[0] != desc.B or q.shape[2] != desc.d or q.dtype != k_pages.dtype or q.device != dev:
+    desc, B, Hkv, cap, d, dev = _paged_cache(k_pages, v_pages, table, lens)
+    shape, dtype = q.shape, q.dtype
+    if (len(shape) != 3 or shape[0] != B or shape[2] != d or dtype is not k_pages.dtype or not q.is_cuda
+            or q.get_device() != dev):
         raise ValueError("q must be [B, H, d] with the cache's B, d, type and device")
-    if q.numel() and q.stride(2) != 1:
+    qst = q.stride()
+    if qst[2] != 1:
         raise ValueError("the last dimension of q must be contiguous")
     if scores is None and scores_out is not None:
         raise ValueError("scores_out needs scores")
-    if scores is not None and scores_out is None:
+    if scores_out is None:
         scores_out = scores
-    made = []
+    made = ()
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        made.append(out)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+        made = (out,)
+    elif (out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or not out.is_cuda
+          or out.get_device() != dev):
         raise ValueError("out must be a contiguous [B, H, d] tensor of q's type on the cache's device")
-    with torch.cuda.device(dev):
-        _check(load_library().lssar_paged_decode(
-            ctypes.byref(desc), q.data_ptr(), _longs(q.stride()[:2]), out.data_ptr(), q.shape[1], int(p), int(mode),
-            _slots("scores", scores, desc, torch.float32, dev), _slots("scores_out", scores_out, desc, torch.float32, dev),
-            _stream_of(stream, dev, *made)))
+    slots = (B, Hkv, cap)
+    _paged_call("lssar_paged_decode", dev, stream, made, desc, q.data_ptr(), _pack_2(*qst[:2]), out.data_ptr(), shape[1],
+                _int32("p", p), _int32("mode", mode), _slots("scores", scores, slots, torch.float32, dev),
+                _slots("scores_out", scores_out, slots, torch.float32, dev))
     return out
 
 
@@ -528,26 +560,25 @@ def lssar_paged_evict(k_pages, v_pages, table, lens, scores, positions, keep, re
     ``keep`` move into the evicted slots before it, in the pages as in scores
     and positions ([B, Hkv, max_pages * page_size] float32 and int32); with
     scores_out and positions_out (both or neither) these are read only.
-    Returns (new lengths, scores_out, positions_out).
+    Returns (new lengths, scores_out, positions_out).  Runs asynchronously on
+    ``stream`` (default: the current stream).
     """
     import torch
-    desc = _paged_cache(k_pages, v_pages, table, lens)
-    dev = k_pages.device
+    desc, B, Hkv, cap, d, dev = _paged_cache(k_pages, v_pages, table, lens)
     if (scores_out is None) != (positions_out is None):
         raise ValueError("scores_out and positions_out go together")
     if scores_out is None:
         scores_out, positions_out = scores, positions
-    made = []
+    made = ()
     if lens_out is None:
         lens_out = torch.empty_like(lens)
-        made.append(lens_out)
-    with torch.cuda.device(dev):
-        _check(load_library().lssar_paged_evict(
-            ctypes.byref(desc), _slots("scores", scores, desc, torch.float32, dev),
-            _slots("positions", positions, desc, torch.int32, dev), int(keep), int(recent), int(sinks),
-            _slots("scores_out", scores_out, desc, torch.float32, dev),
-            _slots("positions_out", positions_out, desc, torch.int32, dev),
-            _per_sequence("lens_out", lens_out, desc, dev), _stream_of(stream, dev, *made)))
+        made = (lens_out,)
+    slots = (B, Hkv, cap)
+    _paged_call("lssar_paged_evict", dev, stream, made, desc, _slots("scores", scores, slots, torch.float32, dev),
+                _slots("positions", positions, slots, torch.int32, dev), _int32("keep", keep), _int32("recent", recent),
+                _int32("sinks", sinks), _slots("scores_out", scores_out, slots, torch.float32, dev),
+                _slots("positions_out", positions_out, slots, torch.int32, dev),
+                _per_sequence("lens_out", lens_out, B, dev))
     return lens_out, scores_out, positions_out
 
 
