@@ -117,26 +117,44 @@ __device__ __forceinline__ int tiles_of(int n) {
     return (n + tile_keys(D) - 1) / tile_keys(D);
 }
 
+// Lengths as they are used: 0 where they are outside the cache.  (Those of many
+// sequences are asked for at once; the error word is written after them.)
+__device__ __forceinline__ int usable(int n, int capacity) { return (unsigned)n <= (unsigned)capacity ? n : 0; }
+
 // Tiles of sequences [0, upto) for one row of each (the whole warp calls it).
 template <int D>
 __device__ __forceinline__ int tiles_before(const PagedCache &c, int upto) {
+    const int cap = c.capacity();
     int x = 0;
-#pragma unroll 1
-    for (int b = threadIdx.x & 31; b < upto; b += 32) x += tiles_of<D>(paged_len(c, b));
+    bool bad = false;
+#pragma unroll 4
+    for (int b = threadIdx.x & 31; b < upto; b += 32) {
+        const int n = c.lens[b];
+        bad |= usable(n, cap) != n;
+        x += tiles_of<D>(usable(n, cap));
+    }
+    if (bad) atomicCAS(c.err, 0u, (unsigned)kErrPagedLength);
     return __reduce_add_sync(0xffffffffu, x);
 }
 
-// The place of tile t < total (the whole warp calls it).
+// The place of tile t < total (the whole warp calls it): eight sequences per lane.
 template <int D>
 __device__ __noinline__ Place locate(const PagedCache &c, int blocks, int t) {
-    const int lane = threadIdx.x & 31, rows_per_seq = c.Hkv * blocks;
+    const int lane = threadIdx.x & 31, rows_per_seq = c.Hkv * blocks, cap = c.capacity();
     Place p;
     int before = 0;
 #pragma unroll 1
-    for (int b0 = 0;; b0 += 32) {
-        const int b = b0 + lane;
-        const int n = b < c.B ? paged_len(c, b) : 0, nt = tiles_of<D>(n);
-        int end = nt * rows_per_seq;
+    for (int b0 = lane * 8;; b0 += 256) {
+        int n[8], sum = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) n[j] = b0 + j < c.B ? c.lens[b0 + j] : 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            n[j] = usable(n[j], cap);
+            sum += tiles_of<D>(n[j]);
+        }
+        int end = sum * rows_per_seq;
+        const int own = end;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, end, o);
@@ -144,12 +162,24 @@ __device__ __noinline__ Place locate(const PagedCache &c, int blocks, int t) {
         }
         const unsigned hit = __ballot_sync(0xffffffffu, before + end > t);
         if (hit) {
+            int in = t - (before + end - own), at = 0, len = 0;
+            bool found = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int tiles = tiles_of<D>(n[j]) * rows_per_seq;
+                if (!found && in < tiles) {
+                    found = true;
+                    at = b0 + j;
+                    len = n[j];
+                }
+                if (!found) in -= tiles;
+            }
             const int l = __ffs(hit) - 1;
-            p.n = __shfl_sync(0xffffffffu, n, l);
-            p.nt = __shfl_sync(0xffffffffu, nt, l);
-            const int in = t - (before + __shfl_sync(0xffffffffu, end, l) - p.nt * rows_per_seq);
+            in = __shfl_sync(0xffffffffu, in, l);
+            p.b = __shfl_sync(0xffffffffu, at, l);
+            p.n = __shfl_sync(0xffffffffu, len, l);
+            p.nt = tiles_of<D>(p.n);
             const int hr = in / p.nt;
-            p.b = b0 + l;
             p.tile = in - hr * p.nt;
             p.h = hr / blocks;
             p.nb = hr - p.h * blocks;

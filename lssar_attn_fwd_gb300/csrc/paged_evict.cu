@@ -337,12 +337,13 @@ cudaError_t launch_paged_evict(const PagedEvict &pr, void *ws, cudaStream_t stre
     if (e != cudaSuccess) return e;
     int *src = static_cast<int *>(ws), *dst = src + (size_t)a.c.B * a.c.Hkv * a.keep, *count = dst + (size_t)a.c.B * a.c.Hkv * a.keep;
     // CTAs per row by the longest row that the table has room for, in one wave of three
-    // per SM (96 rows of 16K tokens: 2, 4 and 8 CTAs each took 77, 68 and 82 us)
+    // per SM (96 rows of 16K tokens: 2, 4 and 8 CTAs each took 77, 68 and 82 us), or
+    // more while the keys do not fit shared memory
     const int cap = a.c.capacity();
     const long long rows = (long long)a.c.B * a.c.Hkv;
     int sms = 0, ctas = 1;
     if ((e = device_sms(&sms)) != cudaSuccess) return e;
-    while (ctas < kMaxCluster && cap > ctas * kChunk && 2 * ctas * rows <= 3 * sms) ctas *= 2;
+    while (ctas < kMaxCluster && cap > ctas * kChunk && (2 * ctas * rows <= 3 * sms || cap > ctas * kCachedKeys)) ctas *= 2;
     const int run = ((cap + ctas - 1) / ctas + 3) & ~3;
     e = run <= kCachedKeys ? launch_select<true>(a, src, dst, count, ctas, run, stream) : launch_select<false>(a, src, dst, count, ctas, run, stream);
     if (e != cudaSuccess) return e;

@@ -234,6 +234,16 @@ def test_decode_long_and_many(torch_mod, lens, hkv, G, d, page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mode,p", [(MODE_LSSAR, 3), (MODE_SOFTMAX, 1)])
+def test_decode_many_sequences(torch_mod, mode, p):
+    # more sequences than a warp looks over at once, most of them short or empty
+    lens = [(7 * b) % 23 if b % 3 else 0 for b in range(700)]
+    lens[0], lens[255], lens[256], lens[699] = 400, 129, 1, 300
+    c = Cache(torch_mod, lens, 2, 64, 16, seed=2)
+    check_decode(torch_mod, c, c.q(4), mode, p, c.slots(1e-2))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("mode,p", [(MODE_LSSAR, 15), (MODE_SOFTMAX_RW, 3), (MODE_SIGMOID_RW, 2), (MODE_LSSA, 1)])
 def test_decode_equal_keys_and_zero_rows(torch_mod, mode, p):
     # equal keys: the uniform row; zero queries and keys: the norm's floor
@@ -416,6 +426,37 @@ def test_evict(torch_mod, kind, lens, keep, recent, sinks, d, page, hkv, in_plac
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens,keep,width", [([300, 90], 64, 10000), ([20000, 3], 5000, 1400), ([20000, 19999], 19000, 1251)])
+def test_evict_wide_tables_and_long_rows(torch_mod, lens, keep, width):
+    # room for 160000 tokens: keys that do not fit shared memory; rows over several CTAs
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    c = Cache(torch, lens, 1, 64, 16, width=width, seed=keep)
+    scores = evict_scores(torch, c, "ties")
+    pos = torch.arange(c.cap, dtype=torch.int32).repeat(2, 1, 1).cuda()
+    bits = lambda t: host(t.view(torch.int16))   # noqa: E731
+    want = po.paged_evict(bits(c.k), bits(c.v), host(c.table), lens, host(scores), host(pos), keep, 30, 2)
+    new, _, _ = api.lssar_paged_evict(*c.args(), scores, pos, keep, recent=30, sinks=2)
+    assert api.device_error_word() == 0 and new.tolist() == want[4].tolist()
+    assert np.array_equal(bits(c.k), want[0]) and np.array_equal(bits(c.v), want[1])
+    assert np.array_equal(host(scores), want[2]) and np.array_equal(host(pos), want[3])
+
+
+@pytest.mark.gpu
+def test_evict_many_rows(torch_mod):
+    # more rows than fit the GPU at once, each over several CTAs
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    c = Cache(torch, [2300] * 12, 40, 64, 128, seed=9)
+    scores = c.slots()
+    pos = torch.arange(c.cap, dtype=torch.int32).repeat(12, 40, 1).cuda()
+    bits = lambda t: host(t.view(torch.int16))   # noqa: E731
+    want = po.paged_evict(bits(c.k), bits(c.v), host(c.table), [2300] * 12, host(scores), host(pos), 1000)
+    api.lssar_paged_evict(*c.args(), scores, pos, 1000)
+    assert np.array_equal(bits(c.k), want[0]) and np.array_equal(host(scores), want[2]) and np.array_equal(host(pos), want[3])
+
+
+@pytest.mark.gpu
 def test_evict_bad_lengths_and_pages(torch_mod):
     torch = torch_mod
     from lssar_attn_fwd_gb300 import api
@@ -523,3 +564,47 @@ def test_streams_and_graphs(torch_mod):
         for name in ("scores", "pos", "out", "after", "lens"):
             assert torch.equal(bits(a[name]), bits(b[name])), name
         assert torch.equal(bits(a["c"].k), bits(b["c"].k)) and torch.equal(bits(a["c"].v), bits(b["c"].v))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,page,half", [(64, 16, False), (128, 24, True)])
+def test_debug_build_checks_fire_nowhere(torch_mod, monkeypatch, d, page, half):
+    # the debug-check build (bounds checks that record a code) gives the same bits and records nothing
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api, build
+    build.build(debug=True)
+    results = []
+    for lib in (api.load_library(), api.load_debug_library()):
+        monkeypatch.setattr(api, "_LIB", lib)
+        c = Cache(torch, LENS_MIX, 2, d, page, half=half, seed=5)
+        q, scores, got = c.q(6), c.slots(), []
+        for mode, p in MODES:
+            so = torch.zeros_like(scores)
+            got += [api.lssar_paged_decode(q, *c.args(), p=p, mode=mode, scores=scores, scores_out=so), so]
+        pos = torch.arange(c.cap, dtype=torch.int32).repeat(c.B, 2, 1).cuda()
+        got += list(api.lssar_paged_evict(*c.args(), scores, pos, 100, recent=9)) + [c.k, c.v]
+        torch.cuda.synchronize()
+        assert api.device_error_word() == 0
+        results.append(got)
+    for a, b in zip(*results):
+        view = torch.int16 if a.element_size() == 2 else torch.int32
+        assert torch.equal(a.view(view), b.view(view))
+
+
+@pytest.mark.gpu
+def test_calls_on_two_streams_at_once(torch_mod):
+    # decode steps of two caches, each on a stream of its own, interleaved without any wait between them
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    caches = [Cache(torch, [3000, 17, 900], 4, 64, 16, seed=s) for s in (1, 2)]
+    qs = [c.q(8) for c in caches]
+    want = [api.lssar_paged_decode(q, *c.args(), p=15) for q, c in zip(qs, caches)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(20):
+        for i in (0, 1):
+            got[i].append(api.lssar_paged_decode(qs[i], *caches[i].args(), p=15, stream=streams[i]))
+    torch.cuda.synchronize()
+    assert api.device_error_word() == 0
+    for i in (0, 1):
+        assert all(torch.equal(x, want[i]) for x in got[i])
