@@ -357,7 +357,15 @@ __device__ __forceinline__ void produce(const Args &g, const CUtensorMap *km, co
         // the next tile's pages are looked up while this one waits for its stage
         const bool more = ++p.t < t1;
         if (more) {
-            if (++p.tile == p.nt) next_row<D>(c, g.sp.blocks, p);
+            if (++p.tile == p.nt) {
+                next_row<D>(c, g.sp.blocks, p);
+                // the compute warps will want that row's queries soon (64 short sequences:
+                // 39.3 -> 38.1 us, a ragged batch 91 -> 87)
+                if (PHASE != kValues && lane < min(kHeads, g.sp.G - p.nb * kHeads) * (D / 64)) {
+                    const uint16_t *q = static_cast<const uint16_t *>(g.a.q) + p.b * g.a.q_b + (p.h * g.sp.G + p.nb * kHeads + lane / (D / 64)) * g.a.q_h;
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane % (D / 64) * 64));
+                }
+            }
             look_up();
         }
 #pragma unroll 1

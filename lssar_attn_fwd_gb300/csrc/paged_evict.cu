@@ -41,7 +41,7 @@ constexpr int kMoveThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;            // portable cluster size
 constexpr int kCachedKeys = 18432;        // keys per CTA held in shared memory: three CTAs per SM
-constexpr int kChunk = 2048;              // slots per CTA that are worth another CTA
+constexpr int kChunk = 4096;              // slots per CTA that are worth another CTA
 constexpr int kMoves = 2;                 // rows that a group of threads moves at once
 
 // Key of a score (see above), and whether its token is protected.
@@ -66,6 +66,12 @@ __device__ __forceinline__ int ld_cluster(const void *p, int rank) {
     int v;
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ptx::cluster_map(ptx::smem_u32(p), (uint32_t)rank)) : "memory");
     return v;
+}
+
+// Barrier of the row's CTAs.
+__device__ __forceinline__ void row_sync(int ctas) {
+    if (ctas == 1) __syncthreads();
+    else ptx::cluster_sync();
 }
 
 // Exclusive prefix sums of x and y over the block, in thread order; *tx, *ty: the block's sums.
@@ -110,6 +116,7 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
     __shared__ Shared sh;
     __shared__ int2 red[kWarps];
     __shared__ unsigned s_bin, s_left;
+    __shared__ bool s_all;
     const int bh = blockIdx.x / ctas, rank = blockIdx.x % ctas, b = bh / c.Hkv, h = bh % c.Hkv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = paged_len(c, b);
@@ -146,7 +153,7 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
         newest = __reduce_max_sync(0xffffffffu, lane < kWarps ? red[lane].x : INT_MIN);
         if (lane == 0) sh.newest = newest;
     }
-    ptx::cluster_sync();
+    row_sync(ctas);
     newest = __reduce_max_sync(0xffffffffu, lane < ctas ? ld_cluster(&sh.newest, lane) : INT_MIN);
     if (CACHED) {
 #pragma unroll 8
@@ -173,7 +180,7 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
             const unsigned bin = in ? (key >> shift) & 255u : 256u, peers = __match_any_sync(0xffffffffu, bin);
             if (in && lane == __ffs(peers) - 1) atomicAdd(&sh.hist[pass][bin], (unsigned)__popc(peers));
         }
-        ptx::cluster_sync();
+        row_sync(ctas);
         // sums over the cluster, then from the highest bin down: thread t has bin 255 - t
         int cnt = 0, zero = 0, t0, t1;
         if (threadIdx.x < 256)
@@ -187,16 +194,23 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
         if (threadIdx.x < 256 && above < (int)left && above + cnt >= (int)left) {
             s_bin = 255 - threadIdx.x;
             s_left = left - above;
+            s_all = above + cnt == (int)left;
         }
         __syncthreads();
         prefix |= s_bin << shift;
         left = s_left;
+        if (s_all) {   // the whole bin stays: every key from its least on, and none is equal to `prefix`
+            prefix -= 1;
+            left = 0;
+            break;
+        }
     }
     // of the keys equal to `prefix` the first `left` stay: those of the CTAs
     // before this one are in the last histogram
     int eq_before = 0;
+    if (left)
 #pragma unroll 1
-    for (int r = 0; r < rank; ++r) eq_before += ld_cluster(&sh.hist[3][prefix & 255u], r);
+        for (int r = 0; r < rank; ++r) eq_before += ld_cluster(&sh.hist[3][prefix & 255u], r);
     // thread t owns consecutive slots, an odd number of them: no two lanes of a read meet
     // in a bank of shared memory
     const int per = ((hi - lo + kThreads - 1) / kThreads) | 1;
@@ -217,7 +231,7 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
         sh.holes = t0;
         sh.movers = t1;
     }
-    ptx::cluster_sync();
+    row_sync(ctas);
     int total = 0;
     for (int r = 0; r < ctas; ++r) {
         const int x = ld_cluster(&sh.holes, r), y = ld_cluster(&sh.movers, r);
@@ -235,7 +249,7 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
         if (j >= a.keep && s) from_list[movers++] = j;
     }
     if (rank == 0 && threadIdx.x == 0) count[bh] = total;
-    ptx::cluster_sync();   // no CTA's shared memory is read after this
+    row_sync(ctas);   // no CTA's shared memory is read after this
 }
 
 // Moves the rows of the lists: `splits` blocks per (sequence, key head).
