@@ -282,16 +282,21 @@ int lssar_paged_append(const lssar_paged_cache_t *cache, const void *k_new, cons
  *   q   : [B, H, d] of the cache's type; q_strides is a HOST array of the
  *         element strides of (B, H), multiples of 8 where the dimension is above 1.
  *   out : [B, H, d] contiguous, of the cache's type, written.
- *   H   : query heads, a multiple of Hkv.
+ *   H   : query heads, a multiple of Hkv, at most 128 * Hkv.
  *   scores, scores_out : [B, Hkv, capacity] float32, both or neither:
  *         scores_out[b][h][s] = scores[b][h][s] + the normalised weights of slot
  *         s of the query heads of h, for s < lens[b]; other slots are not
  *         written.  scores_out may be scores itself.
  * A sequence of length 0 gets out = 0.  One with a bad length gets NaN rows and
  * no scores; with a bad page number, NaN rows and NaN scores in the heads.
- * Results do not depend on the order of anything: the same call gives the same
- * bits.  Scratch: about 4 B * H * (capacity + d) bytes from the library's pool.
- * Errors as lssar_paged_append, and LSSAR_ERR_MODE, LSSAR_ERR_P.
+ * The sums have a fixed order: the same call on the same device gives the same
+ * bits.  Two launches (softmax, LSSA) or three (re-weighting modes, which need a
+ * row's scores before its weights).  Scratch from the library's pool: partial
+ * sums, about 4 * (d + 4) bytes for each of B * H + 3 * 8 * SMs segments, and in
+ * the re-weighting modes or with scores 4 bytes for each (query head, slot) that
+ * the table has room for.  Errors as lssar_paged_append, and LSSAR_ERR_MODE,
+ * LSSAR_ERR_P; LSSAR_ERR_SHAPE also when B * Hkv * ceil(H / (8 Hkv)) *
+ * ceil(capacity / 64) passes 2^31 - 1.
  */
 int lssar_paged_decode(const lssar_paged_cache_t *cache, const void *q, const long long *q_strides, void *out, int H,
                        int p, int mode, const float *scores, float *scores_out, cudaStream_t stream);
@@ -313,7 +318,9 @@ int lssar_paged_decode(const lssar_paged_cache_t *cache, const void *q, const lo
  * Sequences must not share pages with one another here, except pages in which
  * nothing moves.  A bad length: nothing moves, lens_out[b] = lens[b]; rows
  * to or from a bad page number are not copied.
- * Scratch: 8 B * Hkv * keep bytes.  Errors as above, and LSSAR_ERR_KEEP.
+ * Two launches: the selection, a thread-block cluster per (sequence, key head),
+ * and the moves.  Scratch: B * Hkv * (8 keep + 4) bytes.  Errors as above, and
+ * LSSAR_ERR_KEEP.
  */
 int lssar_paged_evict(const lssar_paged_cache_t *cache, const float *scores, const int *positions, int keep, int recent,
                       int sinks, float *scores_out, int *positions_out, int *lens_out, cudaStream_t stream);

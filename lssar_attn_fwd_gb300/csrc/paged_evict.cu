@@ -16,16 +16,15 @@
 // the row's slots and keeps their keys in shared memory, so that scores are read
 // once and positions twice.  The keep-th largest key is found by its four bytes
 // from the highest down: 256-bin histograms whose sums over the cluster meet
-// in distributed shared memory (lanes with equal bytes add once: the leading
-// bytes of accumulated weights are nearly all the same).  Then each thread
-// walks its own consecutive slots, and prefix sums over the block and the cluster
-// number the holes and the movers, whose lists go to scratch.
+// in distributed shared memory.  Then each warp
+// walks its own stretch of slots, ballots and sums over the block and the cluster
+// number the holes and the movers, and their lists go to scratch.
 // paged_move: all SMs move the rows, 16 bytes a lane, two rows of a group of
 // threads at once.  (Moved by the selecting clusters, which leave SMs idle and
 // have few loads in flight, 32 rows of 128K tokens took 226 us.)
 //
 // Bound by HBM for long rows (8 bytes of each slot, 8d of each moved row), by
-// the eight barriers of the selection (a few us each with their code) for short ones.
+// the eight barriers of the selection (about a us each with their code) for short ones.
 #include <climits>
 #include <cstdlib>
 
@@ -43,6 +42,8 @@ constexpr int kMaxCluster = 8;            // portable cluster size
 constexpr int kCachedKeys = 18432;        // keys per CTA held in shared memory: three CTAs per SM
 constexpr int kChunk = 4096;              // slots per CTA that are worth another CTA
 constexpr int kMoves = 2;                 // rows that a group of threads moves at once
+
+constexpr unsigned kZeroKey = 0x80000000u;   // of a score 0
 
 // Key of a score (see above), and whether its token is protected.
 __device__ __forceinline__ unsigned score_key(float s) {
@@ -130,6 +131,7 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
     // slots [lo, hi) are this CTA's
     const int run = ((n + ctas - 1) / ctas + 3) & ~3, lo = min(n, rank * run), hi = min(n, lo + run);
     if (a.scores != a.scores_out)   // the holes' values follow below
+#pragma unroll 4
         for (int j = lo + threadIdx.x; j < min(hi, a.keep); j += kThreads) {
             sc_out[j] = sc[j];
             pos_out[j] = pos[j];
@@ -171,14 +173,24 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
+        unsigned zeros = 0, safes = 0;
 #pragma unroll 2
         for (int i = 0; i < steps; ++i) {   // (a thread meets the keys that it made)
             const int j = lo + i * kThreads + threadIdx.x;
             const unsigned key = j < hi ? key_of(j) : 0u;
-            // lanes out of the count share a bin number of their own
             const bool in = j < hi && (pass == 0 || (key >> (shift + 8)) == (prefix >> (shift + 8)));
-            const unsigned bin = in ? (key >> shift) & 255u : 256u, peers = __match_any_sync(0xffffffffu, bin);
-            if (in && lane == __ffs(peers) - 1) atomicAdd(&sh.hist[pass][bin], (unsigned)__popc(peers));
+            // counted apart: many tokens have no weight at all, and protected ones come
+            // together (lanes with equal bins found by a match cost more than they saved)
+            const bool zero = key == kZeroKey, safe = key == 0xffffffffu;
+            zeros += in && zero;
+            safes += in && safe;
+            if (in && !zero && !safe) atomicAdd(&sh.hist[pass][(key >> shift) & 255u], 1u);
+        }
+        zeros = __reduce_add_sync(0xffffffffu, zeros);
+        safes = __reduce_add_sync(0xffffffffu, safes);
+        if (lane == 0) {
+            if (zeros) atomicAdd(&sh.hist[pass][(kZeroKey >> shift) & 255u], zeros);
+            if (safes) atomicAdd(&sh.hist[pass][255], safes);
         }
         row_sync(ctas);
         // sums over the cluster, then from the highest bin down: thread t has bin 255 - t
@@ -211,28 +223,50 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
     if (left)
 #pragma unroll 1
         for (int r = 0; r < rank; ++r) eq_before += ld_cluster(&sh.hist[3][prefix & 255u], r);
-    // thread t owns consecutive slots, an odd number of them: no two lanes of a read meet
-    // in a bank of shared memory
-    const int per = ((hi - lo + kThreads - 1) / kThreads) | 1;
-    const int j0 = min(hi, lo + (int)threadIdx.x * per), j1 = min(hi, j0 + per);
-    int eq = 0, zero = 0, t0, t1;
-    for (int j = j0; j < j1; ++j) eq += key_of(j) == prefix;
-    block_scan(eq, zero, red, &t0, &t1);
-    const int rank0 = eq_before + eq;
+    // each warp walks its own stretch of slots in order, 32 at a time; ballots rank
+    // the slots within it
+    const int stretch = (((hi - lo + kWarps - 1) / kWarps) + 31) & ~31;
+    const int w0 = min(hi, lo + warp * stretch), w1 = min(hi, w0 + stretch);
+    const unsigned below = (1u << lane) - 1;
+    int eq = 0;
+    if (left)
+#pragma unroll 2
+        for (int j = w0 + lane; j - lane < w1; j += 32) eq += __popc(__ballot_sync(0xffffffffu, j < w1 && key_of(j) == prefix));
+    __syncthreads();
+    if (lane == 0) red[warp] = make_int2(eq, 0);
+    __syncthreads();
+    int rank0 = eq_before + __reduce_add_sync(0xffffffffu, lane < warp ? red[lane].x : 0);
+    // whether slot j (of this lane) stays; counts the keys equal to `prefix` as it goes
+    auto stays = [&](int j, int &seen) {
+        const unsigned key = j < w1 ? key_of(j) : 0u;
+        const bool same = j < w1 && key == prefix;
+        const unsigned all = __ballot_sync(0xffffffffu, same);
+        const bool s = j < w1 && (key > prefix || (same && seen + __popc(all & below) < (int)left));
+        seen += __popc(all);
+        return s;
+    };
     int holes = 0, movers = 0, seen = rank0;
-    auto stays = [&](unsigned key) { return key > prefix || (key == prefix && seen++ < (int)left); };
-    for (int j = j0; j < j1; ++j) {
-        const bool s = stays(key_of(j));
-        holes += j < a.keep && !s;
-        movers += j >= a.keep && s;
+#pragma unroll 2
+    for (int j = w0 + lane; j - lane < w1; j += 32) {
+        const bool s = stays(j, seen);
+        holes += __popc(__ballot_sync(0xffffffffu, j < w1 && j < a.keep && !s));
+        movers += __popc(__ballot_sync(0xffffffffu, j >= a.keep && s));
     }
-    block_scan(holes, movers, red, &t0, &t1);
-    if (threadIdx.x == 0) {
-        sh.holes = t0;
-        sh.movers = t1;
+    __syncthreads();
+    if (lane == 0) red[warp] = make_int2(holes, movers);
+    __syncthreads();
+    holes = __reduce_add_sync(0xffffffffu, lane < warp ? red[lane].x : 0);
+    movers = __reduce_add_sync(0xffffffffu, lane < warp ? red[lane].y : 0);
+    if (warp == 0) {
+        const int x = __reduce_add_sync(0xffffffffu, lane < kWarps ? red[lane].x : 0), y = __reduce_add_sync(0xffffffffu, lane < kWarps ? red[lane].y : 0);
+        if (lane == 0) {
+            sh.holes = x;
+            sh.movers = y;
+        }
     }
     row_sync(ctas);
     int total = 0;
+#pragma unroll 1
     for (int r = 0; r < ctas; ++r) {
         const int x = ld_cluster(&sh.holes, r), y = ld_cluster(&sh.movers, r);
         if (r < rank) {
@@ -243,10 +277,14 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
     }
     int *to_list = dst + (size_t)bh * a.keep, *from_list = src + (size_t)bh * a.keep;
     seen = rank0;
-    for (int j = j0; j < j1; ++j) {
-        const bool s = stays(key_of(j));
-        if (j < a.keep && !s) to_list[holes++] = j;
-        if (j >= a.keep && s) from_list[movers++] = j;
+#pragma unroll 2
+    for (int j = w0 + lane; j - lane < w1; j += 32) {
+        const bool s = stays(j, seen), hole = j < w1 && j < a.keep && !s, mover = j >= a.keep && s;
+        const unsigned hm = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
+        if (hole) to_list[holes + __popc(hm & below)] = j;
+        if (mover) from_list[movers + __popc(mm & below)] = j;
+        holes += __popc(hm);
+        movers += __popc(mm);
     }
     if (rank == 0 && threadIdx.x == 0) count[bh] = total;
     row_sync(ctas);   // no CTA's shared memory is read after this

@@ -92,6 +92,8 @@ def test_bad_decodes_are_refused(lib):
     assert decode(lib, desc(), so=None) == -1
     assert decode(lib, desc(), H=3) == -2
     assert decode(lib, desc(), H=0) == -2
+    assert decode(lib, desc(), H=2 * 129) == -2
+    assert decode(lib, desc(B=1 << 10, max_pages=1 << 20, Hkv=16, page_stride=1 << 14), H=16) == -2
     assert decode(lib, desc(), mode=5) == -5
     assert decode(lib, desc(), p=0) == -4
     assert decode(lib, desc(), p=1025) == -4
