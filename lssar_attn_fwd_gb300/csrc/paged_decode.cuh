@@ -18,7 +18,7 @@
 // of any mix load the SMs evenly.  The part of a row inside one run is a segment.
 // The lengths are on the device: each warp finds its run by a prefix sum.
 //   softmax, LSSA: paged_stream<kBoth>   one pass over K and V tiles, weights
-//                  relative to a running maximum (softmax);
+//                  relative to a running maximum;
 //   re-weighting:  paged_stream<kScores> K tiles -> z (scratch), (m, S1) per segment,
 //                  paged_stream<kValues> row constants from all of the row's
 //                  segments, z -> w, V tiles (asked for before the scores are in,
@@ -96,7 +96,7 @@ struct Split {
 struct Scratch {
     float *z;              // [tile][zg][keys]: z, then w (re-weighting with scores)
     float2 *stats;         // [segment][zg]: max of z, sum of phi
-    float2 *sums;          // [segment][zg]: reference of the exponent (softmax), sum of w
+    float2 *sums;          // [segment][zg]: reference of the exponent (softmax, LSSA), sum of w
     float *o;              // [segment][zg][D]: sum of w v
 };
 
@@ -302,6 +302,18 @@ __device__ __forceinline__ float2 shuffle_xor(float2 x, int o) {
     return make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o));
 }
 
+// The weight of a score in the one-pass modes, relative to 2^ref: 2^(z - ref), or
+// log2(1 + 2^z) 2^-ref with lift = 2^-ref.  A row whose keys all point away from the
+// query has z down to -116, so that the logarithm near 1 (which is 0 from z = -24 on)
+// gives way to its series, log2(e) (u - u^2/2 + u^3/3), u = 2^-|z| < 2^-6: off by u^3/4 < 2^-20.
+template <int MODE>
+__device__ __forceinline__ float weight(float z, float ref, float lift) {
+    if (MODE == kSoftmax) return ptx::ex2(z - ref);
+    const float u = ptx::ex2(-fabsf(z));
+    const float series = 1.4426950408889634f * u * fmaf(u, fmaf(u, 1.f / 3.f, -0.5f), 1.f);
+    return (fmaxf(z, 0.f) + (u < 0.015625f ? series : ptx::lg2(1.f + u))) * lift;
+}
+
 // Row constants m, kappa, beta from the row's maximum and normaliser sum.  (An
 // error in kappa's last bits scales all of the row's weights alike.)
 template <int MODE>
@@ -478,7 +490,7 @@ __global__ void __launch_bounds__(kBlock, (Config<D, PHASE>::kPerSm))
 paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm, const __grid_constant__ Args g) {
     using C = Config<D, PHASE>;
     constexpr bool kRaw = MODE == kSoftmax || MODE == kSoftmaxRw;
-    constexpr bool kRelative = PHASE == kScores ? kRaw : MODE == kSoftmax;   // sums relative to 2^m
+    constexpr bool kRelative = PHASE == kScores ? kRaw : PHASE == kBoth;   // sums relative to 2^reference
     extern __shared__ uint8_t dyn[];
     __shared__ Shared sh;
     const PagedCache &c = g.a.c;
@@ -532,7 +544,8 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
         const int seg = row + blockIdx.x, g0 = p.nb * kHeads, heads = min(kHeads, g.sp.G - g0), cnt = min(t1 - p.t, p.nt - p.tile);
         const bool mine = head < heads;
         bad = false;
-        float2 st = make_float2(kRelative || PHASE == kScores ? kLowest : 0.f, 0.f);   // (maximum or reference, sum of phi or w)
+        float2 st = make_float2(PHASE == kValues ? 0.f : kLowest, 0.f);   // (maximum or reference, sum of phi or w)
+        float lift = 0.f;   // LSSA: 2^-reference
         float o[PHASE == kScores ? 1 : D / 8][4];
         if constexpr (PHASE != kScores) {
 #pragma unroll
@@ -673,12 +686,9 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
                     for (int u = 0; u < C::kEights; ++u) *reinterpret_cast<float2 *>(zrow + 8 * u) = z[u];
                     zrow += g.sp.zg * C::kTile;
                 }
-                float top = st.x;
-                if (PHASE == kScores || MODE == kSoftmax) {
-                    top = fmaxf(z[0].x, z[0].y);
+                float top = fmaxf(z[0].x, z[0].y);
 #pragma unroll
-                    for (int u = 1; u < C::kEights; ++u) top = fmaxf(top, fmaxf(z[u].x, z[u].y));
-                }
+                for (int u = 1; u < C::kEights; ++u) top = fmaxf(top, fmaxf(z[u].x, z[u].y));
                 if constexpr (PHASE == kScores) {
                     top = fmaxf(top, st.x);
                     if (kRaw) st.y *= ptx::ex2(st.x - top);
@@ -686,25 +696,27 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
 #pragma unroll
                     for (int u = 0; u < C::kEights; ++u) st.y += phi(MODE, z[u].x, top) + phi(MODE, z[u].y, top);
                 } else {
-                    if (MODE == kSoftmax) {
-                        // weights 2^(z - m); m follows the maximum only when it has grown by
-                        // more than 8, so that weights stay below 2^8 and rescaling is rare
-                        if (__any_sync(0xffffffffu, top > st.x + 8.f)) {
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                            top = fmaxf(top, st.x);
-                            const float f = ptx::ex2(st.x - top);
-                            st = make_float2(top, st.y * f);
+                    // weights relative to 2^m (softmax), or to 2^min(m, 0) (LSSA, whose weights
+                    // are about 2^z there: 16 bits would lose them); the reference follows the
+                    // maximum only when it has grown by more than 8, so that softmax's weights
+                    // stay below 2^8, LSSA's (at most 118 2^8) in range, and rescaling is rare
+                    if (MODE != kSoftmax) top = fminf(top, 0.f);
+                    if (__any_sync(0xffffffffu, top > st.x + 8.f)) {
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        top = fmaxf(top, st.x);
+                        const float f = ptx::ex2(st.x - top);
+                        st = make_float2(top, st.y * f);
+                        if (MODE != kSoftmax) lift = top > kLowest ? ptx::ex2(-top) : 0.f;
 #pragma unroll
-                            for (int k = 0; k < D / 8; ++k)
+                        for (int k = 0; k < D / 8; ++k)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) o[k][e] *= f;
-                        }
+                            for (int e = 0; e < 4; ++e) o[k][e] *= f;
                     }
                     uint2 ws[C::kEights];
 #pragma unroll
                     for (int u = 0; u < C::kEights; ++u) {
-                        const float2 y = make_float2(phi(MODE, z[u].x, st.x), phi(MODE, z[u].y, st.x));
+                        const float2 y = make_float2(weight<MODE>(z[u].x, st.x, lift), weight<MODE>(z[u].y, st.x, lift));
                         st.y += y.x + y.y;
                         ws[u] = split_weights<T>(y);
                     }
@@ -774,7 +786,7 @@ __device__ __forceinline__ float2 join_sums(const float2 *at, int zg, int count)
 template <typename T, int D, int MODE, bool SCORES>
 __global__ void __launch_bounds__(kJoinThreads, 4) paged_join(const __grid_constant__ Args g, int join_blocks, int warps_per) {
     constexpr int kPerLane = D / 32, kTile = tile_keys(D);
-    constexpr bool kRelative = MODE == kSoftmax;
+    constexpr bool kRelative = !is_reweight(MODE);
     const PagedCache &c = g.a.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = g.sp.G;
     const int per_row = tiles_before<D>(c, c.B), total = per_row * g.sp.heads_rows, run = max(1, (total + g.sp.ctas - 1) / g.sp.ctas);
@@ -855,7 +867,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join(const __grid_const
         for (int x = warp; x < G; x += kJoinWarps) {
             const Segments sg = segments_of(p.b * g.sp.heads_rows + p.h * g.sp.blocks + x / kHeads, start + x / kHeads * p.nt, p.nt, run);
             const float2 all = join_sums<kRelative>(g.s.sums + (long long)sg.first * g.sp.zg + x % kHeads, g.sp.zg, sg.count);
-            if (lane == 0) rowf[x] = make_float2(all.x, ptx::rcp(all.y));
+            if (lane == 0) rowf[x] = make_float2(all.x, ptx::rcp(all.y) * (MODE == kLssa ? ptx::ex2(-all.x) : 1.f));
         }
         __syncthreads();
 #pragma unroll 1
@@ -870,7 +882,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join(const __grid_const
                 const long long tile = start + x / kHeads * p.nt + p.tile + i;
                 float4 w = __ldcg(reinterpret_cast<const float4 *>(&g.s.z[(tile * g.sp.zg + x % kHeads) * kTile + in]));
                 const float2 f = rowf[x];
-                if (!is_reweight(MODE)) w = make_float4(phi(MODE, w.x, f.x), phi(MODE, w.y, f.x), phi(MODE, w.z, f.x), phi(MODE, w.w, f.x));
+                if (!is_reweight(MODE)) w = make_float4(weight<MODE>(w.x, f.x, 1.f), weight<MODE>(w.y, f.x, 1.f), weight<MODE>(w.z, f.x, 1.f), weight<MODE>(w.w, f.x, 1.f));
                 add = make_float4(fmaf(w.x, f.y, add.x), fmaf(w.y, f.y, add.y), fmaf(w.z, f.y, add.z), fmaf(w.w, f.y, add.w));
             }
             if (vec && have >= 4) {

@@ -261,6 +261,83 @@ def test_decode_equal_keys_and_zero_rows(torch_mod, mode, p):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [40, 300, 5000])
+@pytest.mark.parametrize("d,half", [(64, True), (128, False), (128, True)])
+def test_decode_keys_away_from_the_query(torch_mod, n, d, half):
+    # LSSA: every score far below 0, where log(1 + e^x) is about e^x and down to e^-41
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    c = Cache(torch, [n, 3], 1, d, 16, half=half, seed=n)
+    q = c.q(2)
+    for b, count in enumerate((n, 3)):
+        slot = torch.arange(count)
+        away = -q[b, 0].float().cpu() + 0.3 * torch.randn(count, d, generator=c.g)
+        c.k[c.table[b].long().cpu()[slot // 16].cuda(), 0, (slot % 16).cuda()] = away.to(c.dt).cuda()
+    scores = torch.zeros(2, 1, c.cap, device="cuda")
+    out = api.lssar_paged_decode(q, *c.args(), mode=MODE_LSSA, scores=scores)
+    assert api.device_error_word() == 0
+    for b, count in enumerate((n, 3)):
+        kb, vb = (po.gather(host(x), c.table[b].tolist(), count)[:, 0] for x in (c.k, c.v))
+        w = po.row_weights(host(q[b]), kb, MODE_LSSA)
+        # a weight moves by no more than its score does, d log softplus(x) / dx <= 1, which
+        # is |dx| <= (2d + 16) u x_max, u = 2^-24, as in the oracle (sum |q_c k_c| <= |q| |k|) and 4u |x|,
+        # and by 2^-16 of itself: series 2^-20, exponential 2^-22, or logarithm 2^-22 of at
+        # least 2^-5.5; the sum of weights by as much again
+        x_max = po.length_scale(count, d)
+        rel = 2 * ((2 * d + 20) * 2.0 ** -24 * x_max + 2.0 ** -16)
+        # the value product: 2^-15 and the sum's rounding as in the oracle; in fp16 also half
+        # a step of the least weights, 2^-25 against a sum of 2^-1 or more
+        e = (rel + 2.0 ** -15 + (count / 4 + 64) * 2.0 ** -24) * w + (2.0 ** -24 if half else 0.0)
+        ref = w @ vb
+        tol = e @ np.abs(vb)
+        tol = tol + torch.finfo(c.dt).eps / 2 * (np.abs(ref) + tol) + (2.0 ** -25 if half else 0.0)
+        assert (np.abs(host(out[b]) - ref) <= tol).all()
+        got = host(scores[b, 0, :count])
+        assert (np.abs(got - w.sum(axis=0)) <= (rel + (count / 16 + 64) * 2.0 ** -24) * w.sum(axis=0)).all()
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(torch_mod):
+    # pages 2^28 + 8 elements apart, the last ones past 2^31 elements: the same bits as close together
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    n_pages, hkv, page, d, far = 10, 2, 16, 64, 2 ** 28 + 8
+    g = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(n_pages, hkv, page, d, generator=g).bfloat16().cuda() for _ in range(2))
+    pool = torch.empty(n_pages * far, dtype=torch.bfloat16, device="cuda")
+    shape, strides = (n_pages, hkv, page, d), (far, page * d, d, 1)
+    kf, vf = pool.as_strided(shape, strides), pool.as_strided(shape, strides, 2 ** 27)
+    kf.copy_(k)
+    vf.copy_(v)
+    table = torch.tensor([[9, 0, 8, 2], [7, 1, 6, 3]], dtype=torch.int32).cuda()
+    lens = torch.tensor([20, 41], dtype=torch.int32).cuda()
+    new = torch.randn(2, 2, hkv, 10, d, generator=g).bfloat16().cuda()
+    q = torch.randn(2, 3 * hkv, d, generator=g).bfloat16().cuda()
+
+    def serve(k, v):
+        scores = torch.zeros(2, hkv, 4 * page, device="cuda")
+        positions = torch.arange(4 * page, dtype=torch.int32).repeat(2, hkv, 1).cuda()
+        n = api.lssar_paged_append(new[0], new[1], k, v, table, lens, scores=scores, positions=positions)
+        out = api.lssar_paged_decode(q, k, v, table, n, scores=scores)
+        n, _, _ = api.lssar_paged_evict(k, v, table, n, scores, positions, 25, recent=5)
+        soft = api.lssar_paged_decode(q, k, v, table, n, mode=MODE_SOFTMAX)
+        return [n, out, soft, scores, positions, k, v]
+
+    close, apart = serve(k, v), serve(kf, vf)
+    assert api.device_error_word() == 0
+    assert close[0].tolist() == [25, 25] and close[1].isfinite().all() and close[2].isfinite().all()
+    for x, y in zip(close, apart):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_decode_largest_group(torch_mod):
+    c = Cache(torch_mod, [130, 0, 700], 1, 64, 16, seed=6)
+    for mode, p in ((MODE_LSSAR, 3), (MODE_SOFTMAX, 1), (MODE_LSSA, 1)):
+        check_decode(torch_mod, c, c.q(128), mode, p, c.slots(1e-2))
+
+
+@pytest.mark.gpu
 def test_decode_wide_table_strided_query_and_in_place_scores(torch_mod):
     torch = torch_mod
     from lssar_attn_fwd_gb300 import api
