@@ -336,7 +336,7 @@ __device__ void weights_from_stats(float2 hs, int L, int mode, int p, const floa
         const float zj = z[jj];
         float wj;
         if (mode == kSoftmax) wj = exp2f(zj - m);
-        else if (mode == kLssa) wj = sp2_any(zj);
+        else if (mode == kLssa) wj = phi(mode, zj, m);
         else wj = uniform ? 1.f : powi(fmaxf(phi(mode, zj, m) * kappa + beta, 0.f), p);
         w[jj] = wj;
     }

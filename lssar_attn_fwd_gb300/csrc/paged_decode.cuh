@@ -4,8 +4,8 @@
 //
 // Mathematics, per (sequence b, query head): z_j = the score in log2 units,
 // phi_j = the mode's normaliser, S1 = sum phi_j, m = max z_j; the weights are
-// w_j = phi_j (softmax: 2^(z_j - m)), or with re-weighting max(kappa phi_j +
-// beta, 0)^p with kappa, beta from S1, m and i; out = sum w_j v_j / sum w_j.
+// w_j = phi_j (softmax: 2^(z_j - m)), or with re-weighting max(kappa (phi_j -
+// theta), 0)^p with kappa, theta from S1, m and i; out = sum w_j v_j / sum w_j.
 //
 // What bounds it: every key and value row is read once from HBM, 4d bytes per
 // (token, key head) against 4Gd flops for a group of G query heads.  Measured:
@@ -257,7 +257,7 @@ struct Shared {
     uint64_t full[4], empty[4];
     int bad[4];                     // the stage's tile names a page that is none
     float2 red[kWarps][kHeads];
-    float4 rowc[kHeads];
+    float4 rowc[kHeads];             // RowConstants
     int abort_flag;
 };
 
@@ -302,29 +302,48 @@ __device__ __forceinline__ float2 shuffle_xor(float2 x, int o) {
     return make_float2(__shfl_xor_sync(0xffffffffu, x.x, o), __shfl_xor_sync(0xffffffffu, x.y, o));
 }
 
-// The weight of a score in the one-pass modes, relative to 2^ref: 2^(z - ref), or
-// log2(1 + 2^z) 2^-ref with lift = 2^-ref.  A row whose keys all point away from the
-// query has z down to -116, so that the logarithm near 1 (which is 0 from z = -24 on)
-// gives way to its series, log2(e) (u - u^2/2 + u^3/3), u = 2^-|z| < 2^-6: off by u^3/4 < 2^-20.
+// The weights of two scores in the one-pass modes, relative to 2^ref: 2^(z - ref), or
+// log2(1 + 2^z) 2^-ref with lift = 2^-ref.
 template <int MODE>
-__device__ __forceinline__ float weight(float z, float ref, float lift) {
-    if (MODE == kSoftmax) return ptx::ex2(z - ref);
-    const float u = ptx::ex2(-fabsf(z));
-    const float series = 1.4426950408889634f * u * fmaf(u, fmaf(u, 1.f / 3.f, -0.5f), 1.f);
-    return (fmaxf(z, 0.f) + (u < 0.015625f ? series : ptx::lg2(1.f + u))) * lift;
+__device__ __forceinline__ float2 weights(float2 z, float ref, float lift) {
+    const float2 w = phi(MODE, z, ref);
+    return MODE == kSoftmax ? w : make_float2(w.x * lift, w.y * lift);
 }
 
-// Row constants m, kappa, beta from the row's maximum and normaliser sum.  (An
-// error in kappa's last bits scales all of the row's weights alike.)
+// What makes re-weighted weights of a row's scores: x, the maximum m (softmax) or
+// 2^-min(m, 0), which brings phi, down to 2^-116, to about 1; theta, the offset; kappa,
+// 1 / (the largest difference from it); beta, 1 for a uniform row, whose kappa is 0.
+struct RowConstants {
+    float x, kappa, beta, theta;
+};
+
+// The row constants from the row's maximum and normaliser sum.  (An error in kappa's
+// last bits scales all of the row's weights alike.)  A row is uniform where the largest
+// difference is within 1e-5 of the maximum, a few times what the evaluation of phi and
+// of its sum leaves of nearly equal ones; the band is relative, as those errors are.
 template <int MODE>
-__device__ __forceinline__ float4 row_constants(int n, float2 st) {
-    const float m = st.x, theta = n <= 3 ? 0.f : st.y / (float)n, top = phi(MODE, m, m), den = top - theta;
-    float kappa = 0.f, beta = 1.f;     // all-zero re-weighted row: uniform
-    if (den > 1e-5f * top + 2e-5f) {   // the prefill kernel's near-uniform band
-        kappa = ptx::rcp(den);
-        beta = -theta * kappa;
+__device__ __forceinline__ RowConstants row_constants(int n, float2 st) {
+    constexpr bool kRaw = MODE == kSoftmaxRw;
+    const float m = st.x, lift = kRaw ? 1.f : ptx::ex2(-fminf(m, 0.f));
+    const float theta = n <= 3 ? 0.f : st.y * lift / (float)n;
+    const float top = phi(MODE, m, m) * lift, den = top - theta;
+    RowConstants rc = {kRaw ? m : lift, 0.f, 1.f, theta};
+    if (den > 1e-5f * top) {
+        rc.kappa = ptx::rcp(den);
+        rc.beta = 0.f;
     }
-    return make_float4(m, isnan(st.y) ? NAN : kappa, beta, 0.f);
+    if (isnan(st.y)) rc.kappa = NAN;
+    return rc;
+}
+
+// Two scores' re-weighted weights before the power: at most 1 but for kappa's rounding
+// (the difference is formed before it is scaled, so that its rounding is its own).
+template <int MODE>
+__device__ __forceinline__ float2 above_offset(float2 z, RowConstants rc) {
+    const float2 f = phi(MODE, z, rc.x), t = make_float2(-rc.theta, -rc.theta);
+    float2 y = MODE == kSoftmaxRw ? __fadd2_rn(f, t) : __ffma2_rn(f, make_float2(rc.x, rc.x), t);
+    y = __ffma2_rn(y, make_float2(rc.kappa, rc.kappa), make_float2(rc.beta, rc.beta));
+    return make_float2(fmaxf(y.x, 0.f), fmaxf(y.y, 0.f));
 }
 
 // x[i]^p for N values at once (independent chains).
@@ -582,7 +601,8 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
                     x = sh.red[0][threadIdx.x];
 #pragma unroll 1
                     for (int u = 1; u < kWarps; ++u) x = join<kRaw>(x, sh.red[u][threadIdx.x]);
-                    sh.rowc[threadIdx.x] = row_constants<MODE>(p.n, x);
+                    const RowConstants rc = row_constants<MODE>(p.n, x);
+                    sh.rowc[threadIdx.x] = make_float4(rc.x, rc.kappa, rc.beta, rc.theta);
                 }
                 compute_sync();
             }
@@ -599,9 +619,11 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
                     float y[8];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const float4 rc = sh.rowc[x0 + x];
-                        y[2 * x] = have > 0 ? fmaxf(fmaf(phi(MODE, zn[x].x, rc.x), rc.y, rc.z), 0.f) : 0.f;
-                        y[2 * x + 1] = have > 1 ? fmaxf(fmaf(phi(MODE, zn[x].y, rc.x), rc.y, rc.z), 0.f) : 0.f;
+                        const float4 r4 = sh.rowc[x0 + x];
+                        const RowConstants rc = {r4.x, r4.y, r4.z, r4.w};
+                        const float2 v = above_offset<MODE>(zn[x], rc);
+                        y[2 * x] = have > 0 ? v.x : 0.f;
+                        y[2 * x + 1] = have > 1 ? v.y : 0.f;
                     }
                     powers(y, g.a.p);
 #pragma unroll
@@ -694,7 +716,10 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
                     if (kRaw) st.y *= ptx::ex2(st.x - top);
                     st.x = top;
 #pragma unroll
-                    for (int u = 0; u < C::kEights; ++u) st.y += phi(MODE, z[u].x, top) + phi(MODE, z[u].y, top);
+                    for (int u = 0; u < C::kEights; ++u) {
+                        const float2 f = phi(MODE, z[u], top);
+                        st.y += f.x + f.y;
+                    }
                 } else {
                     // weights relative to 2^m (softmax), or to 2^min(m, 0) (LSSA, whose weights
                     // are about 2^z there: 16 bits would lose them); the reference follows the
@@ -716,7 +741,7 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
                     uint2 ws[C::kEights];
 #pragma unroll
                     for (int u = 0; u < C::kEights; ++u) {
-                        const float2 y = make_float2(weight<MODE>(z[u].x, st.x, lift), weight<MODE>(z[u].y, st.x, lift));
+                        const float2 y = weights<MODE>(z[u], st.x, lift);
                         st.y += y.x + y.y;
                         ws[u] = split_weights<T>(y);
                     }
@@ -882,7 +907,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join(const __grid_const
                 const long long tile = start + x / kHeads * p.nt + p.tile + i;
                 float4 w = __ldcg(reinterpret_cast<const float4 *>(&g.s.z[(tile * g.sp.zg + x % kHeads) * kTile + in]));
                 const float2 f = rowf[x];
-                if (!is_reweight(MODE)) w = make_float4(weight<MODE>(w.x, f.x, 1.f), weight<MODE>(w.y, f.x, 1.f), weight<MODE>(w.z, f.x, 1.f), weight<MODE>(w.w, f.x, 1.f));
+                if (!is_reweight(MODE)) {
+                    const float2 a = weights<MODE>(make_float2(w.x, w.y), f.x, 1.f), b = weights<MODE>(make_float2(w.z, w.w), f.x, 1.f);
+                    w = make_float4(a.x, a.y, b.x, b.y);
+                }
                 add = make_float4(fmaf(w.x, f.y, add.x), fmaf(w.y, f.y, add.y), fmaf(w.z, f.y, add.z), fmaf(w.w, f.y, add.w));
             }
             if (vec && have >= 4) {

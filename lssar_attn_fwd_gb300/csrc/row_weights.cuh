@@ -8,22 +8,36 @@
 
 namespace lssar {
 
-// log2(1 + 2^z) without overflow for any z (MUFU ex2 / lg2, as in the
-// prefill kernel)
-__device__ __forceinline__ float sp2_any(float z) {
-    return fmaxf(z, 0.f) + ptx::lg2(1.f + ptx::ex2(-fabsf(z)));
+// log2(1 + 2^z) without overflow for any z, to 2^-19 of its value also where that is
+// small: a row whose keys all point away from the query has z down to -116, and
+// lg2(1 + u), u = 2^-|z|, is off by 2^-22 and 0 from z = -24 on.  log2(1 + u) = u P(u), P of
+// degree 6 with the least largest relative error on [0, 1] (exchange algorithm): 1.3e-6,
+// 1.4e-6 with its steps in fp32.  One special function and seven FMAs, two scores at a
+// time: 2 sequences of 128K tokens, LSSAR, took 67.8 us with lg2 and its series below
+// u = 2^-6.
+__device__ __forceinline__ float2 softplus2(float2 z) {
+    const float2 u = make_float2(ptx::ex2(-fabsf(z.x)), ptx::ex2(-fabsf(z.y)));
+    const auto both = [](float c) { return make_float2(c, c); };
+    float2 r = __ffma2_rn(both(0.020401185378432274f), u, both(-0.09579754620790482f));
+    r = __ffma2_rn(r, u, both(0.2152845412492752f));
+    r = __ffma2_rn(r, u, both(-0.339089035987854f));
+    r = __ffma2_rn(r, u, both(0.4776683747768402f));
+    r = __ffma2_rn(r, u, both(-0.7211594581604004f));
+    r = __ffma2_rn(r, u, both(1.4426932334899902f));
+    return __ffma2_rn(r, u, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
 }
 
 __device__ __forceinline__ float sigmoid2(float z) {   // 1 / (1 + 2^-z)
     return ptx::rcp(1.f + ptx::ex2(-z));
 }
 
-// The normaliser value of a score (softmax modes: relative to the max m).
-__device__ __forceinline__ float phi(int mode, float z, float m) {
-    if (mode == kSoftmax || mode == kSoftmaxRw) return ptx::ex2(z - m);
-    if (mode == kSigmoidRw) return sigmoid2(z);
-    return sp2_any(z);
+// The normaliser values of two scores (softmax modes: relative to the max m).
+__device__ __forceinline__ float2 phi(int mode, float2 z, float m) {
+    if (mode == kSoftmax || mode == kSoftmaxRw) return make_float2(ptx::ex2(z.x - m), ptx::ex2(z.y - m));
+    if (mode == kSigmoidRw) return make_float2(sigmoid2(z.x), sigmoid2(z.y));
+    return softplus2(z);
 }
+__device__ __forceinline__ float phi(int mode, float z, float m) { return phi(mode, make_float2(z, z), m).x; }
 
 __device__ __forceinline__ float powi(float x, int p) {
     float r = 1.f;

@@ -42,10 +42,10 @@ def weight_bound(q, k, mode, p=3):
     2u of sum |q_c k_c| (a tensor unit may truncate) and its scale by a few u:
     |dx| <= (2d + 16) u c sum_c |q_c k_c|, c the row's factor, plus 4u|x|.
     The normaliser phi then moves by phi'(x) dx and by its own evaluation, at
-    most 2^-20 (1 + phi) for softplus (base-2 exponential and logarithm), 2^-20 phi for
-    the others, the exponential's argument rounded to 4u|x|.  Row sums add
-    (n / 16 + 64) u.  A weight max(n phi / S1 - O, 0)^p is increasing in
-    phi: it lies between its values at both ends.
+    most 2^-20 phi, the exponential's argument rounded to 4u|x|; for softplus
+    min(2^-20 (1 + phi), 2^-18 phi): a polynomial's 2^-19 and the exponential's 2^-22.
+    Row sums add (n / 16 + 64) u.  A weight max(n phi / S1 - O, 0)^p is increasing
+    in phi: it lies between its values at both ends.
     """
     u = 2.0 ** -24
     n, d = k.shape
@@ -64,7 +64,7 @@ def weight_bound(q, k, mode, p=3):
         dphi = phi * (1 - phi) * dx + 2.0 ** -20 * phi
     else:
         phi = np.logaddexp(0.0, x)
-        dphi = sigmoid(x) * dx + 2.0 ** -20 * (1 + phi)
+        dphi = sigmoid(x) * dx + np.minimum(2.0 ** -20 * (1 + phi), 2.0 ** -18 * phi)
     s1 = phi.sum(axis=1, keepdims=True)
     ds1 = dphi.sum(axis=1, keepdims=True) / s1 + (n / 16 + 64) * u
     if mode in REWEIGHTED:

@@ -296,6 +296,44 @@ def test_decode_keys_away_from_the_query(torch_mod, n, d, half):
         assert (np.abs(got - w.sum(axis=0)) <= (rel + (count / 16 + 64) * 2.0 ** -24) * w.sum(axis=0)).all()
 
 
+def keys_below(torch, c, q, b, n, top):
+    """Keys of sequence b whose scores against q (one direction) lie from about x = top down to 22 less."""
+    d, x1 = c.d, float(po.length_scale(n, c.d))
+    unit = q.double() / q.double().norm()
+    side = torch.randn(n, d, generator=c.g, dtype=torch.float64)
+    side -= (side @ unit)[:, None] * unit
+    side /= side.norm(dim=1, keepdim=True)
+    low = max(-0.97, (top - 22) / x1)
+    cos = low + (top / x1 - low) * torch.rand(n, 1, generator=c.g, dtype=torch.float64)
+    k = (d ** 0.5 * (cos * unit + (1 - cos ** 2).sqrt() * side)).to(c.dt).cuda()
+    slot = torch.arange(n)
+    c.k[c.table[b].long().cpu()[slot // c.page].cuda(), 0, (slot % c.page).cuda()] = k
+
+
+AWAY = [(300, 64, -8, False), (300, 64, -14, True), (5000, 64, -8, True), (5000, 128, -14, False), (16000, 64, -30, False),
+        (20000, 128, -36, True)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode,p", [(MODE_LSSAR, 1), (MODE_LSSAR, 3), (MODE_LSSAR, 15), (MODE_SIGMOID_RW, 1),
+                                    (MODE_SIGMOID_RW, 15), (MODE_LSSA, 1)])
+@pytest.mark.parametrize("n,d,top,half", AWAY)
+def test_decode_rows_of_keys_away_from_the_query(torch_mod, mode, p, n, d, top, half):
+    # every score is far below 0, and they differ: the weights do too
+    c = Cache(torch_mod, [n, n // 3], 1, d, 16, half=half, seed=n)
+    one = torch_mod.randn(2, 1, d, generator=c.g)
+    q = (one * torch_mod.tensor([1.0, 2.5, 0.1]).view(1, 3, 1) + 0.01).to(c.dt)
+    for b, count in enumerate((n, n // 3)):
+        keys_below(torch_mod, c, q[b, 0], b, count, top)
+    q = q.cuda()
+    for b, count in enumerate((n, n // 3)):
+        kb = po.gather(host(c.k), c.table[b].tolist(), count)[:, 0]
+        w, e = po.row_weights(host(q[b]), kb, mode, p), po.weight_bound(host(q[b]), kb, mode, p)
+        # not uniform by far, and resolved: the comparison can fail
+        assert np.abs(w - 1 / count).sum(axis=1).min() > 0.5 and e.sum(axis=1).max() < 0.1
+    check_decode(torch_mod, c, q, mode, p, c.slots(1e-3))
+
+
 @pytest.mark.gpu
 def test_offsets_past_32_bits(torch_mod):
     # pages 2^28 + 8 elements apart, the last ones past 2^31 elements: the same bits as close together
