@@ -89,6 +89,15 @@ __device__ __forceinline__ float block_reduce(float x, bool is_max, float *red) 
     return r;
 }
 
+// Calls f(j0, j1, two) for a thread's indices below n, two at a time (one: j1 = j0).
+template <typename F>
+__device__ __forceinline__ void for_pairs(int n, F &&f) {
+    for (int j = threadIdx.x; j < n; j += 2 * kDecBlock) {
+        const bool two = j + kDecBlock < n;
+        f(j, two ? j + kDecBlock : j, two);
+    }
+}
+
 // The chunk's rows as a stream of stages of KT rows: row block `it` goes to
 // the ring's stage sequence number base + it (slot (base + it) % kDecStages),
 // so a second stream can follow a first one through the same ring.  The
@@ -292,7 +301,10 @@ dec_scores(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict_
     }
     m = block_reduce(m, true, sm->red);   // its barriers also publish the scores
     float sum = 0.f;
-    for (int jj = threadIdx.x; jj < n; jj += kDecBlock) sum += phi(mode, sm->row[jj], m);
+    for_pairs(n, [&](int j0, int j1, bool two) {
+        const float2 f = phi(mode, make_float2(sm->row[j0], sm->row[j1]), m);
+        sum += f.x + (two ? f.y : 0.f);
+    });
     sum = block_reduce(sum, false, sm->red);
     if (threadIdx.x == 0) part[(size_t)bh * nch + c] = make_float2(m, sum);
 }
@@ -317,29 +329,20 @@ __device__ float2 head_stats(Stat stat, int nch, int mode) {
 
 // The chunk's weights w_j from its scores z_j and the head's statistics.
 __device__ void weights_from_stats(float2 hs, int L, int mode, int p, const float *z, float *w, int n) {
-    const float m = hs.x, s1 = hs.y;
-    float kappa = 0.f, beta = 0.f;
-    bool uniform = false;
-    if (is_reweight(mode)) {
-        const float o = (L <= 3) ? 0.f : 1.f;
-        const float theta = o * s1 / (float)L;
-        const float top = phi(mode, m, m);   // the normaliser at the row maximum
-        const float den = top - theta;
-        if (den > 1e-5f * top + 2e-5f) {   // the prefill kernel's near-uniform band
-            kappa = 1.f / den;
-            beta = -theta * kappa;
+    const float m = hs.x, lift = mode == kLssa ? ptx::ex2(-fminf(m, 0.f)) : 1.f;
+    const RowConstants rc = row_constants(mode, L, hs);
+    for_pairs(n, [&](int j0, int j1, bool two) {
+        const float2 zz = make_float2(z[j0], z[j1]);
+        float2 y;
+        if (is_reweight(mode)) {
+            y = powi(above_offset(mode, zz, rc), p);
         } else {
-            uniform = true;   // all-zero re-weighted row: uniform prefix mean
+            y = phi(mode, zz, m);
+            y = make_float2(y.x * lift, y.y * lift);   // LSSA: down to 2^-116 without the lift
         }
-    }
-    for (int jj = threadIdx.x; jj < n; jj += kDecBlock) {
-        const float zj = z[jj];
-        float wj;
-        if (mode == kSoftmax) wj = exp2f(zj - m);
-        else if (mode == kLssa) wj = phi(mode, zj, m);
-        else wj = uniform ? 1.f : powi(fmaxf(phi(mode, zj, m) * kappa + beta, 0.f), p);
-        w[jj] = wj;
-    }
+        w[j0] = y.x;
+        if (two) w[j1] = y.y;
+    });
 }
 
 __device__ void chunk_weights(const float2 *__restrict__ part_head, int nch, int L, int mode, int p,
@@ -461,7 +464,10 @@ dec_fused(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict__
     }
     m = block_reduce(m, true, sm->red);   // its barriers also publish the scores
     float sum = 0.f;
-    for (int jj = threadIdx.x; jj < n; jj += kDecBlock) sum += phi(mode, sm->row[jj], m);
+    for_pairs(n, [&](int j0, int j1, bool two) {
+        const float2 f = phi(mode, make_float2(sm->row[j0], sm->row[j1]), m);
+        sum += f.x + (two ? f.y : 0.f);
+    });
     sum = block_reduce(sum, false, sm->red);
     // grid barrier: every chunk's statistics are in `part`
     if (threadIdx.x == 0) {
@@ -587,7 +593,10 @@ dec_cluster(const __nv_bfloat16 *__restrict__ q, const __nv_bfloat16 *__restrict
     }
     m = block_reduce(m, true, sm->red);   // its barriers also publish the scores
     float sum = 0.f;
-    for (int jj = threadIdx.x; jj < n; jj += kDecBlock) sum += phi(mode, sm->row[jj], m);
+    for_pairs(n, [&](int j0, int j1, bool two) {
+        const float2 f = phi(mode, make_float2(sm->row[j0], sm->row[j1]), m);
+        sum += f.x + (two ? f.y : 0.f);
+    });
     sum = block_reduce(sum, false, sm->red);
     if (threadIdx.x == 0) stat = make_float2(m, sum);
     ptx::cluster_sync();   // every chunk's statistics are in its CTA's shared memory

@@ -310,42 +310,6 @@ __device__ __forceinline__ float2 weights(float2 z, float ref, float lift) {
     return MODE == kSoftmax ? w : make_float2(w.x * lift, w.y * lift);
 }
 
-// What makes re-weighted weights of a row's scores: x, the maximum m (softmax) or
-// 2^-min(m, 0), which brings phi, down to 2^-116, to about 1; theta, the offset; kappa,
-// 1 / (the largest difference from it); beta, 1 for a uniform row, whose kappa is 0.
-struct RowConstants {
-    float x, kappa, beta, theta;
-};
-
-// The row constants from the row's maximum and normaliser sum.  (An error in kappa's
-// last bits scales all of the row's weights alike.)  A row is uniform where the largest
-// difference is within 1e-5 of the maximum, a few times what the evaluation of phi and
-// of its sum leaves of nearly equal ones; the band is relative, as those errors are.
-template <int MODE>
-__device__ __forceinline__ RowConstants row_constants(int n, float2 st) {
-    constexpr bool kRaw = MODE == kSoftmaxRw;
-    const float m = st.x, lift = kRaw ? 1.f : ptx::ex2(-fminf(m, 0.f));
-    const float theta = n <= 3 ? 0.f : st.y * lift / (float)n;
-    const float top = phi(MODE, m, m) * lift, den = top - theta;
-    RowConstants rc = {kRaw ? m : lift, 0.f, 1.f, theta};
-    if (den > 1e-5f * top) {
-        rc.kappa = ptx::rcp(den);
-        rc.beta = 0.f;
-    }
-    if (isnan(st.y)) rc.kappa = NAN;
-    return rc;
-}
-
-// Two scores' re-weighted weights before the power: at most 1 but for kappa's rounding
-// (the difference is formed before it is scaled, so that its rounding is its own).
-template <int MODE>
-__device__ __forceinline__ float2 above_offset(float2 z, RowConstants rc) {
-    const float2 f = phi(MODE, z, rc.x), t = make_float2(-rc.theta, -rc.theta);
-    float2 y = MODE == kSoftmaxRw ? __fadd2_rn(f, t) : __ffma2_rn(f, make_float2(rc.x, rc.x), t);
-    y = __ffma2_rn(y, make_float2(rc.kappa, rc.kappa), make_float2(rc.beta, rc.beta));
-    return make_float2(fmaxf(y.x, 0.f), fmaxf(y.y, 0.f));
-}
-
 // x[i]^p for N values at once (independent chains).
 template <int N>
 __device__ __forceinline__ void powers(float (&x)[N], int p) {
@@ -601,7 +565,7 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
                     x = sh.red[0][threadIdx.x];
 #pragma unroll 1
                     for (int u = 1; u < kWarps; ++u) x = join<kRaw>(x, sh.red[u][threadIdx.x]);
-                    const RowConstants rc = row_constants<MODE>(p.n, x);
+                    const RowConstants rc = row_constants(MODE, p.n, x);
                     sh.rowc[threadIdx.x] = make_float4(rc.x, rc.kappa, rc.beta, rc.theta);
                 }
                 compute_sync();
@@ -621,7 +585,7 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
                     for (int x = 0; x < 4; ++x) {
                         const float4 r4 = sh.rowc[x0 + x];
                         const RowConstants rc = {r4.x, r4.y, r4.z, r4.w};
-                        const float2 v = above_offset<MODE>(zn[x], rc);
+                        const float2 v = above_offset(MODE, zn[x], rc);
                         y[2 * x] = have > 0 ? v.x : 0.f;
                         y[2 * x + 1] = have > 1 ? v.y : 0.f;
                     }

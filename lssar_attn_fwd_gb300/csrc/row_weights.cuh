@@ -1,6 +1,6 @@
 // The row functions of the decode steps (dense cache and paged cache): the
-// normaliser value of a score and the integer power of the re-weighting, in
-// log2 units (z = log2(e) x).
+// normaliser value of a score, the constants and the integer power of the
+// re-weighting, in log2 units (z = log2(e) x).
 #pragma once
 
 #include "lssar_internal.cuh"
@@ -39,11 +39,45 @@ __device__ __forceinline__ float2 phi(int mode, float2 z, float m) {
 }
 __device__ __forceinline__ float phi(int mode, float z, float m) { return phi(mode, make_float2(z, z), m).x; }
 
-__device__ __forceinline__ float powi(float x, int p) {
-    float r = 1.f;
+// What makes re-weighted weights of a row's scores: x, the maximum m (softmax) or
+// 2^-min(m, 0), which brings phi, down to 2^-116, to about 1; theta, the offset; kappa,
+// 1 / (the largest difference from it); beta, 1 for a uniform row, whose kappa is 0.
+struct RowConstants {
+    float x, kappa, beta, theta;
+};
+
+// The row constants from the row's maximum and normaliser sum.  (An error in kappa's
+// last bits scales all of the row's weights alike.)  A row is uniform where the largest
+// difference is within 1e-5 of the maximum, a few times what the evaluation of phi and
+// of its sum leaves of nearly equal ones; the band is relative, as those errors are.
+__device__ __forceinline__ RowConstants row_constants(int mode, int n, float2 st) {
+    const bool raw = mode == kSoftmaxRw;
+    const float m = st.x, lift = raw ? 1.f : ptx::ex2(-fminf(m, 0.f));
+    const float theta = n <= 3 ? 0.f : st.y * lift / (float)n;
+    const float top = phi(mode, m, m) * lift, den = top - theta;
+    RowConstants rc = {raw ? m : lift, 0.f, 1.f, theta};
+    if (den > 1e-5f * top) {
+        rc.kappa = ptx::rcp(den);
+        rc.beta = 0.f;
+    }
+    if (isnan(st.y)) rc.kappa = NAN;
+    return rc;
+}
+
+// Two scores' re-weighted weights before the power: at most 1 but for kappa's rounding
+// (the difference is formed before it is scaled, so that its rounding is its own).
+__device__ __forceinline__ float2 above_offset(int mode, float2 z, RowConstants rc) {
+    const float2 f = phi(mode, z, rc.x), t = make_float2(-rc.theta, -rc.theta);
+    float2 y = mode == kSoftmaxRw ? __fadd2_rn(f, t) : __ffma2_rn(f, make_float2(rc.x, rc.x), t);
+    y = __ffma2_rn(y, make_float2(rc.kappa, rc.kappa), make_float2(rc.beta, rc.beta));
+    return make_float2(fmaxf(y.x, 0.f), fmaxf(y.y, 0.f));
+}
+
+__device__ __forceinline__ float2 powi(float2 x, int p) {
+    float2 r = make_float2(1.f, 1.f);
     while (p) {
-        if (p & 1) r *= x;
-        x *= x;
+        if (p & 1) r = __fmul2_rn(r, x);
+        x = __fmul2_rn(x, x);
         p >>= 1;
     }
     return r;

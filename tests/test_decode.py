@@ -126,6 +126,36 @@ def test_decode_beyond_cluster_reach(torch_mod):
     assert np.abs(got[0, 0] - ref).max() <= 5e-2
 
 
+@pytest.mark.parametrize("mode,p", [(MODE_LSSA, 1), (MODE_LSSAR, 1), (MODE_LSSAR, 15), (MODE_SIGMOID_RW, 3)])
+@pytest.mark.parametrize("L,d,top", [(300, 64, -8), (5000, 128, -14), (16000, 64, -30)])
+def test_decode_keys_away_from_the_query(torch_mod, mode, p, L, d, top, decode_path):
+    # every score far below 0 and spread over 20: the weights still follow them
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    from oracle import paged_oracle as po
+    g = torch.Generator().manual_seed(L)
+    B, H, x1 = 1, 2, float(po.length_scale(L, d))
+    q, k, v = torch.randn(B, H, d, generator=g), torch.empty(B, H, L, d), torch.randn(B, H, L, d, generator=g)
+    for h in range(H):
+        unit = q[0, h].double() / q[0, h].double().norm()
+        side = torch.randn(L, d, generator=g, dtype=torch.float64)
+        side -= (side @ unit)[:, None] * unit
+        side /= side.norm(dim=1, keepdim=True)
+        low = max(-0.97, (top - 22) / x1)
+        cos = low + (top / x1 - low) * torch.rand(L, 1, generator=g, dtype=torch.float64)
+        k[0, h] = d ** 0.5 * (cos * unit + (1 - cos ** 2).sqrt() * side)
+    q, k, v = (t.bfloat16().cuda() for t in (q, k, v))
+    out = api.lssar_attn_decode(q, k, v, p=p, mode=mode)
+    assert api.device_error_word() == 0
+    for h in range(H):
+        qs, ks, vs, got = (t.double().cpu().numpy() for t in (q[0, h:h + 1], k[0, h], v[0, h], out[0, h:h + 1]))
+        w, e = po.row_weights(qs, ks, mode, p), po.weight_bound(qs, ks, mode, p)
+        assert np.abs(w - 1 / L).sum() > 0.5 and e.sum() < 0.1
+        # the value sum: each product and partial sum off by 2^-24 at most
+        ref, tol = w @ vs, (e + (L + 64) * 2.0 ** -24 * w) @ np.abs(vs)
+        assert (np.abs(got - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol)).all()
+
+
 def expected_cluster_split(BH, L, sms):
     """The cluster path's split of each head's cache: about one wave of four
     CTAs per SM (at least one chunk, at most 16), chunks a multiple of 64 keys
