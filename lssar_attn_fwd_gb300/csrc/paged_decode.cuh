@@ -37,7 +37,7 @@
 //   scores: rows 8-15 the queries, rows 0-7 the tile's own 8 keys, so that one
 //           product gives q.k and, on the diagonal, |k|^2;
 //   values: rows 8-15 the weights rounded to 16 bits, rows 0-7 what the rounding
-//           left over, so that weights keep 16 bits (bf16) or more.
+//           left over, so that weights keep 16 bits (fp16: and 2^-37 of the largest).
 // K and V tiles come by TMA (128-byte swizzle), a piece of a page at a time.
 #pragma once
 
@@ -208,10 +208,17 @@ __device__ __forceinline__ void next_row(const PagedCache &c, int blocks, Place 
     } while (p.nt == 0);
 }
 
+// The element types as operands.  A weight is two of them, rounded and the remainder.  fp16
+// has no step below 2^-24: weights relative to the row's largest one would lose what is
+// below 2^-25 of it, which many keys together make count, so that the largest ones are
+// put between 2^13 and 2^15 (at most 1.45 2^15 = 47514 in LSSA), where the least step is
+// 2^-37 of them and 2^24 keys lose 2^-14.  bf16 has fp32's range.
 template <typename T>
 struct Elem;
 template <>
 struct Elem<__nv_bfloat16> {
+    static constexpr float kRoom = 0.f, kLag = 8.f;   // one pass: log2 of the largest weight is in kRoom + [0, kLag]
+    static constexpr float kTop = 1.f;                // re-weighting: the largest weight
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return ptx::pack_bf16x2(lo, hi); }
     static __device__ __forceinline__ float2 unpack(uint32_t x) {
         return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
@@ -224,6 +231,8 @@ struct Elem<__nv_bfloat16> {
 };
 template <>
 struct Elem<__half> {
+    static constexpr float kRoom = 13.f, kLag = 2.f;
+    static constexpr float kTop = 32768.f;
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return ptx::pack_f16x2(lo, hi); }
     static __device__ __forceinline__ float2 unpack(uint32_t x) {
         return __half22float2(*reinterpret_cast<const __half2 *>(&x));
@@ -596,7 +605,7 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
                             const float2 v = make_float2(y[2 * x], y[2 * x + 1]);
                             wsum[0][x] += x0 ? 0.f : v.x + v.y;
                             wsum[1][x] += x0 ? v.x + v.y : 0.f;
-                            wbuf[(x0 + x) * 32 + (lane ^ (x << 2))] = split_weights<T>(v);
+                            wbuf[(x0 + x) * 32 + (lane ^ (x << 2))] = split_weights<T>(make_float2(v.x * Elem<T>::kTop, v.y * Elem<T>::kTop));
                             if (g.a.scores && have > 0) *reinterpret_cast<float2 *>(zl + (i0 * g.sp.zg + x0 + x) * C::kTile) = v;
                         }
                     if (x0 + 4 < heads) fetch(i0, x0 + 4);
@@ -685,14 +694,23 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
                         st.y += f.x + f.y;
                     }
                 } else {
-                    // weights relative to 2^m (softmax), or to 2^min(m, 0) (LSSA, whose weights
-                    // are about 2^z there: 16 bits would lose them); the reference follows the
-                    // maximum only when it has grown by more than 8, so that softmax's weights
-                    // stay below 2^8, LSSA's (at most 118 2^8) in range, and rescaling is rare
-                    if (MODE != kSoftmax) top = fminf(top, 0.f);
-                    if (__any_sync(0xffffffffu, top > st.x + 8.f)) {
+                    // weights relative to 2^reference: m (softmax), or min(m, 0) (LSSA, whose weights
+                    // are about 2^z there: 16 bits would lose them; in fp16 log2(1 + m) above 0, so
+                    // that the largest weight is about 1 here too), less kRoom.  The reference
+                    // follows the maximum only when that has grown by more than kLag, so that
+                    // rescaling is rare and weights stay below 2^(kRoom + kLag) (LSSA: 1.45 times that;
+                    // in bf16 118 times).
+                    constexpr float kRoom = Elem<T>::kRoom, kMost = kRoom + Elem<T>::kLag;
+                    if (MODE != kSoftmax) top = kRoom == 0.f ? fminf(top, 0.f) : top < 0.f ? top : ptx::lg2(1.f + top);
+                    if (__any_sync(0xffffffffu, top - st.x > kMost)) {
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        if (kRoom != 0.f) {
+                            float ref = top - kRoom;
+                            if (top - ref > kMost) ref = top;            // steps of a top past 2^24
+                            if (MODE != kSoftmax) ref = fmaxf(ref, -126.f);   // 2^-ref is finite
+                            top = ref;
+                        }
                         top = fmaxf(top, st.x);
                         const float f = ptx::ex2(st.x - top);
                         st = make_float2(top, st.y * f);
@@ -727,7 +745,7 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
         if constexpr (PHASE != kScores) {
             // a row with this segment alone is written out, the others go to scratch
             const bool whole = sg.count == 1;
-            float f = kRelative ? ptx::ex2(st.x - all.x) : 1.f;
+            float f = kRelative ? ptx::ex2(st.x - all.x) : 1.f / Elem<T>::kTop;
             if (whole) f *= ptx::rcp(all.y);
 #pragma unroll
             for (int k = 0; k < D / 8; ++k)

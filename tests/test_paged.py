@@ -335,6 +335,85 @@ def test_decode_rows_of_keys_away_from_the_query(torch_mod, mode, p, n, d, top, 
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("mode,p,log2_weight", [(MODE_SOFTMAX, 1, -25.5), (MODE_SOFTMAX, 1, -24.6), (MODE_SOFTMAX, 1, -20.5),
+                                                (MODE_SOFTMAX_RW, 3, -8.0), (MODE_LSSA, 1, -29.0)])
+@pytest.mark.parametrize("n,d", [(131071, 64), (9000, 128)])
+def test_decode_fp16_of_many_small_weights(torch_mod, mode, p, log2_weight, n, d):
+    # one key of a large weight whose value is 0, and many of small ones that make the output
+    torch = torch_mod
+    c = Cache(torch, [n], 1, d, 128, half=True, seed=1)
+    x = torch.zeros(c.cap, d)
+    big = n // 3
+    q = torch.zeros(1, 1, d)
+    if mode == MODE_LSSA:
+        # cosines: 0.3 for the one, the others' x = log2_weight ln 2
+        q[0, 0, 0] = 4.0
+        cos = torch.full((c.cap,), log2_weight * np.log(2) / float(po.length_scale(n, d)))
+        cos[big] = 0.3
+        x[:, 0], x[:, 1] = 16 * cos, 16 * (1 - cos ** 2).sqrt()
+    else:
+        q[0, 0, 0] = 16.0
+        x[big, 0] = -log2_weight * np.log(2) * d ** 0.5 / 16
+        if mode == MODE_SOFTMAX_RW:
+            x[1::2, 0] = -40.0                     # half of the keys: no weight at all
+            x[big, 0] = -log2_weight * np.log(2) * d ** 0.5 / 16
+    pages = c.table[0].long()
+    c.k[pages, 0] = x.view(-1, 128, d).to(c.dt).cuda()
+    c.v[pages, 0] = (1 + 0.5 * torch.randn(c.cap, d, generator=c.g)).view(-1, 128, d).to(c.dt).cuda()
+    c.v[pages[big // 128], 0, big % 128] = 0
+    out, _ = check_decode(torch, c, q.to(c.dt).cuda(), mode, p, c.slots(1e-3))
+    assert (out != 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode,p,log2_weight", [(MODE_SOFTMAX, 1, -25.5), (MODE_SOFTMAX, 1, -24.6), (MODE_SOFTMAX_RW, 3, -8.0)])
+def test_decode_fp16_of_many_small_weights_in_one_segment(torch_mod, mode, p, log2_weight):
+    # 600 sequences share their pages, so that most rows are summed by one block
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    n, B, d = 9000, 600, 64
+    c = Cache(torch, [n], 1, d, 128, half=True, seed=1)
+    x = torch.zeros(c.cap, d)
+    if mode == MODE_SOFTMAX_RW:
+        x[1::2, 0] = -40.0
+    x[n // 3, 0] = -log2_weight * np.log(2) * d ** 0.5 / 16
+    pages = c.table[0].long()
+    c.k[pages, 0] = x.view(-1, 128, d).to(c.dt).cuda()
+    c.v[pages, 0] = (1 + 0.5 * torch.randn(c.cap, d, generator=c.g)).view(-1, 128, d).to(c.dt).cuda()
+    c.v[pages[n // 3 // 128], 0, n // 3 % 128] = 0
+    q = torch.zeros(1, 1, d)
+    q[0, 0, 0] = 16.0
+    q = q.to(c.dt).cuda()
+    out = api.lssar_paged_decode(q.repeat(B, 1, 1), c.k, c.v, c.table.repeat(B, 1), c.lens.repeat(B), p=p, mode=mode)
+    assert api.device_error_word() == 0
+    ref, _, err, _ = po.paged_decode(host(q), host(c.k), host(c.v), host(c.table), [n], mode, p)
+    # as check_decode: the oracle's bound, half a step of fp16, half its least step
+    bad = np.abs(host(out) - ref) - (err + 2.0 ** -11 * (np.abs(ref) + err) + 2.0 ** -25)
+    assert bad.max() <= 0, (bad.max(), err.max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode,p", [(MODE_SOFTMAX, 1), (MODE_SOFTMAX_RW, 3)])
+@pytest.mark.parametrize("size", [300, 2000, 4000, 5600, 30000])
+@pytest.mark.parametrize("grows", [False, True])
+def test_decode_fp16_of_huge_scores(torch_mod, mode, p, size, grows):
+    # scores from 2^20 to 2^33, whose steps pass the weights' range: the best key takes all
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    c = Cache(torch, [390], 1, 64, 16, half=True, seed=size)
+    a = 1 - torch.arange(390) / 400
+    slot = torch.arange(390)
+    pages = c.table[0].long().cpu()[slot // 16].cuda()
+    c.k[pages, 0, (slot % 16).cuda()] = (size * (a.flip(0) if grows else a)).view(-1, 1).repeat(1, 64).to(c.dt).cuda()
+    q = torch.full((1, 2, 64), float(size)).to(c.dt).cuda()
+    out = api.lssar_paged_decode(q, *c.args(), p=p, mode=mode)
+    assert api.device_error_word() == 0
+    best = 389 if grows else 0
+    v = c.v[c.table[0, best // 16].long(), 0, best % 16].float()
+    assert ((out[0].float() - v).abs() <= (2.0 ** -15 + 2.0 ** -11) * v.abs() + 2.0 ** -25).all()
+
+
+@pytest.mark.gpu
 def test_offsets_past_32_bits(torch_mod):
     # pages 2^28 + 8 elements apart, the last ones past 2^31 elements: the same bits as close together
     torch = torch_mod
