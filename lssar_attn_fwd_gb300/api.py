@@ -154,6 +154,29 @@ def _check(status):
         raise LssarError(status, status_string(status))
 
 
+def _stream_of(stream, device):
+    """The torch stream of a ``stream`` argument (a torch stream or a raw handle)."""
+    import torch
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def _make(stream, device, make):
+    """A result tensor that a call on ``stream`` (None: the current one) makes for
+    itself.  Its memory comes in the order of the stream that writes it: a block
+    freed on the current stream may still be read or written by work queued
+    there.  The current stream, which may use the result, is noted for its release."""
+    import torch
+    if stream is None:
+        return make()
+    s = _stream_of(stream, device)
+    with torch.cuda.stream(s):
+        t = make()
+    current = torch.cuda.current_stream(device)
+    if current != s:
+        t.record_stream(current)
+    return t
+
+
 def _forward(name, q, k, v, p, mode, out, stream):
     import torch
 
@@ -168,7 +191,7 @@ def _forward(name, q, k, v, p, mode, out, stream):
         raise ValueError("q, k, v must be on one device")
     B, H, L, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _make(stream, q.device, lambda: torch.empty_like(q))
     elif (out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous()
           or out.device != q.device):
         raise ValueError("out must be a contiguous bfloat16 tensor shaped like q on q's device")
@@ -228,10 +251,10 @@ def lssar_attn_fwd_train(q, k, v, p=3, mode=MODE_LSSAR, out=None, stats=None, st
         raise ValueError("q must be a CUDA tensor")
     _check_like(q, q, k, v)
     B, H, L, d = q.shape
-    out = torch.empty_like(q) if out is None else out
+    out = _make(stream, q.device, lambda: torch.empty_like(q)) if out is None else out
     _check_like(q, out)
     if stats is None:
-        stats = torch.empty((B, H, L, 4), dtype=torch.float32, device=q.device)
+        stats = _make(stream, q.device, lambda: torch.empty((B, H, L, 4), dtype=torch.float32, device=q.device))
     elif stats.shape != (B, H, L, 4) or stats.dtype != torch.float32 or not stats.is_contiguous():
         raise ValueError("stats must be a contiguous float32 [B, H, L, 4] tensor")
     with torch.cuda.device(q.device):
@@ -249,7 +272,7 @@ def _backward(name, q, k, v, dout, stats, p, mode, stream):
     B, H, L, d = q.shape
     if stats.shape != (B, H, L, 4) or stats.dtype != torch.float32 or not stats.is_contiguous():
         raise ValueError("stats must be the float32 [B, H, L, 4] tensor of lssar_attn_fwd_train")
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+    dq, dk, dv = (_make(stream, q.device, lambda: torch.empty_like(q)) for _ in range(3))
     with torch.cuda.device(q.device):
         s = torch.cuda.current_stream(q.device) if stream is None else stream
         ptrs = tuple(t.data_ptr() for t in (q, k, v, dout, stats, dq, dk, dv))
@@ -288,7 +311,7 @@ def lssar_attn_fwd_heads_p(q, k, v, p_per_head, mode=MODE_LSSAR, out=None, strea
     if len(p_per_head) != H:
         raise ValueError("p_per_head must hold one exponent per head")
     if out is None:
-        out = torch.empty_like(q)
+        out = _make(stream, q.device, lambda: torch.empty_like(q))
     with torch.cuda.device(q.device):
         s = torch.cuda.current_stream(q.device) if stream is None else stream
         _check(call_heads_p(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -325,8 +348,8 @@ def lssar_attn_fwd_train_heads_p(q, k, v, p_per_head, mode=MODE_LSSAR, stream=No
     B, H, L, d = q.shape
     if len(p_per_head) != H:
         raise ValueError("p_per_head must hold one exponent per head")
-    out = torch.empty_like(q)
-    stats = torch.empty((B, H, L, 4), dtype=torch.float32, device=q.device)
+    out = _make(stream, q.device, lambda: torch.empty_like(q))
+    stats = _make(stream, q.device, lambda: torch.empty((B, H, L, 4), dtype=torch.float32, device=q.device))
     with torch.cuda.device(q.device):
         s = torch.cuda.current_stream(q.device) if stream is None else stream
         _check(call_train_heads_p(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), stats.data_ptr(),
@@ -346,7 +369,7 @@ def lssar_attn_bwd_heads_p(q, k, v, dout, stats, p_per_head, mode=MODE_LSSAR, st
         raise ValueError("p_per_head must hold one exponent per head")
     if stats.shape != (B, H, L, 4) or stats.dtype != torch.float32 or not stats.is_contiguous():
         raise ValueError("stats must be the float32 [B, H, L, 4] tensor of lssar_attn_fwd_train_heads_p")
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+    dq, dk, dv = (_make(stream, q.device, lambda: torch.empty_like(q)) for _ in range(3))
     with torch.cuda.device(q.device):
         s = torch.cuda.current_stream(q.device) if stream is None else stream
         ptrs = tuple(t.data_ptr() for t in (q, k, v, dout, stats, dq, dk, dv))
@@ -368,7 +391,7 @@ def lssar_attn_decode(q, k_cache, v_cache, p=3, mode=MODE_LSSAR, out=None, strea
     if v_cache.shape != k_cache.shape or tuple(q.shape) != (B, H, d):
         raise ValueError("shapes must be q [B, H, d] and caches [B, H, L, d]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _make(stream, q.device, lambda: torch.empty_like(q))
     with torch.cuda.device(q.device):
         s = torch.cuda.current_stream(q.device) if stream is None else stream
         _check(call_raw("lssar_attn_decode", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
@@ -445,19 +468,12 @@ def _int32(name, value):
     return value
 
 
-def _paged_call(name, dev, stream, made, *args):
+def _paged_call(name, dev, stream, *args):
     """Calls an entry point on the cache's device and the given (default: the
-    current) stream; tensors that this call made are kept from reuse until
-    another stream than the current one is done with them."""
+    current) stream."""
     import torch
     fn = getattr(_LIB or load_library(), name)
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=dev)
-        for t in made:
-            t.record_stream(s)
-        handle = s.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_of(stream, dev).cuda_stream
     if torch._C._cuda_getDevice() == dev:
         status = fn(*args, handle)
     else:
@@ -496,12 +512,10 @@ def lssar_paged_append(k_new, v_new, k_pages, v_pages, table, lens, counts=None,
     kst, vst = k_new.stride(), v_new.stride()
     if n and (kst[3] != 1 or vst[3] != 1):
         raise ValueError("the last dimension of k_new and v_new must be contiguous")
-    made = ()
     if lens_out is None:
-        lens_out = torch.empty_like(lens)
-        made = (lens_out,)
+        lens_out = _make(stream, dev, lambda: torch.empty_like(lens))
     slots = (B, Hkv, cap)
-    _paged_call("lssar_paged_append", dev, stream, made, desc, k_new.data_ptr(), _pack_3(*kst[:3]), v_new.data_ptr(),
+    _paged_call("lssar_paged_append", dev, stream, desc, k_new.data_ptr(), _pack_3(*kst[:3]), v_new.data_ptr(),
                 _pack_3(*vst[:3]), n, _per_sequence("counts", counts, B, dev),
                 _per_sequence("first_positions", first_positions, B, dev),
                 _slots("scores", scores, slots, torch.float32, dev), _slots("positions", positions, slots, torch.int32, dev),
@@ -536,15 +550,13 @@ def lssar_paged_decode(q, k_pages, v_pages, table, lens, p=3, mode=MODE_LSSAR, s
         raise ValueError("scores_out needs scores")
     if scores_out is None:
         scores_out = scores
-    made = ()
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
-        made = (out,)
+        out = _make(stream, dev, lambda: torch.empty(shape, dtype=dtype, device=q.device))
     elif (out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or not out.is_cuda
           or out.get_device() != dev):
         raise ValueError("out must be a contiguous [B, H, d] tensor of q's type on the cache's device")
     slots = (B, Hkv, cap)
-    _paged_call("lssar_paged_decode", dev, stream, made, desc, q.data_ptr(), _pack_2(*qst[:2]), out.data_ptr(), shape[1],
+    _paged_call("lssar_paged_decode", dev, stream, desc, q.data_ptr(), _pack_2(*qst[:2]), out.data_ptr(), shape[1],
                 _int32("p", p), _int32("mode", mode), _slots("scores", scores, slots, torch.float32, dev),
                 _slots("scores_out", scores_out, slots, torch.float32, dev))
     return out
@@ -569,12 +581,10 @@ def lssar_paged_evict(k_pages, v_pages, table, lens, scores, positions, keep, re
         raise ValueError("scores_out and positions_out go together")
     if scores_out is None:
         scores_out, positions_out = scores, positions
-    made = ()
     if lens_out is None:
-        lens_out = torch.empty_like(lens)
-        made = (lens_out,)
+        lens_out = _make(stream, dev, lambda: torch.empty_like(lens))
     slots = (B, Hkv, cap)
-    _paged_call("lssar_paged_evict", dev, stream, made, desc, _slots("scores", scores, slots, torch.float32, dev),
+    _paged_call("lssar_paged_evict", dev, stream, desc, _slots("scores", scores, slots, torch.float32, dev),
                 _slots("positions", positions, slots, torch.int32, dev), _int32("keep", keep), _int32("recent", recent),
                 _int32("sinks", sinks), _slots("scores_out", scores_out, slots, torch.float32, dev),
                 _slots("positions_out", positions_out, slots, torch.int32, dev),

@@ -804,3 +804,46 @@ def test_calls_on_two_streams_at_once(torch_mod):
     assert api.device_error_word() == 0
     for i in (0, 1):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+@pytest.mark.gpu
+def test_results_made_on_another_stream_take_no_block_in_use(torch_mod):
+    # Blocks of the results' sizes, just freed on the current stream, are still written by
+    # work that is queued there: a call on another stream makes its results elsewhere.
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    c = Cache(torch, [40, 3], 2, 64, 16, seed=3)
+    lens = torch.tensor([20, 2], dtype=torch.int32).cuda()
+    q, new, scores = c.q(4), c.q(2), c.slots()
+    pos = torch.arange(c.cap, dtype=torch.int32).repeat(2, 2, 1).cuda()
+    x = torch.randn(4, 2, 3, 100, 64, generator=c.g).bfloat16().cuda()
+    ps = [1, 3, 15]
+    stats = api.lssar_attn_fwd_train(*x[:3])[1]
+    stats_p = api.lssar_attn_fwd_train_heads_p(*x[:3], ps)[1]
+    kw = dict(scores_out=scores.clone(), positions_out=pos.clone())
+    calls = [lambda s: [api.lssar_paged_decode(q, c.k, c.v, c.table, lens, stream=s)],
+             lambda s: [api.lssar_paged_append(new, new, c.k, c.v, c.table, lens, stream=s)],
+             lambda s: [api.lssar_paged_evict(c.k, c.v, c.table, lens, scores, pos, 24, stream=s, **kw)[0]],
+             lambda s: [api.lssar_attn_fwd(*x[:3], stream=s)],
+             lambda s: [api.lssar_attn_fwd_heads_p(*x[:3], ps, stream=s)],
+             lambda s: [api.lssar_attn_decode(x[0, :, :, 0].contiguous(), x[1], x[2], stream=s)],
+             lambda s: list(api.lssar_attn_fwd_train(*x[:3], stream=s)),
+             lambda s: list(api.lssar_attn_fwd_train_heads_p(*x[:3], ps, stream=s)),
+             lambda s: list(api.lssar_attn_bwd(*x, stats, stream=s)),
+             lambda s: list(api.lssar_attn_bwd_heads_p(*x, stats_p, ps, stream=s))]
+    side = torch.cuda.Stream()
+    for i, call in enumerate(calls):
+        want = call(None)
+        torch.cuda.synchronize()
+        for stream in (side, side.cuda_stream)[:2 if i < 4 else 1]:
+            blocks = [torch.empty_like(w) for w in want for _ in range(4)]
+            torch.cuda._sleep(100_000_000)     # about 50 ms
+            for b in blocks:
+                b.fill_(77)
+            del blocks, b
+            got = call(stream)
+            torch.cuda.synchronize()
+            for a, w in zip(got, want):
+                view = torch.int16 if w.element_size() == 2 else torch.int32
+                assert torch.equal(a.view(view), w.view(view)), i
+    assert api.device_error_word() == 0
