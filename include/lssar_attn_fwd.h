@@ -269,7 +269,7 @@ typedef struct {
  * number are dropped (code 52).
  * Errors: LSSAR_ERR_NULL, SHAPE, HEADDIM, PAGE, DTYPE, ALIGN (a pointer or a
  * stride), ALIAS (an output overlaps anything else; k_new, v_new, counts or
- * first_positions overlap the pages, table or lens), CUDA.
+ * first_positions overlap the pages), CUDA.
  */
 int lssar_paged_append(const lssar_paged_cache_t *cache, const void *k_new, const long long *k_strides,
                        const void *v_new, const long long *v_strides, int n, const int *counts,

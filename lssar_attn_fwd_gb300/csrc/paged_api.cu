@@ -55,10 +55,15 @@ int check_cache(const lssar_paged_cache_t *c, lssar::PagedCache *out) {
     return LSSAR_OK;
 }
 
+// Bytes from the first page of K or V to the end of the last.
+size_t page_bytes(const lssar::PagedCache &c) {
+    return ((size_t)(c.n_pages - 1) * c.page_stride + (size_t)c.Hkv * c.page_size * c.d) * 2;
+}
+
 // The memory of K, V, table and lens, with `outs` (written) tested against
 // them, against one another and against `ins` (read).
 bool any_alias(const lssar::PagedCache &c, std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
-    const size_t pages = ((size_t)(c.n_pages - 1) * c.page_stride + (size_t)c.Hkv * c.page_size * c.d) * 2;
+    const size_t pages = page_bytes(c);
     const Range own[4] = {{c.k, pages}, {c.v, pages}, {c.table, (size_t)c.B * c.max_pages * 4}, {c.lens, (size_t)c.B * 4}};
     for (const Range *o = outs.begin(); o != outs.end(); ++o) {
         for (const Range &x : own)
@@ -111,9 +116,9 @@ int lssar_paged_append(const lssar_paged_cache_t *cache, const void *k_new, cons
     const Range sc = {scores, slots}, po = {positions, slots}, lo = {lens_out, seqs};
     const Range cn = {counts, seqs}, fi = {first_positions, seqs};
     if (any_alias(a.c, {sc, po, lo}, {kr, vr, cn, fi})) return LSSAR_ERR_ALIAS;
-    // the pages are written too
-    if (any_alias(a.c, {kr}, {}) || any_alias(a.c, {vr}, {}) || any_alias(a.c, {cn}, {}) || any_alias(a.c, {fi}, {}))
-        return LSSAR_ERR_ALIAS;
+    // the pages are written too (table, lens and the inputs are read, and may be the same)
+    for (const Range &r : {kr, vr, cn, fi})
+        if (overlap(r, {a.c.k, page_bytes(a.c)}) || overlap(r, {a.c.v, page_bytes(a.c)})) return LSSAR_ERR_ALIAS;
     a.k_new = k_new;
     a.v_new = v_new;
     for (int i = 0; i < 3; ++i) {

@@ -847,3 +847,26 @@ def test_results_made_on_another_stream_take_no_block_in_use(torch_mod):
                 view = torch.int16 if w.element_size() == 2 else torch.int32
                 assert torch.equal(a.view(view), w.view(view)), i
     assert api.device_error_word() == 0
+
+
+@pytest.mark.gpu
+def test_append_reads_one_tensor_as_several_arguments(torch_mod):
+    # lens as the first positions says what the default does; as the counts, each sequence doubles
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    c = Cache(torch, [8, 3, 0], 2, 64, 16, seed=4)
+    new = torch.randn(3, 2, 8, 64, generator=c.g).to(c.dt).cuda()
+    results = []
+    for kw in (dict(counts=c.lens.clone()), dict(counts=c.lens, first_positions=c.lens)):
+        k, v, pos = c.k.clone(), c.v.clone(), torch.full((3, 2, c.cap), -1, dtype=torch.int32).cuda()
+        n = api.lssar_paged_append(new, new, k, v, c.table, c.lens, positions=pos, **kw)
+        results.append([n, k.view(torch.int16), v.view(torch.int16), pos])
+    assert api.device_error_word() == 0 and results[0][0].tolist() == [16, 6, 0]
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_appends_that_read_the_pages_are_refused(lib):
+    for at in (KP, KP + 4096, VP + 64):
+        assert append(lib, desc(), counts=at) == -8
+        assert append(lib, desc(), first=at) == -8
+        assert append(lib, desc(), vn=at) == -8
