@@ -296,7 +296,7 @@ int lssar_paged_append(const lssar_paged_cache_t *cache, const void *k_new, cons
  * the re-weighting modes or with scores 4 bytes for each (query head, slot) that
  * the table has room for.  Errors as lssar_paged_append, and LSSAR_ERR_MODE,
  * LSSAR_ERR_P; LSSAR_ERR_SHAPE also when B * Hkv * ceil(H / (8 Hkv)) *
- * ceil(capacity / 64) passes 2^31 - 1.
+ * ceil(capacity / 64) passes 2^31 - 2^16.
  */
 int lssar_paged_decode(const lssar_paged_cache_t *cache, const void *q, const long long *q_strides, void *out, int H,
                        int p, int mode, const float *scores, float *scores_out, cudaStream_t stream);

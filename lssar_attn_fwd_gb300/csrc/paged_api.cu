@@ -141,8 +141,9 @@ int lssar_paged_decode(const lssar_paged_cache_t *cache, const void *q, const lo
     if (st != LSSAR_OK) return st;
     if (!q || !q_strides || !out || !scores != !scores_out) return LSSAR_ERR_NULL;
     if (mode < LSSAR_MODE_SOFTMAX || mode > LSSAR_MODE_SIGMOID_RW) return LSSAR_ERR_MODE;
+    // (tile numbers are ints, and the CTAs' first tiles reach up to one CTA's count past the last)
     if (H < 1 || H % a.c.Hkv || H / a.c.Hkv > 128 || (unsigned long long)a.c.B * H > (1ULL << 24) ||
-        (unsigned long long)a.c.B * a.c.Hkv * ((H / a.c.Hkv + 7) / 8) * ((a.c.capacity() + 63) / 64) > 0x7fffffffULL)
+        (unsigned long long)a.c.B * a.c.Hkv * ((H / a.c.Hkv + 7) / 8) * ((a.c.capacity() + 63) / 64) > 0x7fff0000ULL)
         return LSSAR_ERR_SHAPE;
     const bool reweight = lssar::is_reweight(mode);
     if (reweight && (p < 1 || p > 1024)) return LSSAR_ERR_P;

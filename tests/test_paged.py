@@ -870,3 +870,9 @@ def test_appends_that_read_the_pages_are_refused(lib):
         assert append(lib, desc(), counts=at) == -8
         assert append(lib, desc(), first=at) == -8
         assert append(lib, desc(), vn=at) == -8
+
+
+def test_decodes_of_too_many_tiles_are_refused(lib):
+    # 2^31 - 2^15 tiles: the last CTA's first one would not fit an int
+    c = desc(B=65535, Hkv=1, max_pages=8192, page_stride=1024)
+    assert decode(lib, c, qs=(8192, 64), H=128, mode=0, sc=None, so=None) == -2
