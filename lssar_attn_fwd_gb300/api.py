@@ -402,7 +402,7 @@ def lssar_attn_decode(q, k_cache, v_cache, p=3, mode=MODE_LSSAR, out=None, strea
 # lssar_paged_cache_t and stride arrays as bytes: the paged calls are small
 # enough that marshalling is a good part of their time (a ctypes structure and
 # two arrays cost as much as a launch).
-_CACHE = struct.Struct("@PPPPqiiiiiii")
+_CACHE = struct.Struct("@PPPPqiiiiiii0q")   # (0q: padded to the structure's size)
 _pack_2 = struct.Struct("@2q").pack
 _pack_3 = struct.Struct("@3q").pack
 

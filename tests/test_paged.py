@@ -876,3 +876,9 @@ def test_decodes_of_too_many_tiles_are_refused(lib):
     # 2^31 - 2^15 tiles: the last CTA's first one would not fit an int
     c = desc(B=65535, Hkv=1, max_pages=8192, page_stride=1024)
     assert decode(lib, c, qs=(8192, 64), H=128, mode=0, sc=None, so=None) == -2
+
+
+def test_packed_cache_description_is_the_structure():
+    from lssar_attn_fwd_gb300 import api
+    values = dict(zip((f[0] for f in api.PagedCacheDesc._fields_), range(1, 13)))
+    assert api._CACHE.pack(*values.values()) == bytes(api.PagedCacheDesc(**values))
