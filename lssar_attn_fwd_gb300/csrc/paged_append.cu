@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append(const __grid_cons
     }
     const int t1 = ok ? min(cnt, t0 + stretch) : 0;
     if (t0 >= t1) return;
+    if (!dcheck(b < c.B && t0 >= 0 && len + t1 <= c.capacity(), c.err, kDbgItem)) return;
     const size_t at = (size_t)bh * c.capacity() + len;
     if (a.scores)
         for (int t = t0 + threadIdx.x; t < t1; t += kAppendThreads) a.scores[at + t] = 0.f;
@@ -63,6 +64,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append(const __grid_cons
                 bad = true;
                 continue;
             }
+            if (!dcheck(row[e] >= 0 && row[e] < c.page_size, c.err, kDbgGlobal)) continue;
             const size_t to = pg[e] * c.page_stride + ((size_t)h * c.page_size + row[e]) * c.d + part * 8;
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(c.k) + to) = kx[e];
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(c.v) + to) = vx[e];

@@ -297,6 +297,16 @@ __device__ __forceinline__ Segments segments_of(int row, int start, int nt, int 
     return Segments{row + a, (start + nt - 1) / run - a + 1};
 }
 
+// For the debug build's checks: entries of the segments' scratch; whether the `cnt` tiles
+// from p on are tiles of one row and of the scratch.
+__device__ __forceinline__ int segments_of_all(const Args &g) { return g.a.c.B * g.sp.heads_rows + g.sp.ctas; }
+template <int D>
+__device__ __forceinline__ bool in_numbering(const Args &g, const Place &p, int cnt) {
+    const PagedCache &c = g.a.c;
+    return p.b >= 0 && p.b < c.B && p.h >= 0 && p.h < c.Hkv && p.n <= c.capacity() && p.tile >= 0 && cnt > 0 && p.tile + cnt <= p.nt &&
+           p.t >= 0 && p.t + cnt <= c.B * g.sp.heads_rows * tiles_of<D>(c.capacity());
+}
+
 // (m, s): sums s relative to 2^m.  A row that must not be used has s = NaN.
 __device__ __forceinline__ float2 join_pair(float2 x, float2 y) {
     const float m = fmaxf(x.x, y.x);
@@ -535,6 +545,8 @@ paged_stream(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUt
         const Segments sg = segments_of(row, p.t - p.tile, p.nt, run);
         const int seg = row + blockIdx.x, g0 = p.nb * kHeads, heads = min(kHeads, g.sp.G - g0), cnt = min(t1 - p.t, p.nt - p.tile);
         const bool mine = head < heads;
+        // (every index of the scratch and the outputs follows from these)
+        if (!dcheck(in_numbering<D>(g, p, cnt) && heads > 0 && p.nb < g.sp.blocks && sg.first + sg.count <= segments_of_all(g) && seg < segments_of_all(g), c.err, kDbgItem)) break;
         bad = false;
         float2 st = make_float2(PHASE == kValues ? 0.f : kLowest, 0.f);   // (maximum or reference, sum of phi or w)
         float lift = 0.f;   // LSSA: 2^-reference
@@ -805,6 +817,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join(const __grid_const
         const int n = paged_len(c, b), nt = tiles_of<D>(n), hr = h * g.sp.blocks + gq / kHeads;
         Segments sg = {0, 0};
         if (live && n > 0) sg = segments_of(b * g.sp.heads_rows + hr, tiles_before<D>(c, b) * g.sp.heads_rows + hr * nt, nt, run);
+        if (!dcheck(sg.first + sg.count <= segments_of_all(g), c.err, kDbgItem)) sg = {0, 0};
         const float2 *sums = g.s.sums + (long long)sg.first * g.sp.zg + gq % kHeads;
         const float *o = g.s.o + ((long long)sg.first * g.sp.zg + gq % kHeads) * D + lane * kPerLane;
         ptx::grid_dependency_wait();
@@ -869,6 +882,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) paged_join(const __grid_const
         // number of the row's first tile among the stream's: the rows before it, each `blocks` times
         const int start = (p.t - p.tile - p.h * p.nt) * g.sp.blocks + p.h * g.sp.blocks * p.nt;
         const size_t base = ((size_t)p.b * c.Hkv + p.h) * c.capacity() + (size_t)p.tile * kTile + in;
+        if (!dcheck(in_numbering<D>(g, p, cnt) && start + g.sp.blocks * p.nt <= c.B * g.sp.heads_rows * tiles_of<D>(c.capacity()), c.err, kDbgItem)) break;
         __syncthreads();
 #pragma unroll 1
         for (int x = warp; x < G; x += kJoinWarps) {

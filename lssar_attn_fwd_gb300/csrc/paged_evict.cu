@@ -71,6 +71,12 @@ __device__ __forceinline__ int ld_cluster(const void *p, int rank) {
     return v;
 }
 
+__device__ __forceinline__ unsigned dynamic_shared_bytes() {
+    unsigned x;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(x));
+    return x;
+}
+
 // Barrier of the row's CTAs.
 __device__ __forceinline__ void row_sync(int ctas) {
     if (ctas == 1) __syncthreads();
@@ -138,7 +144,8 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
             sc_out[j] = sc[j];
             pos_out[j] = pos[j];
         }
-    if (n <= a.keep) {   // the whole cluster
+    // (one answer for the whole cluster; in the debug build a run that its shared memory does not hold)
+    if (n <= a.keep || !dcheck(b < c.B && (!CACHED || (unsigned)run * 4u <= dynamic_shared_bytes()), c.err, kDbgItem)) {
         if (rank == 0 && threadIdx.x == 0) count[bh] = 0;
         return;
     }
@@ -283,8 +290,9 @@ paged_select(const __grid_constant__ PagedEvict a, int *__restrict__ src, int *_
     for (int j = w0 + lane; j - lane < w1; j += 32) {
         const bool s = stays(j, seen), hole = j < w1 && j < a.keep && !s, mover = j >= a.keep && s;
         const unsigned hm = __ballot_sync(0xffffffffu, hole), mm = __ballot_sync(0xffffffffu, mover);
-        if (hole) to_list[holes + __popc(hm & below)] = j;
-        if (mover) from_list[movers + __popc(mm & below)] = j;
+        const int hi_at = holes + __popc(hm & below), mo_at = movers + __popc(mm & below);
+        if (hole && dcheck(hi_at < a.keep, c.err, kDbgGlobal)) to_list[hi_at] = j;
+        if (mover && dcheck(mo_at < a.keep, c.err, kDbgGlobal)) from_list[mo_at] = j;
         holes += __popc(hm);
         movers += __popc(mm);
     }
@@ -303,10 +311,12 @@ __global__ void __launch_bounds__(kMoveThreads, 4) paged_move(const __grid_const
     float *sc_out = a.scores_out + base;
     int *pos_out = a.positions_out + base;
     ptx::grid_dependency_wait();
-    const int total = __ldcg(count + bh);
+    int total = __ldcg(count + bh);
+    if (!dcheck(total >= 0 && total <= a.keep, c.err, kDbgItem)) total = 0;
     // scores and positions, a thread each
     for (int i = rank * kMoveThreads + threadIdx.x; i < total; i += splits * kMoveThreads) {
         const int from = __ldcg(from_list + i), to = __ldcg(to_list + i);
+        if (!dcheck(from >= a.keep && from < c.capacity() && to >= 0 && to < a.keep, c.err, kDbgGlobal)) continue;
         sc_out[to] = sc[from];
         pos_out[to] = pos[from];
     }
@@ -324,6 +334,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4) paged_move(const __grid_const
             const int i = i0 + e * groups;
             from[e] = i < total ? __ldcg(from_list + i) : -1;
             to[e] = i < total ? __ldcg(to_list + i) : 0;
+            if (!dcheck(from[e] < c.capacity() && to[e] >= 0 && to[e] < a.keep, c.err, kDbgGlobal)) from[e] = -1, to[e] = 0;
         }
         int pf[kMoves], pt[kMoves], fr[kMoves], tr[kMoves];
 #pragma unroll

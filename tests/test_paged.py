@@ -882,3 +882,34 @@ def test_packed_cache_description_is_the_structure():
     from lssar_attn_fwd_gb300 import api
     values = dict(zip((f[0] for f in api.PagedCacheDesc._fields_), range(1, 13)))
     assert api._CACHE.pack(*values.values()) == bytes(api.PagedCacheDesc(**values))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("G,hkv,d,page,width", [(1, 12, 64, 8, None), (20, 2, 128, 256, None), (3, 1, 64, 24, 700)])
+def test_debug_build_of_a_serving_step(torch_mod, monkeypatch, G, hkv, d, page, width):
+    # append, decode and eviction in the debug-check build (work items, list, scratch and
+    # page indices): the same bits, and nothing recorded
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api, build
+    build.build(debug=True)
+    results = []
+    lens = [0, 1, 255, 256, 700, 1030, 33]
+    for lib in (api.load_library(), api.load_debug_library()):
+        monkeypatch.setattr(api, "_LIB", lib)
+        c = Cache(torch, [n + 40 for n in lens], hkv, d, page, width=width, seed=7)
+        c.lens = torch.tensor(lens, dtype=torch.int32).cuda()
+        counts = torch.tensor([40, 0, 1, 39, 17, 40, 5], dtype=torch.int32).cuda()
+        new, scores = torch.randn(7, hkv, 40, d, generator=c.g).to(c.dt).cuda(), c.slots()
+        pos = torch.arange(c.cap, dtype=torch.int32).repeat(7, hkv, 1).cuda()
+        c.lens = api.lssar_paged_append(new, new, *c.args(), counts=counts, scores=scores, positions=pos)
+        got = [api.lssar_paged_decode(c.q(hkv * G), *c.args(), p=3, mode=mode, scores=scores)
+               for mode in (MODE_SOFTMAX, MODE_LSSA, MODE_LSSAR)]
+        for keep, recent in ((1000, 10), (200, 200), (3, 0)):
+            c.lens, _, _ = api.lssar_paged_evict(*c.args(), scores, pos, keep, recent=recent)
+            got.append(c.lens)
+        torch.cuda.synchronize()
+        assert api.device_error_word() == 0
+        results.append(got + [c.k, c.v, scores, pos])
+    for a, b in zip(*results):
+        view = torch.int16 if a.element_size() == 2 else torch.int32
+        assert torch.equal(a.view(view), b.view(view))
