@@ -513,7 +513,7 @@ def lssar_paged_append(k_new, v_new, k_pages, v_pages, table, lens, counts=None,
     if n and (kst[3] != 1 or vst[3] != 1):
         raise ValueError("the last dimension of k_new and v_new must be contiguous")
     if lens_out is None:
-        lens_out = _make(stream, dev, lambda: torch.empty_like(lens))
+        lens_out = torch.empty_like(lens) if stream is None else _make(stream, dev, lambda: torch.empty_like(lens))
     slots = (B, Hkv, cap)
     _paged_call("lssar_paged_append", dev, stream, desc, k_new.data_ptr(), _pack_3(*kst[:3]), v_new.data_ptr(),
                 _pack_3(*vst[:3]), n, _per_sequence("counts", counts, B, dev),
@@ -551,7 +551,8 @@ def lssar_paged_decode(q, k_pages, v_pages, table, lens, p=3, mode=MODE_LSSAR, s
     if scores_out is None:
         scores_out = scores
     if out is None:
-        out = _make(stream, dev, lambda: torch.empty(shape, dtype=dtype, device=q.device))
+        make = lambda: torch.empty(shape, dtype=dtype, device=q.device)   # noqa: E731
+        out = make() if stream is None else _make(stream, dev, make)
     elif (out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or not out.is_cuda
           or out.get_device() != dev):
         raise ValueError("out must be a contiguous [B, H, d] tensor of q's type on the cache's device")
@@ -582,7 +583,7 @@ def lssar_paged_evict(k_pages, v_pages, table, lens, scores, positions, keep, re
     if scores_out is None:
         scores_out, positions_out = scores, positions
     if lens_out is None:
-        lens_out = _make(stream, dev, lambda: torch.empty_like(lens))
+        lens_out = torch.empty_like(lens) if stream is None else _make(stream, dev, lambda: torch.empty_like(lens))
     slots = (B, Hkv, cap)
     _paged_call("lssar_paged_evict", dev, stream, desc, _slots("scores", scores, slots, torch.float32, dev),
                 _slots("positions", positions, slots, torch.int32, dev), _int32("keep", keep), _int32("recent", recent),
