@@ -329,20 +329,23 @@ __device__ float2 head_stats(Stat stat, int nch, int mode) {
 
 // The chunk's weights w_j from its scores z_j and the head's statistics.
 __device__ void weights_from_stats(float2 hs, int L, int mode, int p, const float *z, float *w, int n) {
-    const float m = hs.x, lift = mode == kLssa ? ptx::ex2(-fminf(m, 0.f)) : 1.f;
-    const RowConstants rc = row_constants(mode, L, hs);
-    for_pairs(n, [&](int j0, int j1, bool two) {
-        const float2 zz = make_float2(z[j0], z[j1]);
-        float2 y;
-        if (is_reweight(mode)) {
-            y = powi(above_offset(mode, zz, rc), p);
-        } else {
-            y = phi(mode, zz, m);
-            y = make_float2(y.x * lift, y.y * lift);   // LSSA: down to 2^-116 without the lift
-        }
-        w[j0] = y.x;
-        if (two) w[j1] = y.y;
-    });
+    const float m = hs.x;
+    auto each = [&](auto &&weight) {
+        for_pairs(n, [&](int j0, int j1, bool two) {
+            const float2 y = weight(make_float2(z[j0], z[j1]));
+            w[j0] = y.x;
+            if (two) w[j1] = y.y;
+        });
+    };
+    if (mode == kSoftmax) {
+        each([&](float2 zz) { return phi(kSoftmax, zz, m); });
+    } else if (mode == kLssa) {
+        const float lift = ptx::ex2(-fminf(m, 0.f));   // weights are down to 2^-116 without it
+        each([&](float2 zz) { return __fmul2_rn(softplus2(zz), make_float2(lift, lift)); });
+    } else {
+        const RowConstants rc = row_constants(mode, L, hs);
+        each([&](float2 zz) { return powi(above_offset(mode, zz, rc), p); });
+    }
 }
 
 __device__ void chunk_weights(const float2 *__restrict__ part_head, int nch, int L, int mode, int p,
