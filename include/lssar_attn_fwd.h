@@ -291,11 +291,14 @@ int lssar_paged_append(const lssar_paged_cache_t *cache, const void *k_new, cons
  * no scores; with a bad page number, NaN rows and NaN scores in the heads.
  * The sums have a fixed order: the same call on the same device gives the same
  * bits.  Two launches (softmax, LSSA) or three (re-weighting modes, which need a
- * row's scores before its weights).  Scratch from the library's pool: partial
- * sums, about 4 * (d + 4) bytes for each of B * H + 3 * 8 * SMs segments, and in
- * the re-weighting modes or with scores 4 bytes for each (query head, slot) that
- * the table has room for.  Errors as lssar_paged_append, and LSSAR_ERR_MODE,
- * LSSAR_ERR_P; LSSAR_ERR_SHAPE also when B * Hkv * ceil(H / (8 Hkv)) *
+ * row's scores before its weights).  K and V are read once for each of the
+ * n8 = ceil(H / (8 Hkv)) blocks of query heads of a key head.  Scratch from the
+ * library's pool, with h8 = min(H / Hkv, 8) heads for every block (groups that
+ * are no multiple of 8 leave some unused): 4 * (d + 4) bytes for each of
+ * (B * Hkv * n8 + 3 * SMs) * h8 partial sums at most, and in the re-weighting
+ * modes or with scores 4 bytes for each of B * Hkv * n8 * h8 heads and slot that
+ * the table has room for (rounded up to a multiple of 8192 / d), whatever the
+ * lengths.  Errors as lssar_paged_append, and LSSAR_ERR_MODE, LSSAR_ERR_P; LSSAR_ERR_SHAPE also when B * Hkv * ceil(H / (8 Hkv)) *
  * ceil(capacity / 64) passes 2^31 - 2^16.
  */
 int lssar_paged_decode(const lssar_paged_cache_t *cache, const void *q, const long long *q_strides, void *out, int H,

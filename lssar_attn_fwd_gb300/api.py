@@ -495,7 +495,8 @@ def lssar_paged_append(k_new, v_new, k_pages, v_pages, table, lens, counts=None,
     counts[b] of the n tokens are appended (default: all).  first_positions:
     [B] int32 position of the first of them (default: lens).  scores (float32)
     and positions (int32), [B, Hkv, max_pages * page_size]: the new slots
-    become 0 and the tokens' positions.  Returns the new lengths (lens_out).
+    become 0 and the tokens' positions.  Returns the new lengths (lens_out, which
+    may not be lens itself).
     Runs asynchronously on ``stream`` (default: the current stream).
     """
     import torch
@@ -573,8 +574,8 @@ def lssar_paged_evict(k_pages, v_pages, table, lens, scores, positions, keep, re
     ``keep`` move into the evicted slots before it, in the pages as in scores
     and positions ([B, Hkv, max_pages * page_size] float32 and int32); with
     scores_out and positions_out (both or neither) these are read only.
-    Returns (new lengths, scores_out, positions_out).  Runs asynchronously on
-    ``stream`` (default: the current stream).
+    Returns (new lengths, scores_out, positions_out); lens_out may not be lens
+    itself.  Runs asynchronously on ``stream`` (default: the current stream).
     """
     import torch
     desc, B, Hkv, cap, d, dev = _paged_cache(k_pages, v_pages, table, lens)

@@ -8,8 +8,9 @@
 // theta), 0)^p with kappa, theta from S1, m and i; out = sum w_j v_j / sum w_j.
 //
 // What bounds it: every key and value row is read once from HBM, 4d bytes per
-// (token, key head) against 4Gd flops for a group of G query heads.  Measured:
-// 8 sequences of 16K tokens, 12 heads of 64, with scores 81 us; 480 MB of ragged
+// (token, key head) against 4Gd flops for a group of G query heads, while G <= 8; each
+// further block of 8 query heads reads them again (from L2 where they are still there).
+// Measured: 8 sequences of 16K tokens, 12 heads of 64, with scores 82 us; 480 MB of ragged
 // grouped sequences, one pass, 86 us (5.6 TB/s; the copies alone reach 6.06).
 //
 // Split.  The tokens of all sequences are cut into tiles of 16 KB of one key

@@ -23,10 +23,12 @@
 // threads at once.  (Moved by the selecting clusters, which leave SMs idle and
 // have few loads in flight, 32 rows of 128K tokens took 226 us.)
 //
-// Bound by HBM for long rows (8 bytes of each slot, 8d of each moved row), by
-// the eight barriers of the selection (about a us each with their code) for short ones.
+// Long rows: HBM bounds the moves (8 bytes of each slot, 8d of each moved row), after a
+// selection of a third to half of the time that overlaps nothing.  Short ones: latency; a row
+// of one CTA goes through up to 24 block barriers with a few steps in shared memory between
+// them, and the moves are a launch of their own (alone 16 and 8 us).
 // Measured: 96 rows of 2K tokens 18.5 us, 96 rows of 16K tokens 66 us, 32 rows of 128K
-// tokens 211-218 us; the moves of the last at 5.8 TB/s, rows of 256 bytes at scattered places.
+// tokens 214-218 us; the moves of the last at 5.8 TB/s, rows of 256 bytes at scattered places.
 #include <climits>
 #include <cstdlib>
 
@@ -41,7 +43,7 @@ constexpr int kThreads = 512;
 constexpr int kMoveThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;            // portable cluster size
-constexpr int kCachedKeys = 18432;        // keys per CTA held in shared memory: three CTAs per SM
+constexpr int kCachedKeys = 18432;        // keys per CTA held in shared memory: two CTAs per SM (three up to about 18100)
 constexpr int kChunk = 4096;              // slots per CTA that are worth another CTA
 constexpr int kMoves = 2;                 // rows that a group of threads moves at once
 
@@ -402,7 +404,8 @@ cudaError_t launch_paged_evict(const PagedEvict &pr, void *ws, cudaStream_t stre
     if (e != cudaSuccess) return e;
     int *src = static_cast<int *>(ws), *dst = src + (size_t)a.c.B * a.c.Hkv * a.keep, *count = dst + (size_t)a.c.B * a.c.Hkv * a.keep;
     // CTAs per row by the longest row that the table has room for, in one wave of three
-    // per SM (96 rows of 16K tokens: 2, 4 and 8 CTAs each took 77, 68 and 82 us), or
+    // per SM (96 rows of 16K tokens: 2, 4 and 8 CTAs each took 77, 68 and 82 us; a run halved
+    // for the wave's sake is at most kCachedKeys / 2, of which three do fit an SM), or
     // more while the keys do not fit shared memory
     const int cap = a.c.capacity();
     const long long rows = (long long)a.c.B * a.c.Hkv;

@@ -13,8 +13,8 @@ namespace lssar {
 // lg2(1 + u), u = 2^-|z|, is off by 2^-22 and 0 from z = -24 on.  log2(1 + u) = u P(u), P of
 // degree 6 with the least largest relative error on [0, 1] (exchange algorithm): 1.3e-6,
 // 1.4e-6 with its steps in fp32.  One special function and seven FMAs, two scores at a
-// time: 2 sequences of 128K tokens, LSSAR, took 67.8 us with lg2 and its series below
-// u = 2^-6.
+// time: 2 sequences of 128K tokens, LSSAR, take 63.8 us; with lg2 and its series below
+// u = 2^-6 they took 67.8.
 __device__ __forceinline__ float2 softplus2(float2 z) {
     const float2 u = make_float2(ptx::ex2(-fabsf(z.x)), ptx::ex2(-fabsf(z.y)));
     const auto both = [](float c) { return make_float2(c, c); };
