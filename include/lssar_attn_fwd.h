@@ -72,8 +72,9 @@ typedef enum {
     LSSAR_ERR_PAGE = -10,   /* paged cache: page_size not a multiple of 8 in 8..256, no
                                page, or a page_stride that does not fit               */
     LSSAR_ERR_DTYPE = -11,  /* paged cache: dtype is not an lssar_dtype_t              */
-    LSSAR_ERR_KEEP = -12    /* lssar_paged_evict: keep < 1, recent < 0, sinks < 0 or
+    LSSAR_ERR_KEEP = -12,   /* lssar_paged_evict: keep < 1, recent < 0, sinks < 0 or
                                recent + sinks > keep                                  */
+    LSSAR_ERR_ROTARY = -13  /* rotary positions: a field of lssar_rotary_t out of range */
 } lssar_status_t;
 
 /*
@@ -327,6 +328,139 @@ int lssar_paged_decode(const lssar_paged_cache_t *cache, const void *q, const lo
  */
 int lssar_paged_evict(const lssar_paged_cache_t *cache, const float *scores, const int *positions, int keep, int recent,
                       int sinks, float *scores_out, int *positions_out, int *lens_out, cudaStream_t stream);
+
+/*
+ * Attention of a chunk: the last counts[b] rows of the attention over the
+ * lens[b] cached tokens of each sequence, in every mode (a prompt in pieces, or
+ * whole; single tokens beside chunks).  Row t < counts[b] is row
+ * i = lens[b] - counts[b] + t + 1: it attends to the slots 0..i-1, its own the
+ * last of them (append first).  i counts cached tokens, also after an eviction.
+ *   q   : [B, H, n, d] of the cache's type; q_strides is a HOST array of the
+ *         element strides of (B, H, n), multiples of 8 where the dimension is
+ *         above 1.  Rows t >= counts[b] are not read.
+ *   n   : rows per sequence, 1..2^24; H: query heads, a multiple of Hkv, at most
+ *         128 * Hkv.
+ *   counts : [B] int32, device, 0..min(n, lens[b]) each; NULL: n for every sequence.
+ *   out : [B, H, n, d] contiguous, of the cache's type.  Rows t >= counts[b] are
+ *         not written.
+ * A bad length or count (code 51) gives NaN in all n rows of that sequence, a bad
+ * page number among the pages in use (code 52) in its rows t < counts[b].  What
+ * the rows of pages past lens[b] hold does not matter.
+ * A value that is infinite or NaN among the cached tokens reaches the rows of
+ * the chunk that attend to it, and may reach rows up to 383 slots before it.
+ * The sums have a fixed order: the same call on the same device gives the same
+ * bits.  Errors as lssar_paged_decode.
+ */
+int lssar_paged_attend(const lssar_paged_cache_t *cache, const void *q, const long long *q_strides, void *out, int H,
+                       int n, const int *counts, int p, int mode, cudaStream_t stream);
+
+/*
+ * Rotary positions (the notes' models are GPT-2 with RoPE): the pair c of a row
+ * at position m turns by m * f_c radians, (u, v) -> (u cos - v sin, u sin + v cos),
+ *   f_c = base^(-2c / rot_dim), c = 0 .. rot_dim / 2 - 1, before scaling.
+ * The pairs are the elements (c, c + rot_dim / 2), or (2c, 2c + 1) where
+ * interleaved; elements from rot_dim on are copied.  For contexts longer than
+ * the trained one f_c is scaled:
+ *   LINEAR  f_c / factor
+ *   BASE    base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   BANDS   f_c (g + (1 - g) / factor), g = clamp((r - low) / (high - low), 0, 1),
+ *           r = original_length f_c / (2 pi): pairs that turn often within the
+ *           trained length keep their frequency
+ * Angles are taken modulo a turn in 64-bit fixed point, exact to 2^-33 turns at
+ * every 32-bit position; the products are in fp32, rounded once.
+ */
+typedef enum {
+    LSSAR_ROPE_PLAIN = 0, LSSAR_ROPE_LINEAR = 1, LSSAR_ROPE_BASE = 2, LSSAR_ROPE_BANDS = 3
+} lssar_rope_scaling_t;
+
+typedef struct {
+    double base;             /* > 1, finite */
+    double factor;           /* >= 1, finite (not PLAIN) */
+    double low, high;        /* 0 <= low < high, finite (BANDS) */
+    int original_length;     /* >= 1 (BANDS) */
+    int rot_dim;             /* a multiple of 16 in 16..d */
+    int interleaved;         /* 0 or 1 */
+    int scaling;             /* lssar_rope_scaling_t */
+} lssar_rotary_t;
+
+/*
+ * Turns q [B, H, L, d] and k [B, Hk, L, d] (k NULL: q alone) by their positions.
+ *   q_strides, k_strides : HOST arrays of the element strides of (B, H, L),
+ *         multiples of 8 where the dimension is above 1.
+ *   positions : device int32, or NULL: token t is at position t.  per_token 0:
+ *         [B], token t of sequence b at positions[b] + t; 1: [B, L].
+ *   q_out, k_out : contiguous, apart from everything else; or the input itself,
+ *         which is then turned in place at its own strides (rows that do not
+ *         overlap; q and k may be slices of one [B, L, heads, d] buffer).
+ * d is 64 or 128, dtype an lssar_dtype_t, H and Hk at least 1.
+ * lssar_rope_bwd turns back: the gradients with respect to the inputs from
+ * those with respect to the outputs (the same arguments).
+ * Errors: LSSAR_ERR_NULL, SHAPE, HEADDIM, DTYPE, ROTARY, ALIGN, ALIAS, CUDA.
+ */
+int lssar_rope(const void *q, const long long *q_strides, void *q_out, int H, const void *k, const long long *k_strides,
+               void *k_out, int Hk, int B, int L, int d, int dtype, const lssar_rotary_t *rotary, const int *positions,
+               int per_token, cudaStream_t stream);
+int lssar_rope_bwd(const void *q, const long long *q_strides, void *q_out, int H, const void *k, const long long *k_strides,
+                   void *k_out, int Hk, int B, int L, int d, int dtype, const lssar_rotary_t *rotary,
+                   const int *positions, int per_token, cudaStream_t stream);
+
+/*
+ * lssar_paged_append with rotary positions, in one launch: token t < counts[b]
+ * of sequence b is at position first_positions[b] + t (NULL: lens[b] + t); its
+ * key is turned on its way to the pages, its query turned into q_out.
+ *   q : [B, H, n, d] of the cache's type, q_strides as above; H >= 1.
+ *   q_out : [B, H, n, d] contiguous, or q itself (in place).  Rows t >= counts[b]
+ *         are not written, nor those of a sequence that is left alone.
+ * Other arguments, results and errors as lssar_paged_append and lssar_rope.
+ */
+int lssar_paged_append_rope(const lssar_paged_cache_t *cache, const void *q, const long long *q_strides, void *q_out,
+                            int H, const void *k_new, const long long *k_strides, const void *v_new,
+                            const long long *v_strides, int n, const lssar_rotary_t *rotary, const int *counts,
+                            const int *first_positions, float *scores, int *positions, int *lens_out,
+                            cudaStream_t stream);
+
+/*
+ * Reserve: page numbers from a list of free pages for counts[b] more tokens of
+ * each sequence, so that an append of them fits.  Sequence b holds
+ * ceil(lens[b] / page_size) pages; what it needs more comes from the end of the
+ * list, in the order of the sequences, and goes to the next columns of its row
+ * of table.
+ *   table : [B, max_pages] int32, device; only those entries are written.
+ *   counts : [B] int32, device, >= 0; NULL: 1 for every sequence.
+ *   free_pages : [n_pages] int32, device, read; its first free_count[0] entries
+ *         are free pages (free_count: [1] int32, device).
+ *   counts_out : [B] int32, written: counts[b] where the sequence has its pages,
+ *         0 where it does not: those that need pages, from the first one on whose
+ *         needs, added to those before it, pass free_count[0] (they get none).
+ *   free_out : [1] int32, written: the free pages left.
+ * A bad length or count, or a new length past the capacity, is not served and
+ * needs nothing; a free_count outside 0..n_pages serves none (free_out =
+ * free_count): code 51.  An entry of the list that is no page of 0..n_pages-1
+ * becomes -1 in the table: code 52.
+ * page_size as in a cache; B, max_pages, n_pages >= 1, max_pages * page_size <=
+ * 2^24.  Outputs overlap nothing else (table is one).
+ */
+int lssar_paged_reserve(int *table, int max_pages, int page_size, const int *lens, const int *counts, int B,
+                        const int *free_pages, int n_pages, const int *free_count, int *counts_out, int *free_out,
+                        cudaStream_t stream);
+
+/*
+ * Release: the pages of sequence b past its first ceil(lens_new[b] / page_size),
+ * up to ceil(lens[b] / page_size), go to the end of the list of free pages, in
+ * the order of the sequences and of their tables (after an eviction, or with
+ * lens_new[b] = 0 at a sequence's end).  The table stays as it is: entries past
+ * a length are not read.
+ *   free_pages : [n_pages], written from entry free_count[0] on.
+ *   free_out : [1] int32, written: the free pages there are now.
+ * A length outside 0..capacity, or a lens_new[b] outside 0..lens[b], releases
+ * nothing: code 51.  A free_count outside 0..n_pages, or one that the released
+ * pages carry past n_pages: nothing is done, free_out = free_count, code 51.
+ * An entry of the table that is no page is passed on as it is, code 52.
+ * Pages that sequences share must be released by one of them alone.
+ * Sizes and errors as lssar_paged_reserve.
+ */
+int lssar_paged_release(const int *table, int max_pages, int page_size, const int *lens, const int *lens_new, int B,
+                        int *free_pages, int n_pages, const int *free_count, int *free_out, cudaStream_t stream);
 
 /*
  * Same operation and contract as lssar_attn_fwd, computed by a plain CUDA-core

@@ -33,6 +33,12 @@ _EXPORTS = (
     "lssar_paged_append",
     "lssar_paged_decode",
     "lssar_paged_evict",
+    "lssar_paged_attend",
+    "lssar_paged_append_rope",
+    "lssar_paged_reserve",
+    "lssar_paged_release",
+    "lssar_rope",
+    "lssar_rope_bwd",
     "lssar_status_string",
     "lssar_device_error_word",
     "lssar_abi_version",
@@ -124,7 +130,14 @@ def _open(path):
     lib.lssar_paged_append.argtypes = [ptr] * 5 + [num] + [ptr] * 6
     lib.lssar_paged_decode.argtypes = [ptr] * 4 + [num] * 3 + [ptr] * 3
     lib.lssar_paged_evict.argtypes = [ptr] * 3 + [num] * 3 + [ptr] * 4
-    for name in ("lssar_paged_append", "lssar_paged_decode", "lssar_paged_evict"):
+    lib.lssar_paged_attend.argtypes = [ptr] * 4 + [num] * 2 + [ptr] + [num] * 2 + [ptr]
+    lib.lssar_paged_append_rope.argtypes = [ptr] * 4 + [num] + [ptr] * 4 + [num] + [ptr] * 7
+    lib.lssar_paged_reserve.argtypes = [ptr] + [num] * 2 + [ptr] * 2 + [num] + [ptr] + [num] + [ptr] * 4
+    lib.lssar_paged_release.argtypes = [ptr] + [num] * 2 + [ptr] * 2 + [num] + [ptr] + [num] + [ptr] * 3
+    rope_args = ([ptr] * 3 + [num]) * 2 + [num] * 4 + [ptr] * 2 + [num] + [ptr]
+    lib.lssar_rope.argtypes = lib.lssar_rope_bwd.argtypes = rope_args
+    for name in ("lssar_paged_append", "lssar_paged_decode", "lssar_paged_evict", "lssar_paged_attend",
+                 "lssar_paged_append_rope", "lssar_paged_reserve", "lssar_paged_release", "lssar_rope", "lssar_rope_bwd"):
         getattr(lib, name).restype = ctypes.c_int
     lib.lssar_selftest_stall.argtypes = [ctypes.c_void_p]
     lib.lssar_selftest_stall.restype = ctypes.c_int
@@ -592,6 +605,239 @@ def lssar_paged_evict(k_pages, v_pages, table, lens, scores, positions, keep, re
                 _slots("positions_out", positions_out, slots, torch.int32, dev),
                 _per_sequence("lens_out", lens_out, B, dev))
     return lens_out, scores_out, positions_out
+
+
+def _rows(name, t, shape, dtype, dev):
+    """The strides of a [B, H, n, d] tensor of rows, d contiguous."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on the same device")
+    st = t.stride()
+    if st[3] != 1 and t.numel():
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return _pack_3(*st[:3])
+
+
+def _same_place(x, y):
+    return x.data_ptr() == y.data_ptr() and x.stride() == y.stride()
+
+
+def lssar_paged_attend(q, k_pages, v_pages, table, lens, counts=None, p=3, mode=MODE_LSSAR, out=None, stream=None):
+    """The rows of a chunk of new tokens against a paged cache, in every mode.
+
+    q: [B, H, n, d] of the cache's type (d contiguous, other strides multiples of
+    8), H a multiple of Hkv, at most 128 * Hkv; the cache as in
+    :func:`lssar_paged_append`, the chunk already appended.  counts: [B] int32, the
+    rows of each sequence (default: n); row t < counts[b] attends to the first
+    lens[b] - counts[b] + t + 1 cached tokens.  Returns out [B, H, n, d]
+    (contiguous); rows t >= counts[b] are not written, and zeros where the call
+    makes out itself.  Runs asynchronously on ``stream`` (default: the current
+    stream).
+    """
+    import torch
+    desc, B, Hkv, cap, d, dev = _paged_cache(k_pages, v_pages, table, lens)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
+        raise ValueError("q must be [B, H, n, d] with the cache's B and d")
+    shape, dtype = q.shape, k_pages.dtype
+    strides = _rows("q", q, shape, dtype, dev)
+    if out is None:
+        new = torch.empty if counts is None else torch.zeros
+        make = lambda: new(shape, dtype=dtype, device=q.device)   # noqa: E731
+        out = make() if stream is None else _make(stream, dev, make)
+    elif (out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or not out.is_cuda
+          or out.get_device() != dev):
+        raise ValueError("out must be a contiguous [B, H, n, d] tensor of q's type on the cache's device")
+    _paged_call("lssar_paged_attend", dev, stream, desc, q.data_ptr(), strides, out.data_ptr(), shape[1], shape[2],
+                _per_sequence("counts", counts, B, dev), _int32("p", p), _int32("mode", mode))
+    return out
+
+
+_ROTARY = struct.Struct("@4d4i")   # lssar_rotary_t
+
+
+class Rotary:
+    """Rotary positions of heads of d elements: the first ``rot_dim`` (default: all)
+    turn by position * frequency, base^(-2c / rot_dim) for pair c; the pairs are
+    (c, c + rot_dim / 2), or (2c, 2c + 1) where interleaved.  scaling for contexts
+    past the trained ``original_length``: "linear" (frequencies / factor), "base"
+    (a larger base) or "bands" (pairs that turn less than ``low`` times within the
+    trained length / factor, those that turn more than ``high`` times unchanged)."""
+
+    SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3}
+
+    def __init__(self, d, rot_dim=None, base=10000.0, interleaved=False, scaling="none", factor=1.0, original_length=1,
+                 low=1.0, high=32.0):
+        if scaling not in self.SCALINGS:
+            raise ValueError(f"scaling must be one of {', '.join(self.SCALINGS)}")
+        self.d, self.rot_dim = int(d), int(d if rot_dim is None else rot_dim)
+        self.desc = _ROTARY.pack(base, factor, low, high, _int32("original_length", original_length),
+                                 _int32("rot_dim", self.rot_dim), bool(interleaved), self.SCALINGS[scaling])
+
+
+def _rope(name, q, k, rotary, positions, q_out, k_out, stream):
+    import torch
+    for t in (q, q if k is None else k):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("q and k must be torch tensors")
+        if not t.is_cuda or t.dim() != 4 or (t.dtype is not torch.bfloat16 and t.dtype is not torch.float16):
+            raise ValueError("q and k must be bfloat16 or float16 CUDA tensors [B, heads, L, d]")
+    (B, H, L, d), dtype, dev = q.shape, q.dtype, q.get_device()
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out needs k")
+    elif (k.shape[0], k.shape[2], k.shape[3]) != (B, L, d):
+        raise ValueError("q and k must share B, L and d")
+    if not isinstance(rotary, Rotary) or rotary.d != d:
+        raise ValueError("rotary must be a Rotary of q's head dimension")
+    per_token = 0
+    if positions is not None:
+        per_token = int(positions.dim() == 2)
+        if (positions.dtype is not torch.int32 or positions.shape != ((B, L) if per_token else (B,))
+                or not positions.is_contiguous() or not positions.is_cuda or positions.get_device() != dev):
+            raise ValueError("positions must be a contiguous int32 [B] or [B, L] tensor on q's device")
+    outs = []
+    for what, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            outs.append(None)
+        elif y is None:
+            make = lambda: torch.empty(x.shape, dtype=dtype, device=x.device)   # noqa: E731,B023
+            outs.append(make() if stream is None else _make(stream, dev, make))
+        elif _same_place(x, y) and y.shape == x.shape and y.dtype is dtype:
+            outs.append(y)
+        elif (y.shape != x.shape or y.dtype is not dtype or not y.is_contiguous() or not y.is_cuda
+              or y.get_device() != dev):
+            raise ValueError(f"{what}_out must be {what} itself or a contiguous tensor like it")
+        else:
+            outs.append(y)
+    args = []
+    for x, y in ((q, outs[0]), (k, outs[1])):
+        args += [None, None, None, 0] if x is None else [x.data_ptr(), _rows("q and k", x, x.shape, dtype, dev),
+                                                         y.data_ptr(), x.shape[1]]
+    _paged_call(name, dev, stream, *args, B, L, d, DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP16, rotary.desc,
+                None if positions is None else positions.data_ptr(), per_token)
+    return outs[0], outs[1]
+
+
+def lssar_rope(q, k, rotary, positions=None, q_out=None, k_out=None, stream=None):
+    """Turns queries and keys by their positions; returns (q_out, k_out).
+
+    q: [B, H, L, d], k: [B, Hk, L, d] or None, bf16 or fp16 (d = 64 or 128
+    contiguous, other strides multiples of 8).  rotary: a :class:`Rotary`.
+    positions: int32 [B] (token t of sequence b at positions[b] + t) or [B, L];
+    default: token t at t.  q_out, k_out: contiguous tensors apart from the
+    inputs, or the inputs themselves (in place).  Runs asynchronously on
+    ``stream`` (default: the current stream).
+    """
+    return _rope("lssar_rope", q, k, rotary, positions, q_out, k_out, stream)
+
+
+def lssar_rope_bwd(dq, dk, rotary, positions=None, dq_out=None, dk_out=None, stream=None):
+    """Gradients with respect to the inputs of :func:`lssar_rope` from those with
+    respect to its outputs (such as dq, dk of :func:`lssar_attn_bwd`): the same
+    rows turned back.  Arguments and results as there."""
+    return _rope("lssar_rope_bwd", dq, dk, rotary, positions, dq_out, dk_out, stream)
+
+
+def lssar_paged_append_rope(q, k_new, v_new, k_pages, v_pages, table, lens, rotary, counts=None, first_positions=None,
+                            scores=None, positions=None, lens_out=None, q_out=None, stream=None):
+    """:func:`lssar_paged_append` with rotary positions, in one launch: keys are
+    turned on their way to the pages, and the queries of the same tokens.
+
+    q: [B, H, n, d] (or [B, H, d] for one token) of the cache's type, strides as
+    k_new's; token t of sequence b is at position first_positions[b] + t (default:
+    lens[b] + t).  q_out: contiguous like q, or q itself (in place); rows t >=
+    counts[b] are not written, and zeros where the call makes q_out itself.
+    Other arguments as :func:`lssar_paged_append`.  Returns (q_out, new lengths).
+    """
+    import torch
+    desc, B, Hkv, cap, d, dev = _paged_cache(k_pages, v_pages, table, lens)
+    if not isinstance(rotary, Rotary) or rotary.d != d:
+        raise ValueError("rotary must be a Rotary of the cache's head dimension")
+    dtype, q_shape = k_pages.dtype, q.shape
+    if q_out is None:
+        new = torch.empty if counts is None else torch.zeros
+        make = lambda: new(q_shape, dtype=dtype, device=q.device)   # noqa: E731
+        q_out = make() if stream is None else _make(stream, dev, make)
+    result = q_out
+    if q_out.shape != q_shape:
+        raise ValueError("q_out must have q's shape")
+    one = lambda t: t.unsqueeze(2) if t.dim() == 3 else t   # noqa: E731
+    q, q_out, k_new, v_new = one(q), one(q_out), one(k_new), one(v_new)
+    if q.dim() != 4 or k_new.dim() != 4:
+        raise ValueError("q, k_new and v_new must be [B, heads, n, d]")
+    n, rows = k_new.shape[2], (B, Hkv, k_new.shape[2], d)
+    kst, vst = _rows("k_new", k_new, rows, dtype, dev), _rows("v_new", v_new, rows, dtype, dev)
+    qst = _rows("q", q, (B, q.shape[1], n, d), dtype, dev)
+    _rows("q_out", q_out, q.shape, dtype, dev)
+    if not q_out.is_contiguous() and not _same_place(q, q_out):
+        raise ValueError("q_out must be contiguous, or q itself")
+    if lens_out is None:
+        lens_out = torch.empty_like(lens) if stream is None else _make(stream, dev, lambda: torch.empty_like(lens))
+    slots = (B, Hkv, cap)
+    _paged_call("lssar_paged_append_rope", dev, stream, desc, q.data_ptr(), qst, q_out.data_ptr(), q.shape[1],
+                k_new.data_ptr(), kst, v_new.data_ptr(), vst, n, rotary.desc, _per_sequence("counts", counts, B, dev),
+                _per_sequence("first_positions", first_positions, B, dev),
+                _slots("scores", scores, slots, torch.float32, dev), _slots("positions", positions, slots, torch.int32, dev),
+                _per_sequence("lens_out", lens_out, B, dev))
+    return result, lens_out
+
+
+def _pages(table, lens, free_pages, free_count, free_out, stream):
+    """Checks the tensors of a page table and a list of free pages; returns (B,
+    max_pages, n_pages, free_out, device index)."""
+    import torch
+    for t in (table, lens, free_pages, free_count):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("table, lens, free_pages and free_count must be torch tensors")
+    if not table.is_cuda or table.dtype is not torch.int32 or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous int32 [B, max_pages] CUDA tensor")
+    dev, (B, max_pages) = table.get_device(), table.shape
+    if free_out is None:
+        free_out = torch.empty_like(free_count) if stream is None else _make(stream, dev, lambda: torch.empty_like(free_count))
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be [n_pages]")
+    n_pages = free_pages.shape[0]
+    for name, t, shape in (("lens", lens, (B,)), ("free_pages", free_pages, (n_pages,)), ("free_count", free_count, (1,)),
+                           ("free_out", free_out, (1,))):
+        if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda or t.get_device() != dev:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on the table's device")
+    return B, max_pages, n_pages, free_out, dev
+
+
+def lssar_paged_reserve(table, lens, counts, page_size, free_pages, free_count, counts_out=None, free_out=None, stream=None):
+    """Page numbers for counts[b] more tokens of each sequence, from a list of free pages.
+
+    table: [B, max_pages] int32, its rows get the new pages behind the
+    ceil(lens[b] / page_size) that they hold; counts: [B] int32, or None (one
+    token each).  free_pages: [n_pages] int32, of which the first free_count[0] are
+    free; pages are taken from their end, in the order of the sequences.  Returns
+    (counts_out, free_out): counts[b] where the sequence got its pages and 0 where
+    the list has run out (the counts of the append that follows), and the free
+    pages left ([1], not free_count itself).  Runs asynchronously on ``stream``
+    (default: the current stream).
+    """
+    import torch
+    B, max_pages, n_pages, free_out, dev = _pages(table, lens, free_pages, free_count, free_out, stream)
+    if counts_out is None:
+        counts_out = torch.empty_like(lens) if stream is None else _make(stream, dev, lambda: torch.empty_like(lens))
+    _paged_call("lssar_paged_reserve", dev, stream, table.data_ptr(), max_pages, _int32("page_size", page_size),
+                lens.data_ptr(), _per_sequence("counts", counts, B, dev), B, free_pages.data_ptr(), n_pages,
+                free_count.data_ptr(), _per_sequence("counts_out", counts_out, B, dev), free_out.data_ptr())
+    return counts_out, free_out
+
+
+def lssar_paged_release(table, lens, lens_new, page_size, free_pages, free_count, free_out=None, stream=None):
+    """Gives the pages between lens_new[b] and lens[b] tokens back to the list of
+    free pages (lens_new 0: all of the sequence's), in the order of the sequences;
+    arguments as :func:`lssar_paged_reserve`.  Returns free_out, the free pages
+    there are now.  Runs asynchronously on ``stream`` (default: the current
+    stream)."""
+    if lens_new is None:
+        raise ValueError("lens_new is needed")
+    B, max_pages, n_pages, free_out, dev = _pages(table, lens, free_pages, free_count, free_out, stream)
+    _paged_call("lssar_paged_release", dev, stream, table.data_ptr(), max_pages, _int32("page_size", page_size),
+                lens.data_ptr(), _per_sequence("lens_new", lens_new, B, dev), B, free_pages.data_ptr(), n_pages,
+                free_count.data_ptr(), free_out.data_ptr())
+    return free_out
 
 
 def lssar_attn_fwd_profiled(q, k, v, p, mode, out, stream, ev_start, ev_main, ev_end):

@@ -360,6 +360,7 @@ const char *lssar_status_string(int status) {
         case LSSAR_ERR_PAGE: return "invalid pages (page_size a multiple of 8 in 8..256, n_pages >= 1, page_stride a multiple of 8 and at least one page)";
         case LSSAR_ERR_DTYPE: return "unknown cache type (bfloat16 or float16)";
         case LSSAR_ERR_KEEP: return "keep must be at least 1 and hold recent + sinks (each >= 0)";
+        case LSSAR_ERR_ROTARY: return "invalid rotary positions (base > 1, rot_dim a multiple of 16 in 16..d, factor >= 1, 0 <= low < high, original_length >= 1)";
         default: return "unknown status";
     }
 }
@@ -369,6 +370,6 @@ int lssar_device_error_word(unsigned int *word) {
     return lssar::read_and_clear_error_word(word) == cudaSuccess ? LSSAR_OK : LSSAR_ERR_CUDA;
 }
 
-int lssar_abi_version(void) { return 10100; }
+int lssar_abi_version(void) { return 10200; }
 
 }  // extern "C"

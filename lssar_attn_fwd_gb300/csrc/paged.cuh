@@ -61,6 +61,30 @@ struct PagedEvict {
 size_t paged_evict_workspace_bytes(const PagedEvict &pr);
 cudaError_t launch_paged_evict(const PagedEvict &pr, void *ws, cudaStream_t stream);
 
+struct PagedAttend {
+    PagedCache c;
+    const void *q;            // (b, h, t) rows at these element strides
+    long long qs[3];
+    void *out;                // [B, H, n, d]
+    const int *counts;        // [B] or null
+    int H, n, p, mode;
+};
+size_t paged_attend_workspace_bytes(const PagedAttend &pr, int sms);
+cudaError_t launch_paged_attend(const PagedAttend &pr, void *ws, int sms, cudaStream_t stream);
+
+// Page numbers taken from, or given back to, a list of free pages.
+struct PagedPages {
+    int *table;               // [B, max_pages]; release: read only
+    const int *lens, *other;  // other: counts or null (reserve), lens_new (release)
+    int *free_pages;          // [n_pages]; reserve: read only
+    const int *free_count;
+    int *counts_out, *free_out;
+    int B, max_pages, page_size, n_pages;
+    unsigned *err;
+};
+cudaError_t launch_paged_reserve(const PagedPages &pr, cudaStream_t stream);
+cudaError_t launch_paged_release(const PagedPages &pr, cudaStream_t stream);
+
 // The length of sequence b, or 0 with the error word set where it is outside
 // 0..capacity.
 __device__ __forceinline__ int paged_len(const PagedCache &c, int b) {

@@ -1,98 +1,16 @@
 // C ABI of the paged key-value cache: argument validation and dispatch.  The
 // declarations and the full contract are in include/lssar_attn_fwd.h.
-#include <cstdint>
 #include <initializer_list>
 
-#include "lssar_attn_fwd.h"
-#include "paged.cuh"
+#include "api_checks.cuh"
 
-namespace {
-
-constexpr int kMaxPageSize = 256;
-constexpr unsigned long long kMaxElems = 1ULL << 40;
-
-// A stretch of device memory that a call reads or writes.
-struct Range {
-    const void *p;
-    size_t bytes;
-};
-
-bool overlap(const Range &a, const Range &b) {
-    const auto x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
-}
-
-bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
-
-// Checks of the cache description (pure host); fills *out.
-int check_cache(const lssar_paged_cache_t *c, lssar::PagedCache *out) {
-    if (!c || !c->k_pages || !c->v_pages || !c->table || !c->lens) return LSSAR_ERR_NULL;
-    if (c->d != 64 && c->d != 128) return LSSAR_ERR_HEADDIM;
-    if (c->dtype != LSSAR_DTYPE_BF16 && c->dtype != LSSAR_DTYPE_FP16) return LSSAR_ERR_DTYPE;
-    if (c->B < 1 || c->Hkv < 1 || c->max_pages < 1) return LSSAR_ERR_SHAPE;
-    if (c->page_size < 8 || c->page_size > kMaxPageSize || c->page_size % 8 || c->n_pages < 1) return LSSAR_ERR_PAGE;
-    const unsigned long long block = (unsigned long long)c->Hkv * c->page_size * c->d;
-    if (block > (1ULL << 31) || c->page_stride < (long long)block || c->page_stride % 8 ||
-        (unsigned long long)c->page_stride > kMaxElems || (unsigned long long)c->n_pages * c->page_stride > kMaxElems)
-        return LSSAR_ERR_PAGE;
-    const unsigned long long cap = (unsigned long long)c->max_pages * c->page_size;
-    if (cap > (1ULL << 24) || (unsigned long long)c->B * c->Hkv > (1ULL << 24) ||
-        (unsigned long long)c->B * c->Hkv * cap * c->d > kMaxElems)
-        return LSSAR_ERR_SHAPE;
-    if (misaligned(c->k_pages, 16) || misaligned(c->v_pages, 16) || misaligned(c->table, 4) || misaligned(c->lens, 4))
-        return LSSAR_ERR_ALIGN;
-    // K and V may be interleaved in one buffer, page by page: their blocks of
-    // `block` elements, page_stride apart, must not meet
-    const long long bytes = (long long)block * 2, stride = c->page_stride * 2;
-    const long long gap = (long long)(reinterpret_cast<intptr_t>(c->v_pages) - reinterpret_cast<intptr_t>(c->k_pages));
-    const long long span = (c->n_pages - 1) * stride + bytes;
-    if (gap > -span && gap < span) {
-        const long long r = ((gap % stride) + stride) % stride;
-        if (r < bytes || r > stride - bytes) return LSSAR_ERR_ALIAS;
-    }
-    *out = lssar::PagedCache{c->k_pages, c->v_pages, c->table, c->lens, c->page_stride, c->n_pages, c->max_pages,
-                             c->page_size, c->B, c->Hkv, c->d, c->dtype == LSSAR_DTYPE_FP16, nullptr};
-    return LSSAR_OK;
-}
-
-// Bytes from the first page of K or V to the end of the last.
-size_t page_bytes(const lssar::PagedCache &c) {
-    return ((size_t)(c.n_pages - 1) * c.page_stride + (size_t)c.Hkv * c.page_size * c.d) * 2;
-}
-
-// The memory of K, V, table and lens, with `outs` (written) tested against
-// them, against one another and against `ins` (read).
-bool any_alias(const lssar::PagedCache &c, std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
-    const size_t pages = page_bytes(c);
-    const Range own[4] = {{c.k, pages}, {c.v, pages}, {c.table, (size_t)c.B * c.max_pages * 4}, {c.lens, (size_t)c.B * 4}};
-    for (const Range *o = outs.begin(); o != outs.end(); ++o) {
-        for (const Range &x : own)
-            if (overlap(*o, x)) return true;
-        for (const Range &x : ins)
-            if (overlap(*o, x)) return true;
-        for (const Range *x = outs.begin(); x != o; ++x)
-            if (overlap(*o, *x)) return true;
-    }
-    return false;
-}
-
-// A [B, Hkv, n, d] view by its strides in elements: the innermost dimension is
-// contiguous, the others any multiple of 8 (16-byte rows).  Fills the range it spans.
-int check_view(const void *p, const long long *s, long long B, long long H, long long n, int d, Range *r) {
-    unsigned long long last = 0;
-    const long long dims[3] = {B, H, n};
-    for (int i = 0; i < 3; ++i) {
-        if (s[i] < 0 || s[i] > (long long)kMaxElems) return LSSAR_ERR_SHAPE;
-        if (dims[i] > 1 && s[i] % 8) return LSSAR_ERR_ALIGN;
-        last += (unsigned long long)(dims[i] > 0 ? dims[i] - 1 : 0) * s[i];
-        if (last > kMaxElems) return LSSAR_ERR_SHAPE;
-    }
-    if (misaligned(p, 16)) return LSSAR_ERR_ALIGN;
-    *r = Range{p, (size_t)(last + d) * 2};
-    return LSSAR_OK;
-}
-
-}  // namespace
+using lssar::any_alias;
+using lssar::check_cache;
+using lssar::check_view;
+using lssar::misaligned;
+using lssar::overlap;
+using lssar::page_bytes;
+using lssar::Range;
 
 extern "C" {
 
@@ -206,6 +124,132 @@ int lssar_paged_evict(const lssar_paged_cache_t *cache, const float *scores, con
     const cudaError_t e = lssar::launch_paged_evict(a, ws, stream);
     if (cudaFreeAsync(ws, stream) != cudaSuccess) return LSSAR_ERR_CUDA;
     return e == cudaSuccess ? LSSAR_OK : LSSAR_ERR_CUDA;
+}
+
+int lssar_paged_append_rope(const lssar_paged_cache_t *cache, const void *q, const long long *q_strides, void *q_out,
+                            int H, const void *k_new, const long long *k_strides, const void *v_new,
+                            const long long *v_strides, int n, const lssar_rotary_t *rotary, const int *counts,
+                            const int *first_positions, float *scores, int *positions, int *lens_out,
+                            cudaStream_t stream) {
+    lssar::PagedAppendRope r = {};
+    lssar::PagedAppend &a = r.a;
+    int st = check_cache(cache, &a.c);
+    if (st != LSSAR_OK) return st;
+    if (!lens_out || !q_strides || !k_strides || !v_strides || (n != 0 && (!q || !q_out || !k_new || !v_new))) return LSSAR_ERR_NULL;
+    if (n < 0 || n > (1 << 24) || H < 1 || H > (1 << 24) || (unsigned long long)a.c.B * a.c.Hkv * n > (1ULL << 31) ||
+        (unsigned long long)a.c.B * H * n > (1ULL << 31))
+        return LSSAR_ERR_SHAPE;
+    if ((st = lssar::rotary_table(rotary, a.c.d, &r.table)) != LSSAR_OK) return st;
+    Range kr = {}, vr = {}, qr = {}, qo = {};
+    if (n > 0) {
+        if ((st = check_view(k_new, k_strides, a.c.B, a.c.Hkv, n, a.c.d, &kr)) != LSSAR_OK) return st;
+        if ((st = check_view(v_new, v_strides, a.c.B, a.c.Hkv, n, a.c.d, &vr)) != LSSAR_OK) return st;
+        if ((st = lssar::rope_view(q, q_strides, q_out, a.c.B, H, n, a.c.d, &r.q, &qr, &qo)) != LSSAR_OK) return st;
+    }
+    for (const void *p : {(const void *)counts, (const void *)first_positions, (const void *)scores,
+                          (const void *)positions, (const void *)lens_out})
+        if (misaligned(p, 4)) return LSSAR_ERR_ALIGN;
+    const size_t slots = (size_t)a.c.B * a.c.Hkv * a.c.capacity() * 4, seqs = (size_t)a.c.B * 4;
+    const Range sc = {scores, slots}, po = {positions, slots}, lo = {lens_out, seqs};
+    const Range cn = {counts, seqs}, fi = {first_positions, seqs};
+    const bool in_place = q == q_out;
+    if (any_alias(a.c, {sc, po, lo}, {kr, vr, cn, fi, qr}) || any_alias(a.c, {sc, po, lo, qo}, {cn, fi})) return LSSAR_ERR_ALIAS;
+    if (!in_place && overlap(qo, qr)) return LSSAR_ERR_ALIAS;
+    if (overlap(qo, kr) && !(in_place && lssar::slices_apart(q_strides, q, H, k_strides, k_new, a.c.Hkv, a.c.B, n, a.c.d))) return LSSAR_ERR_ALIAS;
+    if (overlap(qo, vr) && !(in_place && lssar::slices_apart(q_strides, q, H, v_strides, v_new, a.c.Hkv, a.c.B, n, a.c.d))) return LSSAR_ERR_ALIAS;
+    for (const Range &x : {kr, vr, cn, fi, qr})
+        if (overlap(x, {a.c.k, page_bytes(a.c)}) || overlap(x, {a.c.v, page_bytes(a.c)})) return LSSAR_ERR_ALIAS;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    for (int i = 0; i < 3; ++i) {
+        a.ks[i] = k_strides[i];
+        a.vs[i] = v_strides[i];
+    }
+    r.q.H = H;
+    a.n = n;
+    a.counts = counts;
+    a.first = first_positions;
+    a.scores = scores;
+    a.positions = positions;
+    a.lens_out = lens_out;
+    return lssar::launch_paged_append_rope(r, stream) == cudaSuccess ? LSSAR_OK : LSSAR_ERR_CUDA;
+}
+
+int lssar_paged_attend(const lssar_paged_cache_t *cache, const void *q, const long long *q_strides, void *out, int H,
+                       int n, const int *counts, int p, int mode, cudaStream_t stream) {
+    lssar::PagedAttend a = {};
+    int st = check_cache(cache, &a.c);
+    if (st != LSSAR_OK) return st;
+    if (!q || !q_strides || !out) return LSSAR_ERR_NULL;
+    if (mode < LSSAR_MODE_SOFTMAX || mode > LSSAR_MODE_SIGMOID_RW) return LSSAR_ERR_MODE;
+    if (H < 1 || H % a.c.Hkv || H / a.c.Hkv > 128 || n < 1 || n > (1 << 24) ||
+        (unsigned long long)a.c.B * H * n > (1ULL << 31))
+        return LSSAR_ERR_SHAPE;
+    const bool reweight = lssar::is_reweight(mode);
+    if (reweight && (p < 1 || p > 1024)) return LSSAR_ERR_P;
+    Range qr;
+    if ((st = check_view(q, q_strides, a.c.B, H, n, a.c.d, &qr)) != LSSAR_OK) return st;
+    if (misaligned(out, 16) || misaligned(counts, 4)) return LSSAR_ERR_ALIGN;
+    const Range orow = {out, (size_t)a.c.B * H * n * a.c.d * 2}, cn = {counts, (size_t)a.c.B * 4};
+    if (any_alias(a.c, {orow}, {qr, cn})) return LSSAR_ERR_ALIAS;
+    a.q = q;
+    for (int i = 0; i < 3; ++i) a.qs[i] = q_strides[i];
+    a.out = out;
+    a.counts = counts;
+    a.H = H;
+    a.n = n;
+    a.p = reweight ? p : 1;
+    a.mode = mode;
+    int sms = 0;
+    if (lssar::device_sms(&sms) != cudaSuccess) return LSSAR_ERR_CUDA;
+    void *ws = nullptr;
+    const size_t bytes = lssar::paged_attend_workspace_bytes(a, sms);
+    if (bytes && lssar::scratch_alloc(&ws, bytes, stream) != cudaSuccess) return LSSAR_ERR_CUDA;
+    const cudaError_t e = lssar::launch_paged_attend(a, ws, sms, stream);
+    if (ws && cudaFreeAsync(ws, stream) != cudaSuccess) return LSSAR_ERR_CUDA;
+    return e == cudaSuccess ? LSSAR_OK : LSSAR_ERR_CUDA;
+}
+
+// Sizes and pointers that reserve and release share.
+static int check_pages(const lssar::PagedPages &a, bool reserve) {
+    if (!a.table || !a.lens || (!reserve && !a.other) || !a.free_pages || !a.free_count || !a.free_out || (reserve && !a.counts_out))
+        return LSSAR_ERR_NULL;
+    if (a.B < 1 || a.B > (1 << 24) || a.max_pages < 1) return LSSAR_ERR_SHAPE;
+    if (a.page_size < 8 || a.page_size > lssar::kMaxPageSize || a.page_size % 8 || a.n_pages < 1) return LSSAR_ERR_PAGE;
+    if ((unsigned long long)a.max_pages * a.page_size > (1ULL << 24)) return LSSAR_ERR_SHAPE;
+    for (const void *p : {(const void *)a.table, (const void *)a.lens, (const void *)a.other, (const void *)a.free_pages,
+                          (const void *)a.free_count, (const void *)a.counts_out, (const void *)a.free_out})
+        if (misaligned(p, 4)) return LSSAR_ERR_ALIGN;
+    const size_t seqs = (size_t)a.B * 4;
+    const Range table = {a.table, seqs * a.max_pages}, list = {a.free_pages, (size_t)a.n_pages * 4}, count = {a.free_count, 4};
+    const Range lens = {a.lens, seqs}, other = {a.other, seqs}, counts_out = {a.counts_out, seqs}, free_out = {a.free_out, 4};
+    const Range written[3] = {reserve ? table : list, counts_out, free_out}, read[4] = {reserve ? list : table, count, lens, other};
+    for (int i = 0; i < 3; ++i) {
+        for (const Range &x : read)
+            if (overlap(written[i], x)) return LSSAR_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlap(written[i], written[j])) return LSSAR_ERR_ALIAS;
+    }
+    return LSSAR_OK;
+}
+
+int lssar_paged_reserve(int *table, int max_pages, int page_size, const int *lens, const int *counts, int B,
+                        const int *free_pages, int n_pages, const int *free_count, int *counts_out, int *free_out,
+                        cudaStream_t stream) {
+    const lssar::PagedPages a = {table, lens, counts, const_cast<int *>(free_pages), free_count, counts_out, free_out,
+                                 B, max_pages, page_size, n_pages, nullptr};
+    const int st = check_pages(a, true);
+    if (st != LSSAR_OK) return st;
+    return lssar::launch_paged_reserve(a, stream) == cudaSuccess ? LSSAR_OK : LSSAR_ERR_CUDA;
+}
+
+int lssar_paged_release(const int *table, int max_pages, int page_size, const int *lens, const int *lens_new, int B,
+                        int *free_pages, int n_pages, const int *free_count, int *free_out, cudaStream_t stream) {
+    const lssar::PagedPages a = {const_cast<int *>(table), lens, lens_new, free_pages, free_count, nullptr, free_out,
+                                 B, max_pages, page_size, n_pages, nullptr};
+    const int st = check_pages(a, false);
+    if (st != LSSAR_OK) return st;
+    return lssar::launch_paged_release(a, stream) == cudaSuccess ? LSSAR_OK : LSSAR_ERR_CUDA;
 }
 
 }  // extern "C"
