@@ -344,8 +344,8 @@ int lssar_paged_evict(const lssar_paged_cache_t *cache, const float *scores, con
  *   out : [B, H, n, d] contiguous, of the cache's type.  Rows t >= counts[b] are
  *         not written.
  * A bad length or count (code 51) gives NaN in all n rows of that sequence, a bad
- * page number among the pages in use (code 52) in its rows t < counts[b].  What
- * the rows of pages past lens[b] hold does not matter.
+ * page number among the pages in use (code 52) in the rows that attend to one of
+ * that page's slots.  What the rows of pages past lens[b] hold does not matter.
  * A value that is infinite or NaN among the cached tokens reaches the rows of
  * the chunk that attend to it, and may reach rows up to 383 slots before it.
  * The sums have a fixed order: the same call on the same device gives the same

@@ -69,6 +69,8 @@ struct PagedAttend {
     const int *counts;        // [B] or null
     int H, n, p, mode;
 };
+// Upper bound of the tiles that a call numbers (ints).
+long long paged_attend_tiles(const PagedAttend &pr);
 size_t paged_attend_workspace_bytes(const PagedAttend &pr, int sms);
 cudaError_t launch_paged_attend(const PagedAttend &pr, void *ws, int sms, cudaStream_t stream);
 

@@ -190,14 +190,16 @@ int lssar_paged_attend(const lssar_paged_cache_t *cache, const void *q, const lo
     Range qr;
     if ((st = check_view(q, q_strides, a.c.B, H, n, a.c.d, &qr)) != LSSAR_OK) return st;
     if (misaligned(out, 16) || misaligned(counts, 4)) return LSSAR_ERR_ALIGN;
+    a.H = H;
+    a.n = n;
+    // (tile numbers are ints, and the CTAs' first tiles reach up to one CTA's count past the last)
+    if (lssar::paged_attend_tiles(a) > 0x7fff0000LL) return LSSAR_ERR_SHAPE;
     const Range orow = {out, (size_t)a.c.B * H * n * a.c.d * 2}, cn = {counts, (size_t)a.c.B * 4};
     if (any_alias(a.c, {orow}, {qr, cn})) return LSSAR_ERR_ALIAS;
     a.q = q;
     for (int i = 0; i < 3; ++i) a.qs[i] = q_strides[i];
     a.out = out;
     a.counts = counts;
-    a.H = H;
-    a.n = n;
     a.p = reweight ? p : 1;
     a.mode = mode;
     int sms = 0;

@@ -1,133 +1,82 @@
-// Paged cache, attention of a chunk: row t < counts[b] of a sequence is row
-// i = lens[b] - counts[b] + t + 1 of the attention, in every mode.
-//
-// One warp per row: a pass over the row's keys for the maximum of the scores z and the sum
-// of the normaliser phi, a second for the weights (lanes over keys) and the values (lanes
-// over columns).  Everything in fp32 from the inputs' own bits.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "paged.cuh"
-#include "row_weights.cuh"
-#include "tc_host.cuh"
+// Host side of the chunk attention: the split, the scratch layout and the launches.
+#include "paged_attend.cuh"
 
 namespace lssar {
 namespace {
 
-constexpr int kWarps = 4;
+struct Layout {
+    int G, tokens, ctas, rows, cap128;
+    size_t entries, first, knorm, qscale, stats, sums, o, total;   // the header first
+};
 
-__device__ __forceinline__ float2 pair_of(uint32_t x, bool half) {
-    if (half) return __half22float2(*reinterpret_cast<const __half2 *>(&x));
-    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-}
-
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) attend_rows(const __grid_constant__ PagedAttend a, float scale) {
-    __shared__ float qs[kWarps][D];
-    const PagedCache &c = a.c;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = a.H / c.Hkv;
-    const long long rows = (long long)c.B * a.H * a.n;
-#pragma unroll 1
-    for (long long r = (long long)blockIdx.x * kWarps + warp; r < rows; r += (long long)gridDim.x * kWarps) {
-        const int t = (int)(r % a.n), hq = (int)(r / a.n % a.H), b = (int)(r / a.n / a.H), h = hq / G;
-        const int len = c.lens[b], cnt = a.counts ? a.counts[b] : a.n;
-        bool bad = len < 0 || len > c.capacity() || cnt < 0 || cnt > a.n || cnt > len;
-        if (bad) atomicCAS(c.err, 0u, (unsigned)kErrPagedLength);
-        if (!bad && t >= cnt) continue;
-        const int *table = c.table + (size_t)b * c.max_pages;
-        bool no_page = false;
-        for (int i = lane; !bad && i * c.page_size < len; i += 32) no_page |= (unsigned)table[i] >= (unsigned)c.n_pages;
-        if (no_page) atomicCAS(c.err, 0u, (unsigned)kErrPagedPage);
-        bad |= __any_sync(0xffffffffu, no_page);
-        uint16_t *out = static_cast<uint16_t *>(a.out) + (size_t)r * D;
-        if (bad) {
-            for (int x = lane; x < D; x += 32) out[x] = 0x7fff;   // a NaN in both types
-            continue;
-        }
-        const uint16_t *q = static_cast<const uint16_t *>(a.q) + b * a.qs[0] + hq * a.qs[1] + t * a.qs[2];
-        float qq = 0.f;
-        __syncwarp();
-        for (int x = lane; x < D / 2; x += 32) {
-            const float2 v = pair_of(reinterpret_cast<const uint32_t *>(q)[x], c.half);
-            qs[warp][2 * x] = v.x;
-            qs[warp][2 * x + 1] = v.y;
-            qq += v.x * v.x + v.y * v.y;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) qq += __shfl_xor_sync(0xffffffffu, qq, o);
-        __syncwarp();
-        const int n = len - cnt + t + 1;
-        const bool raw = !uses_normalised_qk(a.mode);
-        const float f = raw ? scale : scale * logf((float)n) / fmaxf(sqrtf(qq), 1e-12f);
-        auto at = [&](int j) { return table[j / c.page_size] * c.page_stride + ((size_t)h * c.page_size + j % c.page_size) * D; };
-        auto score = [&](int j) {
-            const uint32_t *k = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(c.k) + at(j));
-            float dot = 0.f, kk = 0.f;
-#pragma unroll 8
-            for (int x = 0; x < D / 2; ++x) {
-                const float2 v = pair_of(k[x], c.half);
-                dot += qs[warp][2 * x] * v.x + qs[warp][2 * x + 1] * v.y;
-                kk += v.x * v.x + v.y * v.y;
-            }
-            return raw ? dot * f : dot * f / fmaxf(sqrtf(kk), 1e-12f);
-        };
-        float2 st = make_float2(-3e38f, 0.f);
-        for (int j = lane; j < n; j += 32) {
-            const float z = score(j), m = fmaxf(st.x, z);
-            st.y = raw ? st.y * exp2f(st.x - m) + exp2f(z - m) : st.y + phi(a.mode, z, 0.f);
-            st.x = m;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, st.x, o), s2 = __shfl_xor_sync(0xffffffffu, st.y, o), m = fmaxf(st.x, m2);
-            st = make_float2(m, raw ? st.y * exp2f(st.x - m) + s2 * exp2f(m2 - m) : st.y + s2);
-        }
-        const RowConstants rc = row_constants(a.mode, n, st);
-        const float lift = exp2f(-fminf(st.x, 0.f));
-        float sum = 0.f, acc[D / 32] = {};
-        for (int j0 = 0; j0 < n; j0 += 32) {
-            float w = 0.f;
-            if (j0 + lane < n) {
-                const float z = score(j0 + lane);
-                w = is_reweight(a.mode) ? powi(above_offset(a.mode, make_float2(z, z), rc), a.p).x
-                    : raw               ? exp2f(z - st.x)
-                                        : phi(a.mode, z, 0.f) * lift;
-            }
-            sum += w;
-            for (int j = 0; j < min(32, n - j0); ++j) {
-                const float wj = __shfl_sync(0xffffffffu, w, j);
-                const uint16_t *v = static_cast<const uint16_t *>(c.v) + at(j0 + j);
-#pragma unroll
-                for (int x = 0; x < D / 64; ++x) {
-                    const float2 e = pair_of(reinterpret_cast<const uint32_t *>(v)[x * 32 + lane], c.half);
-                    acc[2 * x] += wj * e.x;
-                    acc[2 * x + 1] += wj * e.y;
-                }
-            }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float inv = 1.f / sum;
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-            reinterpret_cast<uint32_t *>(out)[x * 32 + lane] =
-                c.half ? ptx::pack_f16x2(acc[2 * x] * inv, acc[2 * x + 1] * inv) : ptx::pack_bf16x2(acc[2 * x] * inv, acc[2 * x + 1] * inv);
-    }
+Layout layout(const PagedAttend &pr, int sms) {
+    const PagedCache &c = pr.c;
+    Layout l;
+    l.G = pr.H / c.Hkv;
+    l.tokens = attend::kPairRows / l.G;
+    l.rows = (pr.n < l.tokens ? pr.n : l.tokens) * l.G;
+    l.cap128 = (c.capacity() + attend::kKeys - 1) / attend::kKeys * attend::kKeys;
+    const size_t pairs = (size_t)c.B * ((pr.n + l.tokens - 1) / l.tokens), items = pairs * c.Hkv, tiles = items * (l.cap128 / attend::kKeys);
+    l.ctas = (int)(tiles < (size_t)sms ? tiles : sms);
+    const bool norms = uses_normalised_qk(pr.mode), reweight = is_reweight(pr.mode);
+    auto r = [](size_t x) { return (x + 255) & ~(size_t)255; };
+    l.entries = 256;
+    l.first = l.entries + r(pairs * sizeof(int4));
+    l.knorm = l.first + r((size_t)l.ctas * 4);
+    l.qscale = l.knorm + (norms ? r((size_t)c.B * c.Hkv * l.cap128 * 4) : 0);
+    l.stats = l.qscale + (norms ? r((size_t)c.B * pr.H * pr.n * 4) : 0);
+    l.sums = l.stats + (reweight ? r((items + l.ctas) * l.rows * 8) : 0);
+    l.o = l.sums + r((size_t)2 * l.ctas * l.rows * 8);
+    l.total = l.o + r((size_t)2 * l.ctas * l.rows * c.d * 4);
+    return l;
 }
 
 }  // namespace
 
-size_t paged_attend_workspace_bytes(const PagedAttend &, int) { return 0; }
+long long paged_attend_tiles(const PagedAttend &pr) {
+    const long long tokens = attend::kPairRows / (pr.H / pr.c.Hkv), pairs = (pr.n + tokens - 1) / tokens;
+    const long long tiles = (pr.c.capacity() + 63) / 64;      // (the prologue's tiles may be of 64 keys)
+    return (long long)pr.c.B * pr.c.Hkv * pairs > (1LL << 31) ? 1LL << 62 : (long long)pr.c.B * pr.c.Hkv * pairs * tiles;
+}
 
-cudaError_t launch_paged_attend(const PagedAttend &pr, void *, int sms, cudaStream_t stream) {
-    PagedAttend a = pr;
-    const cudaError_t e = error_word_ptr(&a.c.err);
+size_t paged_attend_workspace_bytes(const PagedAttend &pr, int sms) { return layout(pr, sms).total; }
+
+cudaError_t launch_paged_attend(const PagedAttend &pr, void *ws, int sms, cudaStream_t stream) {
+    attend::Args g;
+    g.a = pr;
+    const cudaError_t e = error_word_ptr(&g.a.c.err);
     if (e != cudaSuccess) return e;
-    const float scale = uses_normalised_qk(a.mode) ? score_qmul(a.c.d) : 1.4426950408889634f / sqrtf((float)a.c.d);
-    const long long rows = ((long long)a.c.B * a.H * a.n + kWarps - 1) / kWarps, most = 16LL * sms;
-    if (a.c.d == 64) attend_rows<64><<<(unsigned)(rows < most ? rows : most), kWarps * 32, 0, stream>>>(a, scale);
-    else attend_rows<128><<<(unsigned)(rows < most ? rows : most), kWarps * 32, 0, stream>>>(a, scale);
-    return cudaGetLastError();
+    const PagedCache &c = pr.c;
+    const Layout l = layout(pr, sms);
+    char *base = static_cast<char *>(ws);
+    g.s.head = reinterpret_cast<attend::Header *>(base);
+    g.s.entries = reinterpret_cast<int4 *>(base + l.entries);
+    g.s.first = reinterpret_cast<int *>(base + l.first);
+    g.s.knorm = reinterpret_cast<float *>(base + l.knorm);
+    g.s.qscale = reinterpret_cast<float *>(base + l.qscale);
+    g.s.stats = reinterpret_cast<float2 *>(base + l.stats);
+    g.s.sums = reinterpret_cast<float2 *>(base + l.sums);
+    g.s.o = reinterpret_cast<float *>(base + l.o);
+    g.G = l.G;
+    g.tokens = l.tokens;
+    g.ctas = l.ctas;
+    g.rows = l.rows;
+    g.cap128 = l.cap128;
+    // a copy takes the rows of one page that lie in one tile: the largest power
+    // of two that divides the page size, so that no copy crosses either border
+    const int low = c.page_size & -c.page_size;
+    g.piece_rows = low < attend::kKeys ? low : attend::kKeys;
+    g.scale = !uses_normalised_qk(pr.mode) ? 1.4426950408889634f / sqrtf((float)c.d) : (pr.mode == kSigmoidRw ? -1.f : 1.f) * score_qmul(c.d);
+    g.idesc_s = ptx::idesc_f16(!c.half, attend::kTileRows, attend::kKeys, false, false);
+    g.idesc_pv = ptx::idesc_f16(!c.half, attend::kTileRows, c.d, false, true);
+    CUtensorMap km, vm;
+    if (!make_page_map(&km, c.k, c.half, c.d, c.Hkv * c.page_size, c.n_pages, c.page_stride, g.piece_rows) ||
+        !make_page_map(&vm, c.v, c.half, c.d, c.Hkv * c.page_size, c.n_pages, c.page_stride, g.piece_rows))
+        return cudaErrorInvalidValue;
+    using namespace attend;
+    Launch *const launch[5][2] = {{softmax_d64, softmax_d128}, {lssa_d64, lssa_d128}, {lssar_d64, lssar_d128},
+                                  {softmax_rw_d64, softmax_rw_d128}, {sigmoid_rw_d64, sigmoid_rw_d128}};
+    return launch[pr.mode][c.d == 128](km, vm, g, sms, stream);
 }
 
 }  // namespace lssar

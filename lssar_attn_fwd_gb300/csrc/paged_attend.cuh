@@ -1,0 +1,1347 @@
+// Paged cache, attention of a chunk: the last counts[b] rows of the attention over the
+// lens[b] cached tokens of each sequence, in every mode, grouped heads.
+//
+// Mathematics, for row i (tokens it attends to) and key j < i, in log2 units:
+//   z = log2e / sqrt(d) q.k  (softmax modes)  or  log2e ln d ln i q.k / (|q| |k|);
+//   phi(z) = 2^(z - m), log2(1 + 2^z) or 1 / (1 + 2^-z);  S1 = sum phi, m = max z;
+//   w = phi, or re-weighted max(kappa (phi - theta), 0)^p, theta = O S1 / i,
+//   kappa = 1 / (phi(m) - theta);  out = sum w v / sum w.
+// Scores are products of the inputs' own bits, scaled in fp32 afterwards: 1/|k| of each cached
+// key and the factor of each query row come from a prologue that reads both once.
+//
+// What bounds it: the score warps.  Each score costs about 10 issue slots in the
+// re-weighting modes (two passes), against 4d flops of tensor work and, at 256 rows per
+// key, 4d / 256 bytes.
+//
+// Split.  A work item is a pair of 128-row tiles of the rows (token, head of the group) of one
+// key head: floor(256 / G) tokens.  Its K tiles of 128 keys are numbered through (sequence, pair,
+// key head, tile); each CTA takes an equal run of them wherever items begin or end, as in
+// the decode step, so that chunks and contexts of any mix load the SMs evenly.  The part of an
+// item in one run is a segment.  The numbering needs the lengths, which are on the device:
+//   attend_prepare   plans it (one block), while the other blocks work out the norms;
+//   attend<kStats>   re-weighting modes: scores -> (m, S1) of each segment's rows;
+//   attend<kValues>  row constants from all of the item's segments, scores again,
+//                    weights, sum of w v; writes the rows of whole items;
+//   attend_join      adds the segments of the items that lie in several runs.
+// Each is a programmatic dependent of the one before it.
+//
+// Structure of attend (640 threads): warp 0 the TMA producer of K, V (a piece of a page at a
+// time) and key norms; warps 1, 2 issue the tcgen05.mma of one tile each; warp 3 gathers the rows of q
+// (any strides, any group); four warpgroups of score warps, two per tile, each half of its
+// columns: thread = row (TMEM lane).  Warps whose 32 rows hold none of the item's skip the arithmetic.
+// TMEM (512 columns): kStats: S of tile w, two buffers each, at 256 w + 128 buffer.  kValues: S_w at
+// 128 w; d = 64: P_w at 256 + 64 w, O_w at 384 + 64 w; d = 128: P_w over S_w, O_w at 256 + 128 w.
+#pragma once
+
+#include <cstddef>
+
+#include "paged_decode.cuh"
+#include "tc_kernel.cuh"
+
+namespace lssar {
+namespace attend {
+
+using tc::max3;
+using tc::min3;
+
+enum Phase : int { kStats = 0, kValues = 1 };
+
+constexpr int kTileRows = 128;
+constexpr int kPairRows = 256;
+constexpr int kKeys = 128;                    // keys per tile
+constexpr int kThreads = 640;
+constexpr int kScoreWarp0 = 4;
+// Registers: the control warpgroup gives some back, the score warpgroups take them
+// (128 x 64 + 512 x 104 = 640 x 96).
+constexpr int kLaunchRegs = 96, kCtrlRegs = 64, kScoreRegs = 104;
+static_assert(128 * kCtrlRegs + 512 * kScoreRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kInfo = 4;                      // tiles whose key norms are in shared memory
+constexpr int kItems = 4;                     // depth of the queue of segments
+constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr float kLowest = -3.0e38f;           // below every score, and finite
+enum : unsigned { kErrItem = 61, kErrQ, kErrKvFull, kErrKvEmpty, kErrSFull, kErrSFree, kErrPFull, kErrPFree, kErrOFull, kErrOFree,
+                  kErrInfo, kErrHalves, kErrTileMax, kErrDrain };
+
+// One-pass modes: log2 of the largest weight of a row lies in kRoom + [0, kLag] (fp16, whose
+// least step is 2^-24, needs the room; softplus up to 117 leaves less of it).
+template <int MODE, bool HALF>
+struct Range16 {
+    static constexpr float kRoom = !HALF ? 0.f : MODE == kSoftmax ? 13.f : 8.f;
+    static constexpr float kLag = !HALF ? 8.f : MODE == kSoftmax ? 2.f : 6.f;
+};
+constexpr float kTopFp16 = 32768.f;           // re-weighting: the largest weight in fp16
+constexpr float kNoLift = -118.f;             // LSSA: below every score
+
+struct Header {
+    int total, entries, run;                  // tiles, entries, tiles per CTA
+};
+
+struct Scratch {
+    Header *head;
+    int4 *entries;        // {sequence, pair, tiles of the pair, number of its first tile}
+    int *first;           // [ctas] entry of each CTA's first tile
+    float *knorm;         // [B, Hkv, cap128] 1 / |k|
+    float *qscale;        // [B, H, n] factor of a query row's scores
+    float2 *stats;        // [item + cta][rows]: m, S1 of a segment's rows
+    float2 *sums;         // [2 cta + last][rows]: reference, sum of w
+    float *o;             // [2 cta + last][rows][d]: sum of w v
+};
+
+struct Args {
+    PagedAttend a;
+    Scratch s;
+    int G, tokens;        // H / Hkv, tokens per pair
+    int ctas, rows;       // rows that a segment's scratch holds
+    int cap128;           // capacity, a multiple of 128
+    int piece_rows;       // rows of a page per copy
+    float scale;          // log2e / sqrt(d), or +-log2e ln d
+    uint32_t idesc_s, idesc_pv;
+};
+
+// A segment as the roles of a CTA see it.
+struct Item {
+    int b, h, t0, rows;   // first token, valid rows of the pair
+    int base, len;        // slots before the chunk, cached tokens
+    int nk, kt0, kt1;     // tiles of the item; those of this segment
+    int item, start;      // number of the item, of its first tile
+    int first_bad;        // first slot of a page that is none
+};
+
+struct __align__(16) Shared {
+    float knorm[kInfo][kKeys];
+    float m[2][2][2][kTileRows], s[2][2][2][kTileRows];   // [segment parity][tile][half][row]
+    float tmax[2][2][2][kTileRows];                       // [step parity][tile][half][row]
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2][2], s_free[2][2];                  // [tile][buffer]
+    uint64_t p_full[2], p_free[2], o_full[2], o_free[2], halves[2];
+    uint64_t tile_max[2][4];
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t info_full[kInfo], info_empty[kInfo];
+    uint64_t item_full[kItems], item_empty[kItems];
+    Item items[kItems];
+    unsigned absent[8];   // per stage of V: groups of 8 rows that no copy has filled
+    uint32_t tmem;
+    int abort_flag;
+};
+
+template <int D>
+struct Cfg {
+    static constexpr int kTile = kTileRows * D * 2;      // bytes of a tile of q, k or v
+    static constexpr int kStages = D == 64 ? 8 : 4;
+    static constexpr int kQBufs = D == 64 ? 2 : 1;
+    static constexpr int kRing = kQBufs * 2 * kTile;
+    static constexpr int kShared = kRing + kStages * kTile;
+    static constexpr int kSmem = kShared + (int)sizeof(Shared) + 1024;
+};
+static_assert(Cfg<64>::kSmem <= 232448 && Cfg<128>::kSmem <= 232448, "shared memory");
+
+// Tiles of a pair that starts at token t0, of a sequence with `count` new tokens after `base`.
+__host__ __device__ __forceinline__ int tiles_of_pair(int base, int count, int t0, int tokens) {
+    const int last = t0 + tokens < count ? t0 + tokens : count;     // tokens up to the pair's end
+    return (base + last + kKeys - 1) / kKeys;
+}
+
+// ---------------------------------------------------------------- prologue
+
+constexpr int kPrepThreads = 256;
+
+// Exclusive prefix over the block of two values; the totals in t0, t1.
+__device__ __forceinline__ void block_prefix(long long &x, long long &y, long long &tx, long long &ty, long long (*part)[2]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long ix = x, iy = y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long ax = __shfl_up_sync(0xffffffffu, ix, o), ay = __shfl_up_sync(0xffffffffu, iy, o);
+        if (lane >= o) {
+            ix += ax;
+            iy += ay;
+        }
+    }
+    __syncthreads();
+    if (lane == 31) {
+        part[warp][0] = ix;
+        part[warp][1] = iy;
+    }
+    __syncthreads();
+    tx = ty = 0;
+    x = ix - x;
+    y = iy - y;
+#pragma unroll
+    for (int w = 0; w < kPrepThreads / 32; ++w) {
+        if (w < warp) {
+            x += part[w][0];
+            y += part[w][1];
+        }
+        tx += part[w][0];
+        ty += part[w][1];
+    }
+}
+
+// The plan (one block): entries in the order of (sequence, pair), and each CTA's first one.
+static __device__ __noinline__ void make_plan(const Args &g) {
+    __shared__ long long part[kPrepThreads / 32][2];
+    __shared__ int bad[kPrepThreads];
+    const PagedAttend &a = g.a;
+    const PagedCache &c = a.c;
+    long long entries = 0, tiles = 0;
+#pragma unroll 1
+    for (int base = 0; base < c.B; base += kPrepThreads) {
+        const int b = base + threadIdx.x;
+        int len = 0, cnt = 0;
+        bool ok = true;
+        if (b < c.B) {
+            len = c.lens[b];
+            cnt = a.counts ? a.counts[b] : a.n;
+            ok = len >= 0 && len <= c.capacity() && cnt >= 0 && cnt <= a.n && cnt <= len;
+            if (!ok) {
+                atomicCAS(c.err, 0u, (unsigned)kErrPagedLength);
+                cnt = 0;
+            }
+        }
+        const int pairs = (cnt + g.tokens - 1) / g.tokens;
+        long long mine = 0;
+#pragma unroll 1
+        for (int m = 0; m < pairs; ++m) mine += tiles_of_pair(len - cnt, cnt, m * g.tokens, g.tokens);
+        long long e = pairs, t = mine * c.Hkv, te, tt;
+        block_prefix(e, t, te, tt, part);
+        e += entries;
+        t += tiles;
+#pragma unroll 1
+        for (int m = 0; m < pairs; ++m) {
+            const int nk = tiles_of_pair(len - cnt, cnt, m * g.tokens, g.tokens);
+            g.s.entries[e++] = make_int4(b, m, nk, (int)t);
+            t += (long long)nk * c.Hkv;
+        }
+        entries += te;
+        tiles += tt;
+        // rows of a sequence that must not be used
+        bad[threadIdx.x] = !ok;
+        if (__syncthreads_or(!ok)) {
+#pragma unroll 1
+            for (int i = 0; i < min(kPrepThreads, c.B - base); ++i) {
+                if (!bad[i]) continue;
+                uint4 *row = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (size_t)(base + i) * a.H * a.n * c.d);
+                const size_t pieces = (size_t)a.H * a.n * c.d / 8;
+                for (size_t x = threadIdx.x; x < pieces; x += kPrepThreads) row[x] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            }
+        }
+    }
+    __syncthreads();
+    const int run = max(1, (int)((tiles + g.ctas - 1) / g.ctas));
+    if (threadIdx.x == 0) *g.s.head = Header{(int)tiles, (int)entries, run};
+    for (int cta = threadIdx.x; cta < g.ctas; cta += kPrepThreads) {
+        const long long t = (long long)cta * run;
+        if (t >= tiles) break;
+        int lo = 0, hi = (int)entries - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (g.s.entries[mid].w <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        g.s.first[cta] = lo;
+    }
+}
+
+// Sum of squares of 8 elements.
+__device__ __forceinline__ float squares(uint4 x, bool half) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = half ? __half22float2(*reinterpret_cast<const __half2 *>(&u[i]))
+                              : make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+        s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
+    }
+    return s;
+}
+
+// Block 0 plans; the others, in the normalised modes, take runs of key rows (1 / |k|) and of query
+// rows (factor of the row's scores).  2d bytes of each are read once, by d / 8 lanes a row.
+template <int D>
+__global__ void __launch_bounds__(kPrepThreads) attend_prepare(const __grid_constant__ Args g, int norms) {
+    ptx::launch_dependents();
+    if (blockIdx.x == 0) {
+        make_plan(g);
+        return;
+    }
+    if (!norms) return;
+    const PagedAttend &a = g.a;
+    const PagedCache &c = a.c;
+    constexpr int kLanes = D / 8, kRows = kPrepThreads / kLanes, kTile = paged::tile_keys(D);
+    const int part = threadIdx.x % kLanes, in = threadIdx.x / kLanes, blocks = gridDim.x - 1, blk = blockIdx.x - 1;
+    // keys
+    const int tiles = paged::tiles_before<D>(c, c.B) * c.Hkv, run = (tiles + blocks - 1) / blocks;
+    const int t0 = blk * run, t1 = min(tiles, t0 + run);
+    if (t0 < t1) {
+        paged::Place p = paged::locate<D>(c, 1, t0);
+#pragma unroll 1
+        for (int t = t0; t < t1; ++t) {
+            uint4 x[kTile / kRows];
+#pragma unroll
+            for (int e = 0; e < kTile / kRows; ++e) {
+                const int slot = p.tile * kTile + e * kRows + in, i = slot / c.page_size;
+                const int pg = slot < p.n ? c.table[(size_t)p.b * c.max_pages + i] : -1;
+                x[e] = make_uint4(0, 0, 0, 0);
+                if ((unsigned)pg < (unsigned)c.n_pages)
+                    x[e] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(c.k) + pg * c.page_stride +
+                                                            ((size_t)p.h * c.page_size + slot - i * c.page_size) * D + part * 8);
+            }
+#pragma unroll
+            for (int e = 0; e < kTile / kRows; ++e) {
+                float s = squares(x[e], c.half);
+#pragma unroll
+                for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                const int slot = p.tile * kTile + e * kRows + in;
+                if (part == 0 && slot < p.n) g.s.knorm[((size_t)p.b * c.Hkv + p.h) * g.cap128 + slot] = 1.f / fmaxf(sqrtf(s), 1e-12f);
+            }
+            if (++p.tile == p.nt && t + 1 < t1) paged::next_row<D>(c, 1, p);
+        }
+    }
+    // queries
+    const long long rows = (long long)c.B * a.H * a.n;
+#pragma unroll 1
+    for (long long r = (long long)blk * kRows + in; r - in < rows; r += (long long)blocks * kRows) {
+        float s = 0.f, f = 0.f;
+        if (r < rows) {
+            const int t = (int)(r % a.n), hq = (int)(r / a.n % a.H), b = (int)(r / a.n / a.H);
+            const int cnt = a.counts ? a.counts[b] : a.n;
+            if (t < cnt && t < a.n) {
+                s = squares(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + b * a.qs[0] + hq * a.qs[1] + t * a.qs[2] + part * 8), c.half);
+                f = g.scale * logf((float)(c.lens[b] - cnt + t + 1));
+            }
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (part == 0 && r < rows) g.s.qscale[r] = f / fmaxf(sqrtf(s), 1e-12f);
+    }
+}
+
+// ---------------------------------------------------------------- scores
+
+// A row's state; the score scale is negative in the sigmoid mode, whose registers hold -z.
+struct Row {
+    float a;
+    float x;        // softmax: reference of the exponent less the room; LSSA: 2^(room - reference); else lift
+    float ref;      // one pass: the reference
+    float kappa, beta, theta, ck;
+};
+
+// Four key norms of a tile.  Volatile: between the waits and arrivals around it.
+__device__ __forceinline__ float4 load_norms(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// The 32 scores of columns [32 c, 32 c + 32) of a warpgroup's half: products -> z.
+template <bool NORM>
+__device__ __forceinline__ void to_z(uint32_t (&r)[32], uint32_t knorm, float a) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        float2 f0 = make_float2(a, a), f1 = f0;
+        if constexpr (NORM) {
+            const float4 k = load_norms(knorm + j * 4);
+            f0 = __fmul2_rn(make_float2(k.x, k.y), f0);
+            f1 = __fmul2_rn(make_float2(k.z, k.w), f1);
+        }
+        const float2 z0 = __fmul2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), f0);
+        const float2 z1 = __fmul2_rn(make_float2(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3])), f1);
+        r[j] = __float_as_uint(z0.x);
+        r[j + 1] = __float_as_uint(z0.y);
+        r[j + 2] = __float_as_uint(z1.x);
+        r[j + 3] = __float_as_uint(z1.y);
+    }
+}
+
+// Columns past `last` (relative to this chunk) get no weight.
+__device__ __forceinline__ void mask(uint32_t (&r)[32], int last, float masked) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j > last) r[j] = __float_as_uint(masked);
+}
+
+__device__ __forceinline__ float2 pair_at(const uint32_t *r, int j) { return make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])); }
+
+__device__ __forceinline__ float max_of(const uint32_t (&r)[32], float m) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) m = max3(m, __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+    return m;
+}
+
+// sum phi of a chunk, LSSAR: sum max(z, 0) in acc and prod (1 + 2^-|z|) in prod, one special
+// function a score (as the dense forward); or, ACCURATE, where all of a row's scores of the tile are
+// negative, and the product would lose them, softplus itself.
+template <bool ACCURATE>
+__device__ __forceinline__ void softplus_sum(const uint32_t (&r)[32], float2 &acc, float2 &prod) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float2 z = pair_at(r, j);
+        if constexpr (ACCURATE) {
+            acc = __fadd2_rn(acc, softplus2(z));
+        } else {
+            const float2 u = make_float2(ptx::ex2(-fabsf(z.x)), ptx::ex2(-fabsf(z.y)));
+            prod = __ffma2_rn(prod, u, prod);
+            acc = __fadd2_rn(acc, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+        }
+    }
+}
+
+// x[i]^p, 16 values at once.
+__device__ __forceinline__ void powers16(float2 (&x)[8], int p) {
+    if (p == 1) return;
+    float2 r[8];
+    if (p & 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = x[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = make_float2(1.f, 1.f);
+    }
+#pragma unroll 1
+    for (p >>= 1; p; p >>= 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], x[i]);
+        if (p & 1) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = __fmul2_rn(r[i], x[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = r[i];
+}
+
+// How a warp evaluates its weights (a warp-uniform choice).
+enum Form : int {
+    kMixed = 0,      // softplus by logarithms and a polynomial in turn, to about 2^-19 (1 + its value)
+    kOneExp = 1,     // LSSAR rows that meet the bound of fast_weights.cuh
+    kAccurate = 2    // to 2^-18 of its value and evenly: rows whose scores are all negative, or nearly equal;
+                     // softmax: rows whose scores pass 2^16
+};
+
+// Weights of 16 scores (r[0..15]), summed into acc and packed into 8 words.  `pair0`: number of the
+// first pair in its chunk of 32.
+template <int MODE, bool HALF, int FORM>
+__device__ __forceinline__ void weights16(const uint32_t *r, int pair0, const Row &row, int p, float2 &acc, uint32_t *pk) {
+    const auto both = [](float x) { return make_float2(x, x); };
+    float2 w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 z = pair_at(r, 2 * i);
+        if constexpr (MODE == kSoftmax || MODE == kSoftmaxRw) {
+            // (softmax: z holds the product.  Beyond 2^16 its own rounding would pass the room: scaled first)
+            const float2 e = MODE == kSoftmaxRw ? __fadd2_rn(z, both(-row.x))
+                             : FORM == kMixed   ? __ffma2_rn(z, both(row.a), both(-row.x))
+                                                : make_float2(__fmul_rn(z.x, row.a) - row.x, __fmul_rn(z.y, row.a) - row.x);
+            w[i] = make_float2(ptx::ex2(e.x), ptx::ex2(e.y));
+        } else if constexpr (MODE == kSigmoidRw) {   // z holds -z
+            const float2 v = __fadd2_rn(make_float2(ptx::ex2(z.x), ptx::ex2(z.y)), both(1.f));
+            w[i] = make_float2(ptx::rcp(v.x), ptx::rcp(v.y));
+        } else if constexpr (FORM == kAccurate) {
+            w[i] = softplus2(z);
+        } else if constexpr (FORM == kOneExp) {
+            const float2 u = make_float2(ptx::ex2(-fabsf(z.x)), ptx::ex2(-fabsf(z.y)));
+            w[i] = ptx::fma_sat2(u, both(row.ck), __ffma2_rn(z, both(row.kappa), both(row.beta)));
+        } else {
+            w[i] = poly_pair(pair0 + i, 4) ? sp2x2_poly(z) : tc::sp2x2_direct(z);
+        }
+        if constexpr (is_reweight(MODE) && FORM != kOneExp) {
+            // the difference before its scale where it is small against its terms (kAccurate)
+            if constexpr (FORM == kAccurate) {
+                const float2 y = MODE == kSoftmaxRw ? __fadd2_rn(w[i], both(-row.theta)) : __ffma2_rn(w[i], both(row.x), both(-row.theta));
+                w[i] = ptx::fma_sat2(y, both(row.kappa), both(0.f));
+            } else {
+                w[i] = ptx::fma_sat2(w[i], both(row.kappa), both(row.beta));
+            }
+        } else if constexpr (MODE == kLssa && (FORM == kAccurate || HALF)) {
+            w[i] = __fmul2_rn(w[i], both(row.x));
+        }
+    }
+    if constexpr (is_reweight(MODE)) {
+        powers16(w, p);
+        if constexpr (HALF) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __fmul2_rn(w[i], both(kTopFp16));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        acc = __fadd2_rn(acc, w[i]);
+        pk[i] = HALF ? ptx::pack_f16x2(w[i].x, w[i].y) : ptx::pack_bf16x2(w[i].x, w[i].y);
+    }
+}
+
+template <int MODE, bool HALF>
+__device__ __forceinline__ void weights32(const uint32_t (&r)[32], const Row &row, int form, int p, float2 &acc, uint32_t *pk) {
+    if constexpr (MODE == kLssar) {
+        if (form == kOneExp) {
+            weights16<MODE, HALF, kOneExp>(r, 0, row, p, acc, pk);
+            weights16<MODE, HALF, kOneExp>(r + 16, 8, row, p, acc, pk + 8);
+            return;
+        }
+    }
+    if (form == kAccurate) {
+        weights16<MODE, HALF, kAccurate>(r, 0, row, p, acc, pk);
+        weights16<MODE, HALF, kAccurate>(r + 16, 8, row, p, acc, pk + 8);
+        return;
+    }
+    weights16<MODE, HALF, kMixed>(r, 0, row, p, acc, pk);
+    weights16<MODE, HALF, kMixed>(r + 16, 8, row, p, acc, pk + 8);
+}
+
+// Constants of a re-weighted row from its maximum and normaliser sum; returns the form that it
+// needs.  A row is uniform where the largest difference is within 1e-5 of the maximum, as in the
+// decode step.  Its weights: phi 2^126 clamped to 1, which is 1 for every score that is not masked.
+template <int MODE>
+__device__ __forceinline__ int row_constants(Row &row, float m, float s1, int n, int p) {
+    const bool raw = MODE == kSoftmaxRw;
+    const float lift = raw ? 1.f : ptx::ex2(-fminf(m, 0.f));
+    const float theta = n <= 3 ? 0.f : s1 * lift / (float)n;
+    const float top = raw ? 1.f : MODE == kSigmoidRw ? sigmoid2(m) * lift : softplus2(make_float2(m, m)).x * lift;
+    const float den = top - theta;
+    row.x = raw ? m : lift;
+    row.theta = theta;
+    if (!(den > 1e-5f * top)) {
+        row.theta = 0.f;
+        row.kappa = tc::kUniformSlope;
+        return isnan(s1) ? (row.kappa = NAN, kAccurate) : kAccurate;
+    }
+    row.kappa = ptx::rcp(den);
+    row.beta = -theta * row.kappa;
+    // the mixed form is off by 2^-19 (1 + phi): 2^-12 of the largest difference where that is 2^-7 of
+    // the maximum or more, and the maximum is at least softplus(0)
+    if (den < 0.0078125f * top || (!raw && m < 0.f)) return kAccurate;
+    if constexpr (MODE == kLssar) {
+        row.ck = 2.f * kHalfInvLn2 * row.kappa;
+        if (fast_weights_ok(theta, row.kappa, (float)n, p)) return kOneExp;
+    }
+    return kMixed;
+}
+
+// The shared block's members by 32-bit address (one register, constant offsets).
+#define LSSAR_AT(member) (shared + (uint32_t)offsetof(Shared, member))
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t shared, unsigned *err, unsigned code, bool honour_abort = true) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+#pragma unroll 1
+    while (!ptx::mbar_try_wait_sleep(bar, parity, 1000000)) {
+        if (honour_abort && ptx::ld_shared_s32(LSSAR_AT(abort_flag))) return false;
+        if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
+            atomicCAS(err, 0u, code);
+            ptx::st_shared_s32(LSSAR_AT(abort_flag), 1);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// A ring of `N` barriers: slot and parity of use number `i`.
+template <int N>
+struct Ring {
+    uint32_t i = 0;
+    __device__ __forceinline__ uint32_t slot() const { return i % N; }
+    __device__ __forceinline__ uint32_t parity() const { return (i / N) & 1; }
+    __device__ __forceinline__ bool reused() const { return i >= N; }
+};
+
+template <int D, int MODE, bool HALF, int PHASE>
+__global__ void __launch_bounds__(kThreads, 1)
+attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm, const __grid_constant__ Args g) {
+    using C = Cfg<D>;
+    constexpr int NS = C::kStages, TB = C::kTile;
+    constexpr bool kNorm = uses_normalised_qk(MODE);
+    constexpr bool kOnePass = MODE == kSoftmax || MODE == kLssa;
+    constexpr bool kSepP = D == 64;
+    constexpr int kSBufs = PHASE == kStats ? 2 : 1;
+    constexpr int kPCol = 256, kOCol = kSepP ? 384 : 256;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t sq = ptx::smem_u32(smem), ring = sq + C::kRing;
+    Shared *sh = reinterpret_cast<Shared *>(smem + C::kShared);
+    const uint32_t shared = sq + C::kShared;
+    const PagedAttend &a = g.a;
+    const PagedCache &c = a.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    unsigned *err = c.err;
+
+    ptx::launch_dependents();
+    if (threadIdx.x == 0) {
+        auto init = [](uint64_t *b, uint32_t count) { ptx::mbar_init(ptx::smem_u32(b), count); };
+        for (int i = 0; i < 2; ++i) {
+            init(&sh->q_full[i], 1);
+            init(&sh->q_empty[i], 2);
+            for (int j = 0; j < 2; ++j) {
+                init(&sh->s_full[i][j], 1);
+                init(&sh->s_free[i][j], 256);
+            }
+            init(&sh->p_full[i], 256);
+            init(&sh->p_free[i], 1);
+            init(&sh->o_full[i], 1);
+            init(&sh->o_free[i], 256);
+            init(&sh->halves[i], 256);
+            for (int j = 0; j < 4; ++j) init(&sh->tile_max[i][j], 64);
+        }
+        for (int i = 0; i < 8; ++i) {
+            init(&sh->kv_full[i], 1);
+            init(&sh->kv_empty[i], 2);
+        }
+        for (int i = 0; i < kInfo; ++i) {
+            init(&sh->info_full[i], 1);
+            init(&sh->info_empty[i], 16);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            init(&sh->item_full[i], 1);
+            init(&sh->item_empty[i], 3 + 16);
+        }
+        sh->abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(LSSAR_AT(tmem), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+    // the plan, the norms and (kValues) the statistics are there from here on
+    ptx::grid_dependency_wait();
+
+    auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) -> bool {
+        return __all_sync(0xffffffffu, wait_bar(bar, parity, shared, err, code));
+    };
+    // The next segment, or one with kt0 < 0 at the end; the slot is released by release_item.
+    Ring<kItems> items;
+    auto next_item = [&](Item &it) -> bool {
+        if (!wait_all(LSSAR_AT(item_full) + 8 * items.slot(), items.parity(), kErrItem)) return false;
+        it = sh->items[items.slot()];
+        return it.kt0 >= 0;
+    };
+    auto release_item = [&] {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(LSSAR_AT(item_empty) + 8 * items.slot());
+        ++items.i;
+    };
+
+    if (warp < kScoreWarp0) {
+        if constexpr (PHASE == kValues) ptx::setmaxnreg_dec<kCtrlRegs>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ producer
+            if (ptx::elect_one()) {
+                ptx::prefetch_tensormap(&km);
+                if (PHASE == kValues) ptx::prefetch_tensormap(&vm);
+            }
+            const Header head = *g.s.head;
+            const int piece_rows = g.piece_rows, ps = c.page_size;
+            const int t1 = min((long long)head.total, (long long)(blockIdx.x + 1) * head.run);
+            long long t = (long long)blockIdx.x * head.run;
+            Ring<NS> kv;
+            Ring<kInfo> info;
+            bool ok = true;
+            int pg = -1, row = 0;          // of this lane's piece of the tile asked for: page (-1 past the end, -2 no page), row
+            Item it = {};
+            auto look_up = [&](int kt) {
+                const int s0 = kt * kKeys + lane * piece_rows, i = s0 / ps;
+                pg = -1;
+                if (lane * piece_rows >= kKeys || s0 >= it.len) return;
+                row = it.h * ps + s0 - i * ps;
+                pg = paged_page(c, it.b, i);
+                if (pg < 0) pg = -2;
+            };
+            auto push = [&](const CUtensorMap *map, int page, int y) -> bool {
+                const uint32_t s = kv.slot();
+                if (kv.reused() && !wait_all(LSSAR_AT(kv_empty) + 8 * s, kv.parity() ^ 1, kErrKvEmpty)) return false;
+                const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
+                const uint32_t full = (LSSAR_AT(kv_full) + 8 * s), dst = ring + s * TB + lane * piece_rows * 128;
+                if (lane == 0) {
+                    const int groups = piece_rows / 8;
+                    unsigned absent = 0xffffu;
+                    for (int i = 0; i * piece_rows < kKeys; ++i)
+                        if (there >> i & 1) absent &= ~(((1u << groups) - 1) << (i * groups));
+                    sh->absent[s] = absent;
+                    ptx::mbar_arrive_expect_tx(full, (uint32_t)__popc(there) * piece_rows * D * 2);
+                }
+                __syncwarp();
+                if (page >= 0 && dcheck(y >= 0 && y + piece_rows <= c.Hkv * ps && page < c.n_pages, err, kDbgTma)) {
+                    ptx::tma_load_3d(dst, map, full, 0, y, page);
+                    if (D == 128) ptx::tma_load_3d(dst + kKeys * 128, map, full, 64, y, page);
+                }
+                ++kv.i;
+                return true;
+            };
+            auto push_keys = [&](int kt, int slot) -> bool {
+                if constexpr (kNorm) {
+                    const uint32_t s = info.slot(), full = (LSSAR_AT(info_full) + 8 * s);
+                    if (info.reused() && !wait_all(LSSAR_AT(info_empty) + 8 * s, info.parity() ^ 1, kErrInfo)) return false;
+                    const long long at = ((long long)it.b * c.Hkv + it.h) * g.cap128 + (long long)kt * kKeys;
+                    const bool in = dcheck(kt >= 0 && (kt + 1) * kKeys <= g.cap128 && it.b < c.B, err, kDbgBulk);
+                    if (ptx::elect_one()) {
+                        ptx::mbar_arrive_expect_tx(full, kKeys * 4);
+                        if (in) ptx::bulk_load(LSSAR_AT(knorm) + s * (kKeys * 4), g.s.knorm + at, kKeys * 4, full);
+                    }
+                    __syncwarp();
+                    ++info.i;
+                }
+                // the first slot of a page that is none
+                if (__any_sync(0xffffffffu, pg == -2)) {
+                    const int first = __reduce_min_sync(0xffffffffu, pg == -2 ? kt * kKeys + lane * piece_rows : 0x7fffffff);
+                    if (lane == 0) {
+                        volatile int *bad = &sh->items[slot].first_bad;
+                        *bad = min(*bad, first);
+                    }
+                }
+                return push(&km, pg, row);
+            };
+            int e = 0, h = 0, kt = 0;
+            int4 en = make_int4(0, 0, 0, 0);
+            if (t < t1) {
+                e = g.s.first[blockIdx.x];
+                en = g.s.entries[e];
+                h = (int)(t - en.w) / en.z;
+                kt = (int)(t - en.w) - h * en.z;
+            }
+            while (ok) {
+                const uint32_t slot = items.slot();
+                if (items.reused() && !wait_all(LSSAR_AT(item_empty) + 8 * slot, items.parity() ^ 1, kErrItem)) break;
+                const bool more = t < t1;
+                it.kt0 = -1;
+                if (more) {
+                    const int cnt = a.counts ? a.counts[en.x] : a.n;
+                    it.b = en.x;
+                    it.h = h;
+                    it.t0 = en.y * g.tokens;
+                    it.rows = min(g.tokens, cnt - it.t0) * g.G;
+                    it.len = c.lens[en.x];
+                    it.base = it.len - cnt;
+                    it.nk = en.z;
+                    it.kt0 = kt;
+                    it.kt1 = (int)min((long long)en.z, kt + t1 - t);
+                    it.item = e * c.Hkv + h;
+                    it.start = en.w + h * en.z;
+                    it.first_bad = 0x7fffffff;
+                    if (!dcheck(e < head.entries && h < c.Hkv && it.kt1 > kt && it.rows > 0 && it.rows <= g.rows, err, kDbgItem)) it.kt0 = -1;
+                }
+                if (lane == 0) {
+                    sh->items[slot] = it;
+                    ptx::mbar_arrive(LSSAR_AT(item_full) + 8 * slot);
+                }
+                __syncwarp();
+                ++items.i;
+                if (it.kt0 < 0) break;
+                look_up(it.kt0);
+                if constexpr (PHASE == kStats) {
+                    for (int k = it.kt0; ok && k < it.kt1; ++k) {
+                        ok = push_keys(k, slot);
+                        if (k + 1 < it.kt1) look_up(k + 1);
+                    }
+                } else {
+                    int vpg = pg, vrow = row;
+                    ok = push_keys(it.kt0, slot);
+                    for (int k = it.kt0; ok && k < it.kt1; ++k) {
+                        const int page = vpg, y = vrow;
+                        if (k + 1 < it.kt1) {
+                            look_up(k + 1);
+                            vpg = pg;
+                            vrow = row;
+                            ok = push_keys(k + 1, slot);
+                        }
+                        if (ok) ok = push(&vm, page, y);
+                    }
+                }
+                t += it.kt1 - it.kt0;
+                kt = 0;
+                if (t < t1 && ++h == c.Hkv) {
+                    h = 0;
+                    en = g.s.entries[++e];
+                }
+            }
+            // no copy may be in flight when the CTA ends
+            for (uint32_t i = kv.i > NS ? kv.i - NS : 0; i < kv.i; ++i)
+                wait_bar((LSSAR_AT(kv_full) + 8 * (i % NS)), (i / NS) & 1, shared, err, kErrDrain, false);
+            if constexpr (kNorm)
+                for (uint32_t i = info.i > kInfo ? info.i - kInfo : 0; i < info.i; ++i)
+                    wait_bar((LSSAR_AT(info_full) + 8 * (i % kInfo)), (i / kInfo) & 1, shared, err, kErrDrain, false);
+            __syncwarp();
+        } else if (warp == 3) {
+            // ------------------------------------------------------------ rows of q
+            Ring<C::kQBufs> q;
+            Item it;
+            constexpr int kLanes = D / 8, kStep = 32 / kLanes;
+            const int chunk = lane % kLanes;
+            const uint32_t column = (chunk >> 3) * (kTileRows * 128);
+            while (next_item(it)) {
+                release_item();
+                if (q.reused() && !wait_all(LSSAR_AT(q_empty) + 8 * q.slot(), q.parity() ^ 1, kErrQ)) break;
+                const uint16_t *src = static_cast<const uint16_t *>(a.q) + it.b * a.qs[0] + (long long)it.h * g.G * a.qs[1] + it.t0 * a.qs[2] + chunk * 8;
+                const uint32_t dst = sq + q.slot() * 2 * TB + column;
+                const int rows = it.rows > kTileRows ? kPairRows : kTileRows;
+#pragma unroll 8
+                for (int r = lane / kLanes; r < rows; r += kStep) {
+                    const int v = min(r, it.rows - 1), tok = v / g.G, head = v - tok * g.G;
+                    cp_async16(dst + (r >> 7) * TB + (r & 127) * 128 + (((chunk & 7) ^ (r & 7)) << 4), src + head * a.qs[1] + tok * a.qs[2]);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(LSSAR_AT(q_full) + 8 * q.slot());
+                ++q.i;
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ MMA of tile w
+            const int w = warp - 1;
+            Ring<NS> kv;
+            Ring<C::kQBufs> q;
+            Ring<kSBufs> sb;               // S of this tile
+            uint32_t pv = 0, segs = 0;     // P.V products issued, segments with this tile
+            bool ok = true;
+            auto commit = [&](uint32_t bar) {
+                if (ptx::elect_one()) ptx::mma_commit(bar);
+                __syncwarp();
+            };
+            auto acquire = [&](uint32_t &slot) -> bool {
+                slot = kv.slot();
+                if (!wait_all(LSSAR_AT(kv_full) + 8 * slot, kv.parity(), kErrKvFull)) return false;
+                ++kv.i;
+                ptx::tc_fence_after();
+                return true;
+            };
+            const uint64_t dq0 = ptx::smem_desc_sw128(sq, tc::kKmajorLbo, tc::kKmajorSbo);
+            const uint64_t dk0 = ptx::smem_desc_sw128(ring, tc::kKmajorLbo, tc::kKmajorSbo);
+            const uint64_t dv0 = ptx::smem_desc_sw128(ring, tc::kVLbo, tc::kVSbo);
+            uint32_t qoff = 0;
+            // S = q k^T of the K tile in kslot (its buffer is free once the score warps have read it)
+            auto issue_s = [&](uint32_t kslot) -> bool {
+                const uint32_t buf = sb.slot();
+                if (sb.reused() && !wait_all((LSSAR_AT(s_free) + 16 * (w) + 8 * (buf)), sb.parity() ^ 1, kErrSFree)) return false;
+                ptx::tc_fence_after();
+                const uint64_t dq = dq0 + (uint64_t)((qoff + w * TB) >> 4), dk = dk0 + (uint64_t)((kslot * TB) >> 4);
+                const uint32_t full = (LSSAR_AT(s_full) + 16 * (w) + 8 * (buf));
+                const uint32_t col = tmem + (PHASE == kStats ? w * 256 + buf * kKeys : w * kKeys);
+                dcheck(tmem_in_range(col, tmem, kKeys, 512), err, kDbgTmem);
+                if (ptx::elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
+                        ptx::mma_ss(col, dq + off, dk + off, g.idesc_s, k > 0);
+                    }
+                    ptx::mma_commit(full);
+                }
+                __syncwarp();
+                ++sb.i;
+                return true;
+            };
+            // Rows of a V tile that hold nothing of the sequence (past its end, pages that are none): zeros,
+            // as their weight is 0 and what lies there may be infinite.
+            auto clear_rows = [&](uint32_t vslot, int left) {
+                const unsigned absent = *(volatile unsigned *)&sh->absent[vslot];
+                if (left >= kKeys && absent == 0) return;
+                for (int r = lane; r < kKeys; r += 32)
+                    if (r >= left || (absent >> (r >> 3) & 1)) {
+#pragma unroll
+                        for (int x = 0; x < D / 8; ++x)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + vslot * TB + (x >> 3) * 16384 + r * 128 + (x & 7) * 16), "r"(0) : "memory");
+                    }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            };
+            auto issue_pv = [&](uint32_t vslot, bool accumulate) {
+                const uint64_t dv = dv0 + (uint64_t)((vslot * TB) >> 4);
+                if (ptx::elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        ptx::mma_ts(tmem + kOCol + w * D, kSepP ? tmem + kPCol + 64 * w + 8 * k : tmem + w * kKeys + (k / 4) * 64 + (k % 4) * 8,
+                                    dv + (uint64_t)((k * 2048) >> 4), g.idesc_pv, (accumulate || k > 0) ? 1u : 0u);
+                }
+                __syncwarp();
+            };
+            Item it;
+            while (ok && next_item(it)) {
+                release_item();
+                const bool live = it.rows > w * kTileRows;
+                if (!(ok = wait_all(LSSAR_AT(q_full) + 8 * q.slot(), q.parity(), kErrQ))) break;
+                qoff = q.slot() * 2 * TB;
+                ptx::tc_fence_after();
+                uint32_t kslot, vslot;
+                if constexpr (PHASE == kStats) {
+                    for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
+                        if (!(ok = acquire(kslot))) break;
+                        if (live) ok = issue_s(kslot);
+                        commit(LSSAR_AT(kv_empty) + 8 * kslot);
+                    }
+                } else {
+                    if (!(ok = acquire(kslot))) break;
+                    if (live && !(ok = issue_s(kslot))) break;
+                    commit(LSSAR_AT(kv_empty) + 8 * kslot);
+                    for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
+                        const bool next = kt + 1 < it.kt1;
+                        if (next && !(ok = acquire(kslot))) break;
+                        if constexpr (kSepP) {
+                            // the next scores as soon as the score warps have these
+                            if (live && next && !(ok = issue_s(kslot))) break;
+                            if (next) commit(LSSAR_AT(kv_empty) + 8 * kslot);
+                        }
+                        if (!(ok = acquire(vslot))) break;
+                        if (live) {
+                            clear_rows(vslot, it.len - kt * kKeys);
+                            // d = 64: P is in its columns; d = 128: over S, which its release says
+                            if constexpr (kSepP) {
+                                if (!(ok = wait_all(LSSAR_AT(p_full) + 8 * w, pv & 1, kErrPFull))) break;
+                            } else {
+                                if (!(ok = wait_all((LSSAR_AT(s_free) + 16 * (w) + 8 * (0)), pv & 1, kErrSFree))) break;
+                            }
+                            ptx::tc_fence_after();
+                            if (kt == it.kt0 && segs > 0) {
+                                if (!(ok = wait_all(LSSAR_AT(o_free) + 8 * w, (segs - 1) & 1, kErrOFree))) break;
+                                ptx::tc_fence_after();
+                            }
+                            issue_pv(vslot, kt > it.kt0);
+                            ++pv;
+                            if constexpr (kSepP) commit(LSSAR_AT(p_free) + 8 * w);
+                            if (!next) {
+                                commit(LSSAR_AT(o_full) + 8 * w);
+                                ++segs;
+                            }
+                        }
+                        commit(LSSAR_AT(kv_empty) + 8 * vslot);
+                        if constexpr (!kSepP) {
+                            if (live && next && !(ok = issue_s(kslot))) break;
+                            if (next) commit(LSSAR_AT(kv_empty) + 8 * kslot);
+                        }
+                    }
+                }
+                commit(LSSAR_AT(q_empty) + 8 * q.slot());
+                ++q.i;
+            }
+            __syncwarp();
+        }
+    } else {
+        if constexpr (PHASE == kValues) ptx::setmaxnreg_inc<kScoreRegs>();
+        // ------------------------------------------------------------ score warps
+        const int wg = (warp - kScoreWarp0) >> 2, w = wg & 1, half = wg >> 1, quarter = warp & 3;
+        const int in = quarter * 32 + lane;                      // row of the tile = TMEM lane
+        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_col = tmem + lane_addr + (PHASE == kStats ? w * 256 : w * kKeys) + half * 64;
+        const uint32_t p_col = kSepP ? tmem + lane_addr + kPCol + 64 * w + 32 * half : s_col;
+        const uint32_t o_col = tmem + lane_addr + kOCol + w * D + half * (D / 2);
+        dcheck(tmem_in_range(s_col, tmem, 64, 512) && (PHASE == kStats || tmem_in_range(o_col, tmem, D / 2, 512)), err, kDbgTmem);
+        const uint32_t s_full = LSSAR_AT(s_full) + 16 * w, s_free = LSSAR_AT(s_free) + 16 * w;
+        const uint32_t p_done = (kSepP ? LSSAR_AT(p_full) + 8 * w : s_free), p_free = LSSAR_AT(p_free) + 8 * w;
+        // this row's place in the exchange arrays, of the first parity, and the other half's
+        const uint32_t mine = (w * 2 + half) * (kTileRows * 4) + 4 * in, others = (w * 2 + (half ^ 1)) * (kTileRows * 4) + 4 * in;
+        constexpr uint32_t kParity = 4 * kTileRows * 4;
+        constexpr float kMasked = MODE == kSigmoidRw ? INFINITY : -INFINITY;
+        Ring<kSBufs> sb;
+        Ring<kInfo> info;
+        uint32_t pv = 0, segs = 0, steps = 0, exchanges = 0;
+        const int run = g.s.head->run;
+        bool ok = true;
+        auto field = [&](size_t offset) { return ptx::ld_shared_s32(LSSAR_AT(items) + items.slot() * (uint32_t)sizeof(Item) + (uint32_t)offset); };
+#define LSSAR_ITEM(name) field(offsetof(Item, name))
+        auto take_norms = [&] {        // the tile's key norms are there
+            return !kNorm || wait_all(LSSAR_AT(info_full) + 8 * info.slot(), info.parity(), kErrInfo);
+        };
+        auto leave_norms = [&] {       // they have been read
+            if constexpr (kNorm) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(LSSAR_AT(info_empty) + 8 * info.slot());
+                ++info.i;
+            }
+        };
+        // 32 products of the tile from column 32 x of this half on, as they are
+        auto load = [&](uint32_t (&z)[32], uint32_t col) {
+            ptx::tmem_ld32(col, z);
+            ptx::tmem_ld_wait();
+            ptx::reg_fence(z);
+        };
+        while (ok) {
+            if (!wait_all(LSSAR_AT(item_full) + 8 * items.slot(), items.parity(), kErrItem)) break;
+            const int kt0 = LSSAR_ITEM(kt0), kt1 = LSSAR_ITEM(kt1), rows = LSSAR_ITEM(rows);
+            if (kt0 < 0) break;
+            if (rows <= w * kTileRows) {                         // none of this tile's
+                for (int kt = kt0; ok && kt < kt1; ++kt) {
+                    ok = take_norms();
+                    leave_norms();
+                }
+                release_item();
+                continue;
+            }
+            const bool live = rows > w * kTileRows + quarter * 32;
+            const int v = min(w * kTileRows + in, rows - 1);     // row of the pair (past the last: the last)
+            // last slot that the row attends to, and that of the warp's first row
+            const int limit = LSSAR_ITEM(base) + LSSAR_ITEM(t0) + v / g.G;
+            const int least = __shfl_sync(0xffffffffu, limit, 0);
+            Row row = {};
+            row.a = g.scale;
+            if constexpr (kNorm) {
+                const int hq = LSSAR_ITEM(h) * g.G + v % g.G;
+                row.a = g.s.qscale[((size_t)LSSAR_ITEM(b) * a.H + hq) * a.n + LSSAR_ITEM(t0) + v / g.G];
+            }
+            int form = kMixed;
+            if constexpr (PHASE == kValues && is_reweight(MODE)) {
+                // the row's maximum and sum from the segments of its item
+                float m = kLowest, s1 = 0.f;
+                const int start = LSSAR_ITEM(start), c0 = start / run, c1 = (start + LSSAR_ITEM(nk) - 1) / run;
+                const float2 *part = g.s.stats + (size_t)LSSAR_ITEM(item) * g.rows + v;
+#pragma unroll 4
+                for (int cta = c0; cta <= c1; ++cta) {
+                    const float2 x = part[(size_t)cta * g.rows];
+                    const float top = fmaxf(m, x.x);
+                    s1 = MODE == kSoftmaxRw ? s1 * ptx::ex2(m - top) + x.y * ptx::ex2(x.x - top) : s1 + x.y;
+                    m = top;
+                }
+                form = row_constants<MODE>(row, m, s1, limit + 1, a.p);
+                // one form for the warp: all rows or none by one exponential
+                const unsigned accurate = __ballot_sync(0xffffffffu, form == kAccurate), one = __ballot_sync(0xffffffffu, form == kOneExp);
+                form = accurate ? kAccurate : one == 0xffffffffu ? kOneExp : kMixed;
+            }
+            if constexpr (PHASE == kValues && kOnePass) {
+                row.ref = MODE == kSoftmax ? kLowest : kNoLift;
+                row.x = MODE == kSoftmax ? kLowest : ptx::ex2(Range16<MODE, HALF>::kRoom - kNoLift);
+                form = MODE == kLssa ? kAccurate : kMixed;
+            }
+            float m_run = MODE == kSigmoidRw ? INFINITY : MODE == kLssar ? kLowest : -INFINITY, sum_run = 0.f;
+            float2 acc = make_float2(0.f, 0.f);
+            for (int kt = kt0; kt < kt1; ++kt, ++steps) {
+                const uint32_t buf = sb.slot(), col = s_col + buf * kKeys;
+                if (!(ok = wait_all(s_full + 8 * buf, sb.parity(), kErrSFull))) break;
+                ++sb.i;
+                ptx::tc_fence_after();
+                if (!live) {
+                    // none of the item's rows: the barriers only
+                    ptx::tc_fence_before();
+                    if constexpr (PHASE == kStats || kSepP) ptx::mbar_arrive(s_free + 8 * buf);
+                    if (!(ok = take_norms())) break;
+                    leave_norms();
+                    if constexpr (PHASE == kValues) {
+                        // (not before the last step's arrivals are all in, which its product follows)
+                        if (kSepP && pv > 0 && !(ok = wait_all(p_free, (pv - 1) & 1, kErrPFree))) break;
+                        ptx::mbar_arrive(p_done);
+                        ++pv;
+                    }
+                    continue;
+                }
+                if (!(ok = take_norms())) break;
+                const uint32_t knorm = LSSAR_AT(knorm) + info.slot() * (kKeys * 4) + half * 256;
+                const int last = limit - kt * kKeys - half * 64;      // last column of the half that is not masked
+                const bool masked = least < kt * kKeys + half * 64 + 63;
+                if constexpr (PHASE == kStats) {
+                    uint32_t r0[32], r1[32];
+                    ptx::tmem_ld32(col, r0);
+                    ptx::tmem_ld32(col + 32, r1);
+                    ptx::tmem_ld_wait();
+                    ptx::reg_fence(r0);
+                    ptx::reg_fence(r1);
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(s_free + 8 * buf);               // the next product may write here
+                    to_z<kNorm>(r0, knorm, row.a);
+                    to_z<kNorm>(r1, knorm + 128, row.a);
+                    leave_norms();
+                    if (masked) {
+                        mask(r0, last, kMasked);
+                        mask(r1, last - 32, kMasked);
+                    }
+                    if constexpr (MODE == kSoftmaxRw) {
+                        tc::softmax_tile_stats(r0, r1, m_run, sum_run);
+                    } else if constexpr (MODE == kSigmoidRw) {
+                        const float2 one = make_float2(1.f, 1.f);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float2 x = pair_at(r0, j), y = pair_at(r1, j);
+                            m_run = min3(min3(m_run, x.x, x.y), y.x, y.y);
+                            const float2 vx = __fadd2_rn(make_float2(ptx::ex2(x.x), ptx::ex2(x.y)), one);
+                            const float2 vy = __fadd2_rn(make_float2(ptx::ex2(y.x), ptx::ex2(y.y)), one);
+                            acc = __fadd2_rn(acc, make_float2(ptx::rcp(vx.x), ptx::rcp(vx.y)));
+                            acc = __fadd2_rn(acc, make_float2(ptx::rcp(vy.x), ptx::rcp(vy.y)));
+                        }
+                    } else {
+                        const float top = max_of(r1, max_of(r0, -INFINITY));
+                        m_run = fmaxf(m_run, top);
+                        float2 prod[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
+                        if (__any_sync(0xffffffffu, top < 0.f)) {
+                            softplus_sum<true>(r0, acc, prod[0]);
+                            softplus_sum<true>(r1, acc, prod[1]);
+                        } else {
+                            softplus_sum<false>(r0, acc, prod[0]);
+                            softplus_sum<false>(r1, acc, prod[1]);
+                            sum_run += ptx::lg2((prod[0].x * prod[0].y) * (prod[1].x * prod[1].y));
+                        }
+                    }
+                    continue;
+                }
+                bool raise = false;
+                float alpha = 1.f;
+                if constexpr (kOnePass) {
+                    // The reference of a row's weights: its running maximum (LSSA: up to 0, where softplus is
+                    // at least 1), raised when a tile's passes it by more than the lag.  Both halves' maxima meet in
+                    // shared memory.  A warp whose LSSA rows are all at 0 stays there.
+                    if (MODE == kSoftmax || form == kAccurate) {
+                        float top = -INFINITY;
+#pragma unroll 1
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t z[32];
+                            load(z, col + x * 32);
+                            if constexpr (MODE == kLssa) to_z<true>(z, knorm + x * 128, row.a);
+                            if (masked) mask(z, last - x * 32, -INFINITY);
+                            top = max_of(z, top);
+                        }
+                        if constexpr (MODE == kSoftmax) top = __fmul_rn(top, row.a);      // (rounded as the scores are, in no FMA)
+                        const uint32_t at = LSSAR_AT(tmax) + (exchanges & 1) * kParity;
+                        ptx::st_shared_f32(at + mine, top);
+                        ptx::mbar_arrive(LSSAR_AT(tile_max) + 32 * w + 8 * quarter);
+                        if (!(ok = wait_all(LSSAR_AT(tile_max) + 32 * w + 8 * quarter, exchanges & 1, kErrTileMax))) break;
+                        top = fmaxf(top, ptx::ld_shared_f32(at + others));
+                        ++exchanges;
+                        if constexpr (MODE == kLssa) top = fminf(top, 0.f);
+                        raise = top - row.ref > Range16<MODE, HALF>::kLag || (MODE == kLssa && top >= 0.f && row.ref < 0.f);
+                        if (raise) {
+                            if constexpr (MODE == kSoftmax) {
+                                // (scores so large that their steps pass the room: without it)
+                                float x = top - Range16<MODE, HALF>::kRoom;
+                                if (!(top - x <= Range16<MODE, HALF>::kRoom)) x = top;
+                                alpha = ptx::ex2(row.x - x);
+                                row.x = x;
+                            } else {
+                                alpha = ptx::ex2(row.ref - top);
+                                row.x = ptx::ex2(Range16<MODE, HALF>::kRoom - top);
+                            }
+                            row.ref = top;
+                            acc = __fmul2_rn(acc, make_float2(alpha, alpha));
+                        }
+                        if constexpr (MODE == kSoftmax) form = __any_sync(0xffffffffu, fabsf(row.ref) > 65536.f) ? kAccurate : kMixed;
+                    }
+                }
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t z[32], pk[16];
+                    load(z, col + x * 32);
+                    if (kSepP && x == 1) {
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(s_free);                     // the next product may write here
+                    }
+                    if constexpr (MODE != kSoftmax) to_z<kNorm>(z, knorm + x * 128, row.a);
+                    if (masked) mask(z, last - x * 32, kMasked);
+                    weights32<MODE, HALF>(z, row, form, a.p, acc, pk);
+                    if constexpr (kSepP) {
+                        // P and O are free once the product before has read the one and written the other
+                        if (x == 0 && pv > 0) {
+                            if (!(ok = wait_all(p_free, (pv - 1) & 1, kErrPFree))) break;
+                            ptx::tc_fence_after();
+                        }
+                    }
+                    ptx::tmem_st16(p_col + x * 16, pk);
+                }
+                if (!ok) break;
+                leave_norms();
+                // (the tile that raised the last row to 0 was still weighted in the accurate form)
+                if constexpr (MODE == kLssa) {
+                    if (form == kAccurate && __all_sync(0xffffffffu, row.ref >= 0.f)) form = kMixed;
+                }
+                if constexpr (kOnePass) {
+                    if (kt > kt0 && __any_sync(0xffffffffu, raise)) {
+#pragma unroll 1
+                        for (int x = 0; x < D / 2; x += 16) {
+                            uint32_t o[16];
+                            ptx::tmem_ld16(o_col + x, o);
+                            ptx::tmem_ld_wait();
+                            ptx::reg_fence(o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                            ptx::tmem_st16(o_col + x, o);
+                        }
+                    }
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(p_done);
+                ++pv;
+            }
+            if (!ok) break;
+            // the two halves of a row meet
+            const uint32_t par = segs & 1;
+            const float part = (acc.x + acc.y) + sum_run;
+            ptx::st_shared_f32(LSSAR_AT(s) + par * kParity + mine, part);
+            const float m_part = MODE == kSigmoidRw ? -m_run : fmaxf(m_run, kLowest);
+            if constexpr (PHASE == kStats) ptx::st_shared_f32(LSSAR_AT(m) + par * kParity + mine, m_part);
+            ptx::mbar_arrive(LSSAR_AT(halves) + 8 * w);
+            if (!(ok = wait_all(LSSAR_AT(halves) + 8 * w, par, kErrHalves))) break;
+            const float other = ptx::ld_shared_f32(LSSAR_AT(s) + par * kParity + others);
+            const bool valid = w * kTileRows + in < rows;
+            if constexpr (PHASE == kStats) {
+                ++segs;
+                if (half == 0 && valid) {
+                    const float m1 = ptx::ld_shared_f32(LSSAR_AT(m) + par * kParity + others), m = fmaxf(m_part, m1);
+                    const float s = MODE == kSoftmaxRw ? part * ptx::ex2(m_part - m) + other * ptx::ex2(m1 - m) : part + other;
+                    const long long at = LSSAR_ITEM(item) + (long long)blockIdx.x;
+                    if (dcheck(v < g.rows, err, kDbgGlobal)) g.s.stats[at * g.rows + v] = make_float2(m, s);
+                }
+                release_item();
+                continue;
+            }
+            // (half 0's part first in both, so that both see the same sum)
+            float sum = half == 0 ? part + other : other + part;
+            if (limit >= LSSAR_ITEM(first_bad)) sum = NAN;
+            if (!(ok = wait_all(LSSAR_AT(o_full) + 8 * w, segs & 1, kErrOFull))) break;
+            ++segs;
+            ptx::tc_fence_after();
+            const int b = LSSAR_ITEM(b), hq = LSSAR_ITEM(h) * g.G + v % g.G, t = LSSAR_ITEM(t0) + v / g.G, start = LSSAR_ITEM(start);
+            const bool whole = kt0 == 0 && kt1 == LSSAR_ITEM(nk);
+            // a segment's part: of the run's first item in its first place, of its last in its second
+            const int place = 2 * blockIdx.x + (kt0 == 0 && start != (long long)blockIdx.x * run ? 1 : 0);
+            const size_t to = (size_t)place * g.rows + v;
+            const bool in_range = dcheck(b < c.B && hq < a.H && t < a.n && v < g.rows && place < 2 * g.ctas, err, kDbgGlobal);
+            const float inv = 1.f / sum;
+            if (valid && in_range && !whole && half == 0) g.s.sums[to] = make_float2(MODE == kSoftmax ? row.x : row.ref, sum);
+            if (live) {
+#pragma unroll 1
+                for (int x = 0; x < D / 64; ++x) {
+                    uint32_t o[32];
+                    load(o, o_col + x * 32);
+                    if (!valid || !in_range) continue;
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (((size_t)b * a.H + hq) * a.n + t) * D + half * (D / 2) + x * 32);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t u[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 f = __fmul2_rn(pair_at(o, 8 * j + 2 * k), make_float2(inv, inv));
+                                u[k] = HALF ? ptx::pack_f16x2(f.x, f.y) : ptx::pack_bf16x2(f.x, f.y);
+                            }
+                            dst[j] = make_uint4(u[0], u[1], u[2], u[3]);
+                        }
+                    } else {
+                        uint4 *dst = reinterpret_cast<uint4 *>(g.s.o + to * D + half * (D / 2) + x * 32);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) dst[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    }
+                }
+            }
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(LSSAR_AT(o_free) + 8 * w);
+            release_item();
+        }
+#undef LSSAR_ITEM
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- join
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 32;
+
+// Items that lie in several runs: block x takes the one that run x + 1 begins inside of, if that is
+// the first such run; blockIdx.y: a group of its rows.
+template <int D, bool HALF, bool RELATIVE>
+__global__ void __launch_bounds__(kJoinThreads) attend_join(const __grid_constant__ Args g) {
+    const PagedAttend &a = g.a;
+    const PagedCache &c = a.c;
+    ptx::grid_dependency_wait();
+    const Header head = *g.s.head;
+    const int cta = blockIdx.x + 1;
+    const long long x = (long long)cta * head.run;
+    if (x >= head.total) return;
+    const int4 en = g.s.entries[g.s.first[cta]];
+    const int h = (int)(x - en.w) / en.z, start = en.w + h * en.z;
+    if (start == x || x - head.run > start) return;
+    const int last = (start + en.z - 1) / head.run, cnt = a.counts ? a.counts[en.x] : a.n, t0 = en.y * g.tokens;
+    const int rows = min(g.tokens, cnt - t0) * g.G;
+    const int own = 2 * (cta - 1) + (start != x - head.run);       // the first run's place
+    constexpr int kLanes = D / 4, kStep = kJoinThreads / kLanes;
+    const int part = threadIdx.x % kLanes;
+#pragma unroll 1
+    for (int r = blockIdx.y * kJoinRows + threadIdx.x / kLanes; r < min(rows, (int)(blockIdx.y + 1) * kJoinRows); r += kStep) {
+        float m = RELATIVE ? kLowest : 0.f, w = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = cta - 1; k <= last; ++k) {
+            const size_t at = (size_t)(k == cta - 1 ? own : 2 * k) * g.rows + r;
+            const float2 s = g.s.sums[at];
+            const float4 v = reinterpret_cast<const float4 *>(g.s.o + at * D)[part];
+            float f = 1.f;
+            if (RELATIVE) {
+                const float top = fmaxf(m, s.x), old = ptx::ex2(m - top);
+                f = ptx::ex2(s.x - top);
+                m = top;
+                w *= old;
+                o = make_float4(o.x * old, o.y * old, o.z * old, o.w * old);
+            }
+            w = fmaf(s.y, f, w);
+            o = make_float4(fmaf(v.x, f, o.x), fmaf(v.y, f, o.y), fmaf(v.z, f, o.z), fmaf(v.w, f, o.w));
+        }
+        const int tok = r / g.G, hq = h * g.G + r - tok * g.G;
+        const float inv = 1.f / w;
+        const uint32_t lo = HALF ? ptx::pack_f16x2(o.x * inv, o.y * inv) : ptx::pack_bf16x2(o.x * inv, o.y * inv);
+        const uint32_t hi = HALF ? ptx::pack_f16x2(o.z * inv, o.w * inv) : ptx::pack_bf16x2(o.z * inv, o.w * inv);
+        const size_t out_row = ((size_t)en.x * a.H + hq) * a.n + t0 + tok;
+        if (dcheck(en.x < c.B && hq < a.H && t0 + tok < a.n, c.err, kDbgGlobal))
+            reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + out_row * D)[part] = make_uint2(lo, hi);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+template <int D, int MODE, bool HALF, int PHASE>
+cudaError_t launch_phase(const CUtensorMap &km, const CUtensorMap &vm, const Args &g, cudaStream_t stream) {
+    static PerDeviceOnce once;
+    const void *fn = (const void *)attend_kernel<D, MODE, HALF, PHASE>;
+    constexpr int smem = Cfg<D>::kSmem;
+    const cudaError_t e = per_device_once(once, nullptr, [&](int &) {
+        // registers move between the warpgroups (kValues): only a launch at exactly
+        // kLaunchRegs a thread adds up
+        cudaFuncAttributes attr;
+        const cudaError_t x = cudaFuncGetAttributes(&attr, fn);
+        if (x != cudaSuccess) return x;
+        if (PHASE == kValues && attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (e != cudaSuccess) return e;
+    void *args[] = {(void *)&km, (void *)&vm, (void *)&g};
+    return paged::launch_kernel(fn, g.ctas, kThreads, smem, true, args, stream);
+}
+
+template <int D, int MODE, bool HALF>
+cudaError_t launch_mode(const CUtensorMap &km, const CUtensorMap &vm, const Args &g, int sms, cudaStream_t stream) {
+    int norms = uses_normalised_qk(MODE);
+    void *prep[] = {(void *)&g, (void *)&norms};
+    cudaError_t e = paged::launch_kernel((const void *)attend_prepare<D>, norms ? 1 + 4 * sms : 1, kPrepThreads, 0, false, prep, stream);
+    if (e != cudaSuccess) return e;
+    if constexpr (is_reweight(MODE))
+        if ((e = launch_phase<D, MODE, false, kStats>(km, vm, g, stream)) != cudaSuccess) return e;
+    if ((e = launch_phase<D, MODE, HALF, kValues>(km, vm, g, stream)) != cudaSuccess) return e;
+    if (g.ctas < 2) return cudaSuccess;
+    void *args[] = {(void *)&g};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)g.ctas - 1, (unsigned)(g.rows + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, (const void *)attend_join<D, HALF, !is_reweight(MODE)>, args);
+}
+
+// One call per mode and d, in files of their own so that the instances compile in parallel.
+using Launch = cudaError_t(const CUtensorMap &km, const CUtensorMap &vm, const Args &g, int sms, cudaStream_t st);
+Launch softmax_d64, softmax_d128, lssa_d64, lssa_d128, lssar_d64, lssar_d128, softmax_rw_d64, softmax_rw_d128, sigmoid_rw_d64, sigmoid_rw_d128;
+
+#define LSSAR_ATTEND_INSTANCE(NAME, MODE, D)                                                                             \
+    cudaError_t NAME(const CUtensorMap &km, const CUtensorMap &vm, const Args &g, int sms, cudaStream_t st) {            \
+        return g.a.c.half ? launch_mode<D, MODE, true>(km, vm, g, sms, st) : launch_mode<D, MODE, false>(km, vm, g, sms, st); \
+    }
+
+}  // namespace attend
+}  // namespace lssar

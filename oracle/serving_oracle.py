@@ -107,12 +107,14 @@ def attend_bound(q, k, mode, p=3):
 def attend_row(q, k, v, mode, p, half_step):
     """One row's outputs [G, d] over all of k, v [n, d], and the bound on their
     error before the output's rounding: the weights', their rounding to 16 bits
-    (half_step), and the value sum in float32.  LSSAR from p = 4 on may use the
+    (half_step; of fp16 also half its least step, 2^-25, against a largest weight
+    of 0.69 2^8 or more), and the value sum in float32.  LSSAR from p = 4 on may use the
     one-exponential softplus, which moves the weights in sum by at most 2e-4 of
     their total, and the output by twice that of the largest value."""
     n = len(k)
     w, e = row_weights(q, k, mode, p), attend_bound(q, k, mode, p)
-    err = (e + (half_step + 2.0 ** -20 + (n / 4 + 64) * 2.0 ** -24) * w) @ np.abs(v)
+    least = 2.0 ** -32 * w.max(axis=1, keepdims=True) if half_step == 2.0 ** -11 else 0.0
+    err = (e + (half_step + 2.0 ** -20 + (n / 4 + 64) * 2.0 ** -24) * w + least) @ np.abs(v)
     return w @ v, err + (4e-4 * np.abs(v).max(axis=0) if mode == MODE_LSSAR and p >= 4 else 0.0)
 
 
