@@ -16,7 +16,7 @@ Layout layout(const PagedAttend &pr, int sms) {
     l.tokens = attend::kPairRows / l.G;
     l.rows = (pr.n < l.tokens ? pr.n : l.tokens) * l.G;
     l.cap128 = (c.capacity() + attend::kKeys - 1) / attend::kKeys * attend::kKeys;
-    const size_t pairs = (size_t)c.B * ((pr.n + l.tokens - 1) / l.tokens), items = pairs * c.Hkv, tiles = items * (l.cap128 / attend::kKeys);
+    const size_t pairs = (size_t)c.B * ((pr.n + l.tokens - 1) / l.tokens), items = pairs * c.Hkv, tiles = items * (l.cap128 / attend::kKeys + attend::kItemCost);
     l.ctas = (int)(tiles < (size_t)sms ? tiles : sms);
     const bool norms = uses_normalised_qk(pr.mode), reweight = is_reweight(pr.mode);
     auto r = [](size_t x) { return (x + 255) & ~(size_t)255; };
@@ -35,7 +35,7 @@ Layout layout(const PagedAttend &pr, int sms) {
 
 long long paged_attend_tiles(const PagedAttend &pr) {
     const long long tokens = attend::kPairRows / (pr.H / pr.c.Hkv), pairs = (pr.n + tokens - 1) / tokens;
-    const long long tiles = (pr.c.capacity() + 63) / 64;      // (the prologue's tiles may be of 64 keys)
+    const long long tiles = (pr.c.capacity() + 63) / 64 + attend::kItemCost;      // (the prologue's tiles may be of 64 keys)
     return (long long)pr.c.B * pr.c.Hkv * pairs > (1LL << 31) ? 1LL << 62 : (long long)pr.c.B * pr.c.Hkv * pairs * tiles;
 }
 
@@ -67,6 +67,8 @@ cudaError_t launch_paged_attend(const PagedAttend &pr, void *ws, int sms, cudaSt
     const int low = c.page_size & -c.page_size;
     g.piece_rows = low < attend::kKeys ? low : attend::kKeys;
     g.scale = !uses_normalised_qk(pr.mode) ? 1.4426950408889634f / sqrtf((float)c.d) : (pr.mode == kSigmoidRw ? -1.f : 1.f) * score_qmul(c.d);
+    g.power = {0, pr.p};
+    for (; g.power.rest % 3 == 0; g.power.rest /= 3) ++g.power.cubes;
     g.idesc_s = ptx::idesc_f16(!c.half, attend::kTileRows, attend::kKeys, false, false);
     g.idesc_pv = ptx::idesc_f16(!c.half, attend::kTileRows, c.d, false, true);
     CUtensorMap km, vm;

@@ -26,9 +26,9 @@
 // Each is a programmatic dependent of the one before it.
 //
 // Structure of attend (640 threads): warp 0 the TMA producer of K, V (a piece of a page at a
-// time) and key norms; warps 1, 2 issue the tcgen05.mma of one tile each; warp 3 gathers the rows of q
-// (any strides, any group); four warpgroups of score warps, two per tile, each half of its
-// columns: thread = row (TMEM lane).  Warps whose 32 rows hold none of the item's skip the arithmetic.
+// time) and key norms; warps 1, 2 issue the tcgen05.mma of one tile each; warp 3 has no role; four warpgroups of score
+// warps, two per tile, each half of its columns: thread = row (TMEM lane).  They also gather the rows of q
+// (any strides, any group) of the next segment during the last step of this one.  Warps whose 32 rows hold none of the item's skip the arithmetic.
 // TMEM (512 columns): kStats: S of tile w, two buffers each, at 256 w + 128 buffer.  kValues: S_w at
 // 128 w; d = 64: P_w at 256 + 64 w, O_w at 384 + 64 w; d = 128: P_w over S_w, O_w at 256 + 128 w.
 #pragma once
@@ -57,7 +57,9 @@ constexpr int kLaunchRegs = 96, kCtrlRegs = 64, kScoreRegs = 104;
 static_assert(128 * kCtrlRegs + 512 * kScoreRegs <= kThreads * kLaunchRegs, "register split");
 constexpr int kInfo = 4;                      // tiles whose key norms are in shared memory
 constexpr int kItems = 4;                     // depth of the queue of segments
+constexpr int kItemCost = 2;                  // what an item costs beside its tiles, in tiles (they are numbered before its first)
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint32_t kNapProducer = 200;   // ns between its polls of a barrier
 constexpr float kLowest = -3.0e38f;           // below every score, and finite
 enum : unsigned { kErrItem = 61, kErrQ, kErrKvFull, kErrKvEmpty, kErrSFull, kErrSFree, kErrPFull, kErrPFree, kErrOFull, kErrOFree,
                   kErrInfo, kErrHalves, kErrTileMax, kErrDrain };
@@ -78,13 +80,18 @@ struct Header {
 
 struct Scratch {
     Header *head;
-    int4 *entries;        // {sequence, pair, tiles of the pair, number of its first tile}
+    int4 *entries;        // {sequence, pair, tiles of the pair and its cost, number of the first of them}
     int *first;           // [ctas] entry of each CTA's first tile
     float *knorm;         // [B, Hkv, cap128] 1 / |k|
     float *qscale;        // [B, H, n] factor of a query row's scores
     float2 *stats;        // [item + cta][rows]: m, S1 of a segment's rows
     float2 *sums;         // [2 cta + last][rows]: reference, sum of w
     float *o;             // [2 cta + last][rows][d]: sum of w v
+};
+
+// The exponent as 3^cubes * rest, so that p = 15 takes five products.
+struct Power {
+    int cubes, rest;
 };
 
 struct Args {
@@ -95,6 +102,7 @@ struct Args {
     int cap128;           // capacity, a multiple of 128
     int piece_rows;       // rows of a page per copy
     float scale;          // log2e / sqrt(d), or +-log2e ln d
+    Power power;
     uint32_t idesc_s, idesc_pv;
 };
 
@@ -103,7 +111,7 @@ struct Item {
     int b, h, t0, rows;   // first token, valid rows of the pair
     int base, len;        // slots before the chunk, cached tokens
     int nk, kt0, kt1;     // tiles of the item; those of this segment
-    int item, start;      // number of the item, of its first tile
+    int item, start;      // number of the item, of its first tile (its cost comes before)
     int first_bad;        // first slot of a page that is none
 };
 
@@ -111,7 +119,7 @@ struct __align__(16) Shared {
     float knorm[kInfo][kKeys];
     float m[2][2][2][kTileRows], s[2][2][2][kTileRows];   // [segment parity][tile][half][row]
     float tmax[2][2][2][kTileRows];                       // [step parity][tile][half][row]
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full[2];
     uint64_t s_full[2][2], s_free[2][2];                  // [tile][buffer]
     uint64_t p_full[2], p_free[2], o_full[2], o_free[2], halves[2];
     uint64_t tile_max[2][4];
@@ -128,8 +136,7 @@ template <int D>
 struct Cfg {
     static constexpr int kTile = kTileRows * D * 2;      // bytes of a tile of q, k or v
     static constexpr int kStages = D == 64 ? 8 : 4;
-    static constexpr int kQBufs = D == 64 ? 2 : 1;
-    static constexpr int kRing = kQBufs * 2 * kTile;
+    static constexpr int kRing = 2 * kTile;              // behind the two tiles of q
     static constexpr int kShared = kRing + kStages * kTile;
     static constexpr int kSmem = kShared + (int)sizeof(Shared) + 1024;
 };
@@ -201,14 +208,14 @@ static __device__ __noinline__ void make_plan(const Args &g) {
         const int pairs = (cnt + g.tokens - 1) / g.tokens;
         long long mine = 0;
 #pragma unroll 1
-        for (int m = 0; m < pairs; ++m) mine += tiles_of_pair(len - cnt, cnt, m * g.tokens, g.tokens);
+        for (int m = 0; m < pairs; ++m) mine += kItemCost + tiles_of_pair(len - cnt, cnt, m * g.tokens, g.tokens);
         long long e = pairs, t = mine * c.Hkv, te, tt;
         block_prefix(e, t, te, tt, part);
         e += entries;
         t += tiles;
 #pragma unroll 1
         for (int m = 0; m < pairs; ++m) {
-            const int nk = tiles_of_pair(len - cnt, cnt, m * g.tokens, g.tokens);
+            const int nk = kItemCost + tiles_of_pair(len - cnt, cnt, m * g.tokens, g.tokens);
             g.s.entries[e++] = make_int4(b, m, nk, (int)t);
             t += (long long)nk * c.Hkv;
         }
@@ -353,8 +360,10 @@ __device__ __forceinline__ void to_z(uint32_t (&r)[32], uint32_t knorm, float a)
     }
 }
 
-// Columns past `last` (relative to this chunk) get no weight.
+// Columns past `last` (relative to this chunk) get no weight.  (The empty instruction keeps the caller's
+// branch: as selects it cost two instructions for each score of every tile.)
 __device__ __forceinline__ void mask(uint32_t (&r)[32], int last, float masked) {
+    asm volatile("");
 #pragma unroll
     for (int j = 0; j < 32; ++j)
         if (j > last) r[j] = __float_as_uint(masked);
@@ -386,28 +395,33 @@ __device__ __forceinline__ void softplus_sum(const uint32_t (&r)[32], float2 &ac
     }
 }
 
-// x[i]^p, 16 values at once.
-__device__ __forceinline__ void powers16(float2 (&x)[8], int p) {
-    if (p == 1) return;
-    float2 r[8];
-    if (p & 1) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = x[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = make_float2(1.f, 1.f);
-    }
+// x[i]^p, 16 values at once (loops over the exponent, the same for all threads; no value is copied).
+__device__ __forceinline__ void powers16(float2 (&x)[8], Power pw) {
+    float2 s[8];
 #pragma unroll 1
-    for (p >>= 1; p; p >>= 1) {
+    for (int c = pw.cubes; c > 0; --c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], __fmul2_rn(x[i], x[i]));
+    }
+    int p = pw.rest;
+#pragma unroll 1
+    for (; !(p & 1); p >>= 1) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], x[i]);
+    }
+    if (p == 1) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = __fmul2_rn(x[i], x[i]);
+#pragma unroll 1
+    for (p >>= 1;;) {
         if (p & 1) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] = __fmul2_rn(r[i], x[i]);
+            for (int i = 0; i < 8; ++i) x[i] = __fmul2_rn(x[i], s[i]);
         }
-    }
+        if ((p >>= 1) == 0) break;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = r[i];
+        for (int i = 0; i < 8; ++i) s[i] = __fmul2_rn(s[i], s[i]);
+    }
 }
 
 // How a warp evaluates its weights (a warp-uniform choice).
@@ -418,10 +432,15 @@ enum Form : int {
                      // softmax: rows whose scores pass 2^16
 };
 
+// Of every 16 pairs, those whose softplus takes the polynomial: the rest of the work leaves the FMA pipe
+// more room in LSSA.
+template <int MODE>
+constexpr int kPolyPairs = MODE == kLssa ? 8 : 4;
+
 // Weights of 16 scores (r[0..15]), summed into acc and packed into 8 words.  `pair0`: number of the
 // first pair in its chunk of 32.
 template <int MODE, bool HALF, int FORM>
-__device__ __forceinline__ void weights16(const uint32_t *r, int pair0, const Row &row, int p, float2 &acc, uint32_t *pk) {
+__device__ __forceinline__ void weights16(const uint32_t *r, int pair0, const Row &row, Power p, float2 &acc, uint32_t *pk) {
     const auto both = [](float x) { return make_float2(x, x); };
     float2 w[8];
 #pragma unroll
@@ -442,7 +461,7 @@ __device__ __forceinline__ void weights16(const uint32_t *r, int pair0, const Ro
             const float2 u = make_float2(ptx::ex2(-fabsf(z.x)), ptx::ex2(-fabsf(z.y)));
             w[i] = ptx::fma_sat2(u, both(row.ck), __ffma2_rn(z, both(row.kappa), both(row.beta)));
         } else {
-            w[i] = poly_pair(pair0 + i, 4) ? sp2x2_poly(z) : tc::sp2x2_direct(z);
+            w[i] = poly_pair(pair0 + i, kPolyPairs<MODE>) ? sp2x2_poly(z) : tc::sp2x2_direct(z);
         }
         if constexpr (is_reweight(MODE) && FORM != kOneExp) {
             // the difference before its scale where it is small against its terms (kAccurate)
@@ -471,7 +490,7 @@ __device__ __forceinline__ void weights16(const uint32_t *r, int pair0, const Ro
 }
 
 template <int MODE, bool HALF>
-__device__ __forceinline__ void weights32(const uint32_t (&r)[32], const Row &row, int form, int p, float2 &acc, uint32_t *pk) {
+__device__ __forceinline__ void weights32(const uint32_t (&r)[32], const Row &row, int form, Power p, float2 &acc, uint32_t *pk) {
     if constexpr (MODE == kLssar) {
         if (form == kOneExp) {
             weights16<MODE, HALF, kOneExp>(r, 0, row, p, acc, pk);
@@ -520,11 +539,16 @@ __device__ __forceinline__ int row_constants(Row &row, float m, float s1, int n,
 // The shared block's members by 32-bit address (one register, constant offsets).
 #define LSSAR_AT(member) (shared + (uint32_t)offsetof(Shared, member))
 
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t shared, unsigned *err, unsigned code, bool honour_abort = true) {
+// A bounded wait that sleeps `nap` ns between polls: warps that poll without a pause took a third of the
+// issue slots from the score warps.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t shared, unsigned *err, unsigned code, uint32_t nap, bool honour_abort = true) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer_ns();
 #pragma unroll 1
-    while (!ptx::mbar_try_wait_sleep(bar, parity, 1000000)) {
+    for (uint32_t spin = 1;; ++spin) {
+        if (nap) __nanosleep(nap);
+        if (ptx::mbar_try_wait_sleep(bar, parity, 1000000)) return true;
+        if ((spin & 63u) != 0) continue;
         if (honour_abort && ptx::ld_shared_s32(LSSAR_AT(abort_flag))) return false;
         if (ptx::globaltimer_ns() - t0 > kWaitLimitNs) {
             atomicCAS(err, 0u, code);
@@ -532,7 +556,6 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint32_t
             return false;
         }
     }
-    return true;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -572,8 +595,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
     if (threadIdx.x == 0) {
         auto init = [](uint64_t *b, uint32_t count) { ptx::mbar_init(ptx::smem_u32(b), count); };
         for (int i = 0; i < 2; ++i) {
-            init(&sh->q_full[i], 1);
-            init(&sh->q_empty[i], 2);
+            init(&sh->q_full[i], 256);
             for (int j = 0; j < 2; ++j) {
                 init(&sh->s_full[i][j], 1);
                 init(&sh->s_free[i][j], 256);
@@ -595,7 +617,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
         }
         for (int i = 0; i < kItems; ++i) {
             init(&sh->item_full[i], 1);
-            init(&sh->item_empty[i], 3 + 16);
+            init(&sh->item_empty[i], 2 + 16);
         }
         sh->abort_flag = 0;
         ptx::fence_mbar_init();
@@ -612,8 +634,9 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
     // the plan, the norms and (kValues) the statistics are there from here on
     ptx::grid_dependency_wait();
 
+    const uint32_t nap = warp == 0 ? kNapProducer : 0u;
     auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) -> bool {
-        return __all_sync(0xffffffffu, wait_bar(bar, parity, shared, err, code));
+        return __all_sync(0xffffffffu, wait_bar(bar, parity, shared, err, code, nap));
     };
     // The next segment, or one with kt0 < 0 at the end; the slot is released by release_item.
     Ring<kItems> items;
@@ -708,9 +731,10 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             while (ok) {
                 const uint32_t slot = items.slot();
                 if (items.reused() && !wait_all(LSSAR_AT(item_empty) + 8 * slot, items.parity() ^ 1, kErrItem)) break;
-                const bool more = t < t1;
+                // (tiles of the item up to the run's end; none where only its cost lies before it)
+                const int kt1 = t < t1 ? (int)min((long long)en.z, kt + t1 - t) - kItemCost : 0;
                 it.kt0 = -1;
-                if (more) {
+                if (kt1 > 0) {
                     const int cnt = a.counts ? a.counts[en.x] : a.n;
                     it.b = en.x;
                     it.h = h;
@@ -718,13 +742,13 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     it.rows = min(g.tokens, cnt - it.t0) * g.G;
                     it.len = c.lens[en.x];
                     it.base = it.len - cnt;
-                    it.nk = en.z;
-                    it.kt0 = kt;
-                    it.kt1 = (int)min((long long)en.z, kt + t1 - t);
+                    it.nk = en.z - kItemCost;
+                    it.kt0 = max(kt - kItemCost, 0);
+                    it.kt1 = kt1;
                     it.item = e * c.Hkv + h;
-                    it.start = en.w + h * en.z;
+                    it.start = en.w + h * en.z + kItemCost;
                     it.first_bad = 0x7fffffff;
-                    if (!dcheck(e < head.entries && h < c.Hkv && it.kt1 > kt && it.rows > 0 && it.rows <= g.rows, err, kDbgItem)) it.kt0 = -1;
+                    if (!dcheck(e < head.entries && h < c.Hkv && it.kt1 > it.kt0 && it.rows > 0 && it.rows <= g.rows, err, kDbgItem)) it.kt0 = -1;
                 }
                 if (lane == 0) {
                     sh->items[slot] = it;
@@ -753,7 +777,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                         if (ok) ok = push(&vm, page, y);
                     }
                 }
-                t += it.kt1 - it.kt0;
+                t += kt1 + kItemCost - kt;
                 kt = 0;
                 if (t < t1 && ++h == c.Hkv) {
                     h = 0;
@@ -762,43 +786,17 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             }
             // no copy may be in flight when the CTA ends
             for (uint32_t i = kv.i > NS ? kv.i - NS : 0; i < kv.i; ++i)
-                wait_bar((LSSAR_AT(kv_full) + 8 * (i % NS)), (i / NS) & 1, shared, err, kErrDrain, false);
+                wait_bar((LSSAR_AT(kv_full) + 8 * (i % NS)), (i / NS) & 1, shared, err, kErrDrain, nap, false);
             if constexpr (kNorm)
                 for (uint32_t i = info.i > kInfo ? info.i - kInfo : 0; i < info.i; ++i)
-                    wait_bar((LSSAR_AT(info_full) + 8 * (i % kInfo)), (i / kInfo) & 1, shared, err, kErrDrain, false);
+                    wait_bar((LSSAR_AT(info_full) + 8 * (i % kInfo)), (i / kInfo) & 1, shared, err, kErrDrain, nap, false);
             __syncwarp();
-        } else if (warp == 3) {
-            // ------------------------------------------------------------ rows of q
-            Ring<C::kQBufs> q;
-            Item it;
-            constexpr int kLanes = D / 8, kStep = 32 / kLanes;
-            const int chunk = lane % kLanes;
-            const uint32_t column = (chunk >> 3) * (kTileRows * 128);
-            while (next_item(it)) {
-                release_item();
-                if (q.reused() && !wait_all(LSSAR_AT(q_empty) + 8 * q.slot(), q.parity() ^ 1, kErrQ)) break;
-                const uint16_t *src = static_cast<const uint16_t *>(a.q) + it.b * a.qs[0] + (long long)it.h * g.G * a.qs[1] + it.t0 * a.qs[2] + chunk * 8;
-                const uint32_t dst = sq + q.slot() * 2 * TB + column;
-                const int rows = it.rows > kTileRows ? kPairRows : kTileRows;
-#pragma unroll 8
-                for (int r = lane / kLanes; r < rows; r += kStep) {
-                    const int v = min(r, it.rows - 1), tok = v / g.G, head = v - tok * g.G;
-                    cp_async16(dst + (r >> 7) * TB + (r & 127) * 128 + (((chunk & 7) ^ (r & 7)) << 4), src + head * a.qs[1] + tok * a.qs[2]);
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(LSSAR_AT(q_full) + 8 * q.slot());
-                ++q.i;
-            }
-            __syncwarp();
-        } else {
+        } else if (warp < 3) {
             // ------------------------------------------------------------ MMA of tile w
             const int w = warp - 1;
             Ring<NS> kv;
-            Ring<C::kQBufs> q;
             Ring<kSBufs> sb;               // S of this tile
-            uint32_t pv = 0, segs = 0;     // P.V products issued, segments with this tile
+            uint32_t pv = 0, qs = 0, segs = 0;     // P.V products issued; q tiles taken, segments ended, of this tile
             bool ok = true;
             auto commit = [&](uint32_t bar) {
                 if (ptx::elect_one()) ptx::mma_commit(bar);
@@ -814,13 +812,12 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             const uint64_t dq0 = ptx::smem_desc_sw128(sq, tc::kKmajorLbo, tc::kKmajorSbo);
             const uint64_t dk0 = ptx::smem_desc_sw128(ring, tc::kKmajorLbo, tc::kKmajorSbo);
             const uint64_t dv0 = ptx::smem_desc_sw128(ring, tc::kVLbo, tc::kVSbo);
-            uint32_t qoff = 0;
             // S = q k^T of the K tile in kslot (its buffer is free once the score warps have read it)
             auto issue_s = [&](uint32_t kslot) -> bool {
                 const uint32_t buf = sb.slot();
                 if (sb.reused() && !wait_all((LSSAR_AT(s_free) + 16 * (w) + 8 * (buf)), sb.parity() ^ 1, kErrSFree)) return false;
                 ptx::tc_fence_after();
-                const uint64_t dq = dq0 + (uint64_t)((qoff + w * TB) >> 4), dk = dk0 + (uint64_t)((kslot * TB) >> 4);
+                const uint64_t dq = dq0 + (uint64_t)((w * TB) >> 4), dk = dk0 + (uint64_t)((kslot * TB) >> 4);
                 const uint32_t full = (LSSAR_AT(s_full) + 16 * (w) + 8 * (buf));
                 const uint32_t col = tmem + (PHASE == kStats ? w * 256 + buf * kKeys : w * kKeys);
                 dcheck(tmem_in_range(col, tmem, kKeys, 512), err, kDbgTmem);
@@ -864,8 +861,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             while (ok && next_item(it)) {
                 release_item();
                 const bool live = it.rows > w * kTileRows;
-                if (!(ok = wait_all(LSSAR_AT(q_full) + 8 * q.slot(), q.parity(), kErrQ))) break;
-                qoff = q.slot() * 2 * TB;
+                if (live && !(ok = wait_all(LSSAR_AT(q_full) + 8 * w, qs++ & 1, kErrQ))) break;
                 ptx::tc_fence_after();
                 uint32_t kslot, vslot;
                 if constexpr (PHASE == kStats) {
@@ -902,21 +898,18 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                             }
                             issue_pv(vslot, kt > it.kt0);
                             ++pv;
+                            // (what the score warps wait for first: a commit takes some 300 cycles)
                             if constexpr (kSepP) commit(LSSAR_AT(p_free) + 8 * w);
+                            else if (next && !(ok = issue_s(kslot))) break;
                             if (!next) {
                                 commit(LSSAR_AT(o_full) + 8 * w);
                                 ++segs;
                             }
                         }
                         commit(LSSAR_AT(kv_empty) + 8 * vslot);
-                        if constexpr (!kSepP) {
-                            if (live && next && !(ok = issue_s(kslot))) break;
-                            if (next) commit(LSSAR_AT(kv_empty) + 8 * kslot);
-                        }
+                        if (!kSepP && next) commit(LSSAR_AT(kv_empty) + 8 * kslot);
                     }
                 }
-                commit(LSSAR_AT(q_empty) + 8 * q.slot());
-                ++q.i;
             }
             __syncwarp();
         }
@@ -953,6 +946,36 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 ++info.i;
             }
         };
+        // The next segment's rows of q (any strides, any group): each thread half of its row, into the tile
+        // that the last product of the segment before has read.  Returns whether this tile has any.
+        auto gather = [&](uint32_t slot, bool &some) -> bool {
+            const uint32_t it = LSSAR_AT(items) + slot % kItems * (uint32_t)sizeof(Item);
+            if (!wait_all(LSSAR_AT(item_full) + 8 * (slot % kItems), slot / kItems & 1, kErrItem)) return false;
+            auto next = [&](size_t offset) { return ptx::ld_shared_s32(it + (uint32_t)offset); };
+            const int rows = next(offsetof(Item, rows));
+            some = next(offsetof(Item, kt0)) >= 0 && rows > w * kTileRows;
+            if (!some) return true;
+            const int v = min(w * kTileRows + in, rows - 1), tok = v / g.G, head = next(offsetof(Item, h)) * g.G + v - tok * g.G;
+            const uint16_t *src = static_cast<const uint16_t *>(a.q) + next(offsetof(Item, b)) * a.qs[0] + head * a.qs[1] +
+                                  (next(offsetof(Item, t0)) + tok) * a.qs[2] + half * (D / 2);
+            const uint32_t dst = sq + w * TB + (D == 128 ? half * (kTileRows * 128) : 0) + in * 128;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+                const int piece = D == 128 ? x : half * 4 + x;
+                cp_async16(dst + ((piece ^ (in & 7)) << 4), src + x * 8);
+            }
+            return true;
+        };
+        // ... they are there
+        auto hand_over = [&](bool some) {
+            if (!some) return;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            ptx::fence_proxy_async_smem();
+            ptx::mbar_arrive(LSSAR_AT(q_full) + 8 * w);
+        };
+        bool some = false;
+        ok = gather(0, some);
+        if (ok) hand_over(some);
         // 32 products of the tile from column 32 x of this half on, as they are
         auto load = [&](uint32_t (&z)[32], uint32_t col) {
             ptx::tmem_ld32(col, z);
@@ -968,6 +991,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     ok = take_norms();
                     leave_norms();
                 }
+                if (ok && (ok = gather(items.i + 1, some))) hand_over(some);
                 release_item();
                 continue;
             }
@@ -1012,6 +1036,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 if (!(ok = wait_all(s_full + 8 * buf, sb.parity(), kErrSFull))) break;
                 ++sb.i;
                 ptx::tc_fence_after();
+                if (kt + 1 == kt1 && !(ok = gather(items.i + 1, some))) break;      // (the last product with this q is done)
                 if (!live) {
                     // none of the item's rows: the barriers only
                     ptx::tc_fence_before();
@@ -1126,7 +1151,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     }
                     if constexpr (MODE != kSoftmax) to_z<kNorm>(z, knorm + x * 128, row.a);
                     if (masked) mask(z, last - x * 32, kMasked);
-                    weights32<MODE, HALF>(z, row, form, a.p, acc, pk);
+                    weights32<MODE, HALF>(z, row, form, g.power, acc, pk);
                     if constexpr (kSepP) {
                         // P and O are free once the product before has read the one and written the other
                         if (x == 0 && pv > 0) {
@@ -1162,6 +1187,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 ++pv;
             }
             if (!ok) break;
+            hand_over(some);
             // the two halves of a row meet
             const uint32_t par = segs & 1;
             const float part = (acc.x + acc.y) + sum_run;
@@ -1189,10 +1215,10 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             if (!(ok = wait_all(LSSAR_AT(o_full) + 8 * w, segs & 1, kErrOFull))) break;
             ++segs;
             ptx::tc_fence_after();
-            const int b = LSSAR_ITEM(b), hq = LSSAR_ITEM(h) * g.G + v % g.G, t = LSSAR_ITEM(t0) + v / g.G, start = LSSAR_ITEM(start);
+            const int b = LSSAR_ITEM(b), hq = LSSAR_ITEM(h) * g.G + v % g.G, t = LSSAR_ITEM(t0) + v / g.G;
             const bool whole = kt0 == 0 && kt1 == LSSAR_ITEM(nk);
             // a segment's part: of the run's first item in its first place, of its last in its second
-            const int place = 2 * blockIdx.x + (kt0 == 0 && start != (long long)blockIdx.x * run ? 1 : 0);
+            const int place = 2 * blockIdx.x + (kt0 == 0 ? 1 : 0);
             const size_t to = (size_t)place * g.rows + v;
             const bool in_range = dcheck(b < c.B && hq < a.H && t < a.n && v < g.rows && place < 2 * g.ctas, err, kDbgGlobal);
             const float inv = 1.f / sum;
@@ -1253,11 +1279,11 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const __grid_constan
     const long long x = (long long)cta * head.run;
     if (x >= head.total) return;
     const int4 en = g.s.entries[g.s.first[cta]];
-    const int h = (int)(x - en.w) / en.z, start = en.w + h * en.z;
-    if (start == x || x - head.run > start) return;
-    const int last = (start + en.z - 1) / head.run, cnt = a.counts ? a.counts[en.x] : a.n, t0 = en.y * g.tokens;
+    // the item's first tile, behind its cost
+    const int h = (int)(x - en.w) / en.z, start = en.w + h * en.z + kItemCost;
+    if (start >= x || x - head.run > start) return;
+    const int last = (start + en.z - kItemCost - 1) / head.run, cnt = a.counts ? a.counts[en.x] : a.n, t0 = en.y * g.tokens;
     const int rows = min(g.tokens, cnt - t0) * g.G;
-    const int own = 2 * (cta - 1) + (start != x - head.run);       // the first run's place
     constexpr int kLanes = D / 4, kStep = kJoinThreads / kLanes;
     const int part = threadIdx.x % kLanes;
 #pragma unroll 1
@@ -1266,7 +1292,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const __grid_constan
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int k = cta - 1; k <= last; ++k) {
-            const size_t at = (size_t)(k == cta - 1 ? own : 2 * k) * g.rows + r;
+            const size_t at = (size_t)(2 * k + (k == cta - 1)) * g.rows + r;      // its first segment in the second place
             const float2 s = g.s.sums[at];
             const float4 v = reinterpret_cast<const float4 *>(g.s.o + at * D)[part];
             float f = 1.f;
