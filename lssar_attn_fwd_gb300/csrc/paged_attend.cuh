@@ -55,14 +55,18 @@ constexpr int kScoreWarp0 = 4;
 // (128 x 64 + 512 x 104 = 640 x 96).
 constexpr int kLaunchRegs = 96, kCtrlRegs = 64, kScoreRegs = 104;
 static_assert(128 * kCtrlRegs + 512 * kScoreRegs <= kThreads * kLaunchRegs, "register split");
-constexpr int kInfo = 4;                      // tiles whose key norms are in shared memory
+// Tiles whose key norms are in shared memory.  They come with the tile's keys, and their slot is used again 16
+// tiles later: the stage of tile j's keys was given up by both MMA warps after they issued the scores of a
+// tile j - 8 or later, for which the score warps had read the scores of the tile two before, and the norms of
+// the one before that (kStats, d = 64; the others leave fewer tiles between).
+constexpr int kInfo = 16;
 constexpr int kItems = 4;                     // depth of the queue of segments
 constexpr int kItemCost = 2;                  // what an item costs beside its tiles, in tiles (they are numbered before its first)
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint32_t kNapProducer = 200;   // ns between its polls of a barrier
 constexpr float kLowest = -3.0e38f;           // below every score, and finite
 enum : unsigned { kErrItem = 61, kErrQ, kErrKvFull, kErrKvEmpty, kErrSFull, kErrSFree, kErrPFull, kErrPFree, kErrOFull, kErrOFree,
-                  kErrInfo, kErrHalves, kErrTileMax, kErrDrain };
+                  kErrHalves, kErrTileMax, kErrDrain };
 
 // One-pass modes: log2 of the largest weight of a row lies in kRoom + [0, kLag] (fp16, whose
 // least step is 2^-24, needs the room; softplus up to 117 leaves less of it).
@@ -89,9 +93,9 @@ struct Scratch {
     float *o;             // [2 cta + last][rows][d]: sum of w v
 };
 
-// The exponent as 3^cubes * rest, so that p = 15 takes five products.
+// The exponent, itself and as 3^cubes * rest.
 struct Power {
-    int cubes, rest;
+    int exact, cubes, rest;
 };
 
 struct Args {
@@ -124,7 +128,6 @@ struct __align__(16) Shared {
     uint64_t p_full[2], p_free[2], o_full[2], o_free[2], halves[2];
     uint64_t tile_max[2][4];
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t info_full[kInfo], info_empty[kInfo];
     uint64_t item_full[kItems], item_empty[kItems];
     Item items[kItems];
     unsigned absent[8];   // per stage of V: groups of 8 rows that no copy has filled
@@ -395,8 +398,23 @@ __device__ __forceinline__ void softplus_sum(const uint32_t (&r)[32], float2 &ac
     }
 }
 
-// x[i]^p, 16 values at once (loops over the exponent, the same for all threads; no value is copied).
+// x[i]^p, 16 values at once.  P = 3 and 15, the exponents of the method's own results, unrolled; others by loops
+// over 3^cubes * rest, the same for all threads (their branches cost two instructions for each score).
+template <int P>
 __device__ __forceinline__ void powers16(float2 (&x)[8], Power pw) {
+    if constexpr (P == 3 || P == 15) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 c = __fmul2_rn(x[i], __fmul2_rn(x[i], x[i]));
+            if constexpr (P == 3) {
+                x[i] = c;
+            } else {
+                const float2 d = __fmul2_rn(c, c);
+                x[i] = __fmul2_rn(c, __fmul2_rn(d, d));
+            }
+        }
+        return;
+    }
     float2 s[8];
 #pragma unroll 1
     for (int c = pw.cubes; c > 0; --c) {
@@ -439,7 +457,7 @@ constexpr int kPolyPairs = MODE == kLssa ? 8 : 4;
 
 // Weights of 16 scores (r[0..15]), summed into acc and packed into 8 words.  `pair0`: number of the
 // first pair in its chunk of 32.
-template <int MODE, bool HALF, int FORM>
+template <int MODE, bool HALF, int FORM, int P>
 __device__ __forceinline__ void weights16(const uint32_t *r, int pair0, const Row &row, Power p, float2 &acc, uint32_t *pk) {
     const auto both = [](float x) { return make_float2(x, x); };
     float2 w[8];
@@ -476,7 +494,7 @@ __device__ __forceinline__ void weights16(const uint32_t *r, int pair0, const Ro
         }
     }
     if constexpr (is_reweight(MODE)) {
-        powers16(w, p);
+        powers16<P>(w, p);
         if constexpr (HALF) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = __fmul2_rn(w[i], both(kTopFp16));
@@ -489,22 +507,28 @@ __device__ __forceinline__ void weights16(const uint32_t *r, int pair0, const Ro
     }
 }
 
+template <int MODE, bool HALF, int FORM, int P>
+__device__ __forceinline__ void weights32(const uint32_t (&r)[32], const Row &row, Power p, float2 &acc, uint32_t *pk) {
+    weights16<MODE, HALF, FORM, P>(r, 0, row, p, acc, pk);
+    weights16<MODE, HALF, FORM, P>(r + 16, 8, row, p, acc, pk + 8);
+}
+
 template <int MODE, bool HALF>
 __device__ __forceinline__ void weights32(const uint32_t (&r)[32], const Row &row, int form, Power p, float2 &acc, uint32_t *pk) {
-    if constexpr (MODE == kLssar) {
-        if (form == kOneExp) {
-            weights16<MODE, HALF, kOneExp>(r, 0, row, p, acc, pk);
-            weights16<MODE, HALF, kOneExp>(r + 16, 8, row, p, acc, pk + 8);
-            return;
-        }
-    }
     if (form == kAccurate) {
-        weights16<MODE, HALF, kAccurate>(r, 0, row, p, acc, pk);
-        weights16<MODE, HALF, kAccurate>(r + 16, 8, row, p, acc, pk + 8);
-        return;
+        weights32<MODE, HALF, kAccurate, 0>(r, row, p, acc, pk);
+    } else if (!is_reweight(MODE)) {
+        weights32<MODE, HALF, kMixed, 0>(r, row, p, acc, pk);
+    } else if (MODE == kLssar && form == kOneExp) {
+        if (p.exact == 15) weights32<MODE, HALF, kOneExp, 15>(r, row, p, acc, pk);
+        else weights32<MODE, HALF, kOneExp, 0>(r, row, p, acc, pk);
+    } else if (p.exact == 15) {
+        weights32<MODE, HALF, kMixed, 15>(r, row, p, acc, pk);
+    } else if (p.exact == 3) {
+        weights32<MODE, HALF, kMixed, 3>(r, row, p, acc, pk);
+    } else {
+        weights32<MODE, HALF, kMixed, 0>(r, row, p, acc, pk);
     }
-    weights16<MODE, HALF, kMixed>(r, 0, row, p, acc, pk);
-    weights16<MODE, HALF, kMixed>(r + 16, 8, row, p, acc, pk + 8);
 }
 
 // Constants of a re-weighted row from its maximum and normaliser sum; returns the form that it
@@ -611,10 +635,6 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             init(&sh->kv_full[i], 1);
             init(&sh->kv_empty[i], 2);
         }
-        for (int i = 0; i < kInfo; ++i) {
-            init(&sh->info_full[i], 1);
-            init(&sh->info_empty[i], 16);
-        }
         for (int i = 0; i < kItems; ++i) {
             init(&sh->item_full[i], 1);
             init(&sh->item_empty[i], 2 + 16);
@@ -664,7 +684,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             const int t1 = min((long long)head.total, (long long)(blockIdx.x + 1) * head.run);
             long long t = (long long)blockIdx.x * head.run;
             Ring<NS> kv;
-            Ring<kInfo> info;
+            uint32_t info = 0;             // tiles of keys asked for
             bool ok = true;
             int pg = -1, row = 0;          // of this lane's piece of the tile asked for: page (-1 past the end, -2 no page), row
             Item it = {};
@@ -676,7 +696,8 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 pg = paged_page(c, it.b, i);
                 if (pg < 0) pg = -2;
             };
-            auto push = [&](const CUtensorMap *map, int page, int y) -> bool {
+            // (norms: the tile whose keys these are, -1 for values)
+            auto push = [&](const CUtensorMap *map, int page, int y, int norms) -> bool {
                 const uint32_t s = kv.slot();
                 if (kv.reused() && !wait_all(LSSAR_AT(kv_empty) + 8 * s, kv.parity() ^ 1, kErrKvEmpty)) return false;
                 const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
@@ -687,8 +708,14 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     for (int i = 0; i * piece_rows < kKeys; ++i)
                         if (there >> i & 1) absent &= ~(((1u << groups) - 1) << (i * groups));
                     sh->absent[s] = absent;
-                    ptx::mbar_arrive_expect_tx(full, (uint32_t)__popc(there) * piece_rows * D * 2);
+                    ptx::mbar_arrive_expect_tx(full, (uint32_t)__popc(there) * piece_rows * D * 2 + (kNorm && norms >= 0 ? kKeys * 4 : 0));
+                    if (kNorm && norms >= 0) {
+                        const long long at = ((long long)it.b * c.Hkv + it.h) * g.cap128 + (long long)norms * kKeys;
+                        if (dcheck((norms + 1) * kKeys <= g.cap128 && it.b < c.B, err, kDbgBulk))
+                            ptx::bulk_load(LSSAR_AT(knorm) + info % kInfo * (kKeys * 4), g.s.knorm + at, kKeys * 4, full);
+                    }
                 }
+                if (norms >= 0) ++info;
                 __syncwarp();
                 if (page >= 0 && dcheck(y >= 0 && y + piece_rows <= c.Hkv * ps && page < c.n_pages, err, kDbgTma)) {
                     ptx::tma_load_3d(dst, map, full, 0, y, page);
@@ -698,18 +725,6 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 return true;
             };
             auto push_keys = [&](int kt, int slot) -> bool {
-                if constexpr (kNorm) {
-                    const uint32_t s = info.slot(), full = (LSSAR_AT(info_full) + 8 * s);
-                    if (info.reused() && !wait_all(LSSAR_AT(info_empty) + 8 * s, info.parity() ^ 1, kErrInfo)) return false;
-                    const long long at = ((long long)it.b * c.Hkv + it.h) * g.cap128 + (long long)kt * kKeys;
-                    const bool in = dcheck(kt >= 0 && (kt + 1) * kKeys <= g.cap128 && it.b < c.B, err, kDbgBulk);
-                    if (ptx::elect_one()) {
-                        ptx::mbar_arrive_expect_tx(full, kKeys * 4);
-                        if (in) ptx::bulk_load(LSSAR_AT(knorm) + s * (kKeys * 4), g.s.knorm + at, kKeys * 4, full);
-                    }
-                    __syncwarp();
-                    ++info.i;
-                }
                 // the first slot of a page that is none
                 if (__any_sync(0xffffffffu, pg == -2)) {
                     const int first = __reduce_min_sync(0xffffffffu, pg == -2 ? kt * kKeys + lane * piece_rows : 0x7fffffff);
@@ -718,7 +733,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                         *bad = min(*bad, first);
                     }
                 }
-                return push(&km, pg, row);
+                return push(&km, pg, row, kt);
             };
             int e = 0, h = 0, kt = 0;
             int4 en = make_int4(0, 0, 0, 0);
@@ -774,7 +789,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                             vrow = row;
                             ok = push_keys(k + 1, slot);
                         }
-                        if (ok) ok = push(&vm, page, y);
+                        if (ok) ok = push(&vm, page, y, -1);
                     }
                 }
                 t += kt1 + kItemCost - kt;
@@ -787,9 +802,6 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             // no copy may be in flight when the CTA ends
             for (uint32_t i = kv.i > NS ? kv.i - NS : 0; i < kv.i; ++i)
                 wait_bar((LSSAR_AT(kv_full) + 8 * (i % NS)), (i / NS) & 1, shared, err, kErrDrain, nap, false);
-            if constexpr (kNorm)
-                for (uint32_t i = info.i > kInfo ? info.i - kInfo : 0; i < info.i; ++i)
-                    wait_bar((LSSAR_AT(info_full) + 8 * (i % kInfo)), (i / kInfo) & 1, shared, err, kErrDrain, nap, false);
             __syncwarp();
         } else if (warp < 3) {
             // ------------------------------------------------------------ MMA of tile w
@@ -930,22 +942,12 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
         constexpr uint32_t kParity = 4 * kTileRows * 4;
         constexpr float kMasked = MODE == kSigmoidRw ? INFINITY : -INFINITY;
         Ring<kSBufs> sb;
-        Ring<kInfo> info;
-        uint32_t pv = 0, segs = 0, steps = 0, exchanges = 0;
+        uint32_t pv = 0, segs = 0, exchanges = 0;
+        uint32_t tiles = 0;            // tiles of keys that the CTA has taken
         const int run = g.s.head->run;
         bool ok = true;
         auto field = [&](size_t offset) { return ptx::ld_shared_s32(LSSAR_AT(items) + items.slot() * (uint32_t)sizeof(Item) + (uint32_t)offset); };
 #define LSSAR_ITEM(name) field(offsetof(Item, name))
-        auto take_norms = [&] {        // the tile's key norms are there
-            return !kNorm || wait_all(LSSAR_AT(info_full) + 8 * info.slot(), info.parity(), kErrInfo);
-        };
-        auto leave_norms = [&] {       // they have been read
-            if constexpr (kNorm) {
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(LSSAR_AT(info_empty) + 8 * info.slot());
-                ++info.i;
-            }
-        };
         // The next segment's rows of q (any strides, any group): each thread half of its row, into the tile
         // that the last product of the segment before has read.  Returns whether this tile has any.
         auto gather = [&](uint32_t slot, bool &some) -> bool {
@@ -987,11 +989,8 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             const int kt0 = LSSAR_ITEM(kt0), kt1 = LSSAR_ITEM(kt1), rows = LSSAR_ITEM(rows);
             if (kt0 < 0) break;
             if (rows <= w * kTileRows) {                         // none of this tile's
-                for (int kt = kt0; ok && kt < kt1; ++kt) {
-                    ok = take_norms();
-                    leave_norms();
-                }
-                if (ok && (ok = gather(items.i + 1, some))) hand_over(some);
+                tiles += kt1 - kt0;
+                if ((ok = gather(items.i + 1, some))) hand_over(some);
                 release_item();
                 continue;
             }
@@ -1031,7 +1030,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             }
             float m_run = MODE == kSigmoidRw ? INFINITY : MODE == kLssar ? kLowest : -INFINITY, sum_run = 0.f;
             float2 acc = make_float2(0.f, 0.f);
-            for (int kt = kt0; kt < kt1; ++kt, ++steps) {
+            for (int kt = kt0; kt < kt1; ++kt, ++tiles) {
                 const uint32_t buf = sb.slot(), col = s_col + buf * kKeys;
                 if (!(ok = wait_all(s_full + 8 * buf, sb.parity(), kErrSFull))) break;
                 ++sb.i;
@@ -1041,8 +1040,6 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     // none of the item's rows: the barriers only
                     ptx::tc_fence_before();
                     if constexpr (PHASE == kStats || kSepP) ptx::mbar_arrive(s_free + 8 * buf);
-                    if (!(ok = take_norms())) break;
-                    leave_norms();
                     if constexpr (PHASE == kValues) {
                         // (not before the last step's arrivals are all in, which its product follows)
                         if (kSepP && pv > 0 && !(ok = wait_all(p_free, (pv - 1) & 1, kErrPFree))) break;
@@ -1051,8 +1048,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     }
                     continue;
                 }
-                if (!(ok = take_norms())) break;
-                const uint32_t knorm = LSSAR_AT(knorm) + info.slot() * (kKeys * 4) + half * 256;
+                const uint32_t knorm = LSSAR_AT(knorm) + tiles % kInfo * (kKeys * 4) + half * 256;
                 const int last = limit - kt * kKeys - half * 64;      // last column of the half that is not masked
                 const bool masked = least < kt * kKeys + half * 64 + 63;
                 if constexpr (PHASE == kStats) {
@@ -1066,7 +1062,6 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     ptx::mbar_arrive(s_free + 8 * buf);               // the next product may write here
                     to_z<kNorm>(r0, knorm, row.a);
                     to_z<kNorm>(r1, knorm + 128, row.a);
-                    leave_norms();
                     if (masked) {
                         mask(r0, last, kMasked);
                         mask(r1, last - 32, kMasked);
@@ -1141,13 +1136,20 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                         if constexpr (MODE == kSoftmax) form = __any_sync(0xffffffffu, fabsf(row.ref) > 65536.f) ? kAccurate : kMixed;
                     }
                 }
-#pragma unroll 1
+                uint32_t zz[2][32];
+                load(zz[0], col);
+                ptx::tmem_ld32(col + 32, zz[1]);                      // on its way while the first is weighted
+#pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    uint32_t z[32], pk[16];
-                    load(z, col + x * 32);
-                    if (kSepP && x == 1) {
-                        ptx::tc_fence_before();
-                        ptx::mbar_arrive(s_free);                     // the next product may write here
+                    uint32_t (&z)[32] = zz[x];
+                    uint32_t pk[16];
+                    if (x == 1) {
+                        ptx::tmem_ld_wait();
+                        ptx::reg_fence(z);
+                        if (kSepP) {
+                            ptx::tc_fence_before();
+                            ptx::mbar_arrive(s_free);                 // the next product may write here
+                        }
                     }
                     if constexpr (MODE != kSoftmax) to_z<kNorm>(z, knorm + x * 128, row.a);
                     if (masked) mask(z, last - x * 32, kMasked);
@@ -1162,7 +1164,6 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     ptx::tmem_st16(p_col + x * 16, pk);
                 }
                 if (!ok) break;
-                leave_norms();
                 // (the tile that raised the last row to 0 was still weighted in the accurate form)
                 if constexpr (MODE == kLssa) {
                     if (form == kAccurate && __all_sync(0xffffffffu, row.ref >= 0.f)) form = kMixed;
