@@ -6,7 +6,7 @@ namespace {
 
 struct Layout {
     int G, tokens, ctas, rows, cap128;
-    size_t entries, first, knorm, qscale, stats, sums, o, total;   // the header first
+    size_t entries, first, knorm, stats, sums, o, total;   // the header first
 };
 
 Layout layout(const PagedAttend &pr, int sms) {
@@ -23,8 +23,7 @@ Layout layout(const PagedAttend &pr, int sms) {
     l.entries = 256;
     l.first = l.entries + r(pairs * sizeof(int4));
     l.knorm = l.first + r((size_t)l.ctas * 4);
-    l.qscale = l.knorm + (norms ? r((size_t)c.B * c.Hkv * l.cap128 * 4) : 0);
-    l.stats = l.qscale + (norms ? r((size_t)c.B * pr.H * pr.n * 4) : 0);
+    l.stats = l.knorm + (norms ? r((size_t)c.B * c.Hkv * l.cap128 * 4) : 0);
     l.sums = l.stats + (reweight ? r((items + l.ctas) * l.rows * 8) : 0);
     l.o = l.sums + r((size_t)2 * l.ctas * l.rows * 8);
     l.total = l.o + r((size_t)2 * l.ctas * l.rows * c.d * 4);
@@ -53,7 +52,6 @@ cudaError_t launch_paged_attend(const PagedAttend &pr, void *ws, int sms, cudaSt
     g.s.entries = reinterpret_cast<int4 *>(base + l.entries);
     g.s.first = reinterpret_cast<int *>(base + l.first);
     g.s.knorm = reinterpret_cast<float *>(base + l.knorm);
-    g.s.qscale = reinterpret_cast<float *>(base + l.qscale);
     g.s.stats = reinterpret_cast<float2 *>(base + l.stats);
     g.s.sums = reinterpret_cast<float2 *>(base + l.sums);
     g.s.o = reinterpret_cast<float *>(base + l.o);
@@ -70,6 +68,7 @@ cudaError_t launch_paged_attend(const PagedAttend &pr, void *ws, int sms, cudaSt
     g.power = {pr.p, 0, pr.p};
     for (; g.power.rest % 3 == 0; g.power.rest /= 3) ++g.power.cubes;
     g.idesc_s = ptx::idesc_f16(!c.half, attend::kTileRows, attend::kKeys, false, false);
+    g.idesc_s64 = ptx::idesc_f16(!c.half, attend::kTileRows, 64, false, false);
     g.idesc_pv = ptx::idesc_f16(!c.half, attend::kTileRows, c.d, false, true);
     CUtensorMap km, vm;
     if (!make_page_map(&km, c.k, c.half, c.d, c.Hkv * c.page_size, c.n_pages, c.page_stride, g.piece_rows) ||

@@ -7,7 +7,7 @@
 //   w = phi, or re-weighted max(kappa (phi - theta), 0)^p, theta = O S1 / i,
 //   kappa = 1 / (phi(m) - theta);  out = sum w v / sum w.
 // Scores are products of the inputs' own bits, scaled in fp32 afterwards: 1/|k| of each cached
-// key and the factor of each query row come from a prologue that reads both once.
+// key comes from a prologue that reads them once, |q| from the gathered rows.
 //
 // What bounds it: the score warps.  Each score costs about 10 issue slots in the
 // re-weighting modes (two passes), against 4d flops of tensor work and, at 256 rows per
@@ -87,7 +87,6 @@ struct Scratch {
     int4 *entries;        // {sequence, pair, tiles of the pair and its cost, number of the first of them}
     int *first;           // [ctas] entry of each CTA's first tile
     float *knorm;         // [B, Hkv, cap128] 1 / |k|
-    float *qscale;        // [B, H, n] factor of a query row's scores
     float2 *stats;        // [item + cta][rows]: m, S1 of a segment's rows
     float2 *sums;         // [2 cta + last][rows]: reference, sum of w
     float *o;             // [2 cta + last][rows][d]: sum of w v
@@ -107,7 +106,7 @@ struct Args {
     int piece_rows;       // rows of a page per copy
     float scale;          // log2e / sqrt(d), or +-log2e ln d
     Power power;
-    uint32_t idesc_s, idesc_pv;
+    uint32_t idesc_s, idesc_s64, idesc_pv;     // scores of 128 keys, of 64; sum of w v
 };
 
 // A segment as the roles of a CTA see it.
@@ -121,10 +120,11 @@ struct Item {
 
 struct __align__(16) Shared {
     float knorm[kInfo][kKeys];
-    float m[2][2][2][kTileRows], s[2][2][2][kTileRows];   // [segment parity][tile][half][row]
+    float m[2][2][2][kTileRows], s[2][2][2][kTileRows];   // [meeting parity][tile][half][row]
+    float qq[2][2][2][kTileRows];                         // sum of squares of the next row of q, likewise
     float tmax[2][2][2][kTileRows];                       // [step parity][tile][half][row]
     uint64_t q_full[2];
-    uint64_t s_full[2][2], s_free[2][2];                  // [tile][buffer]
+    uint64_t s_full[2][2], s_free[2][2];                  // [tile][buffer], or (kSplit) [tile][half]
     uint64_t p_full[2], p_free[2], o_full[2], o_free[2], halves[2];
     uint64_t tile_max[2][4];
     uint64_t kv_full[8], kv_empty[8];
@@ -149,6 +149,19 @@ static_assert(Cfg<64>::kSmem <= 232448 && Cfg<128>::kSmem <= 232448, "shared mem
 __host__ __device__ __forceinline__ int tiles_of_pair(int base, int count, int t0, int tokens) {
     const int last = t0 + tokens < count ? t0 + tokens : count;     // tokens up to the pair's end
     return (base + last + kKeys - 1) / kKeys;
+}
+
+// Sum of squares of 8 elements.
+__device__ __forceinline__ float squares(uint4 x, bool half) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = half ? __half22float2(*reinterpret_cast<const __half2 *>(&u[i]))
+                              : make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+        s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
+    }
+    return s;
 }
 
 // ---------------------------------------------------------------- prologue
@@ -252,21 +265,8 @@ static __device__ __noinline__ void make_plan(const Args &g) {
     }
 }
 
-// Sum of squares of 8 elements.
-__device__ __forceinline__ float squares(uint4 x, bool half) {
-    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = half ? __half22float2(*reinterpret_cast<const __half2 *>(&u[i]))
-                              : make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
-        s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
-    }
-    return s;
-}
-
-// Block 0 plans; the others, in the normalised modes, take runs of key rows (1 / |k|) and of query
-// rows (factor of the row's scores).  2d bytes of each are read once, by d / 8 lanes a row.
+// Block 0 plans; the others, in the normalised modes, take runs of key rows: 1 / |k|.  2d bytes of each are
+// read once, by d / 8 lanes a row.
 template <int D>
 __global__ void __launch_bounds__(kPrepThreads) attend_prepare(const __grid_constant__ Args g, int norms) {
     ptx::launch_dependents();
@@ -306,23 +306,6 @@ __global__ void __launch_bounds__(kPrepThreads) attend_prepare(const __grid_cons
             }
             if (++p.tile == p.nt && t + 1 < t1) paged::next_row<D>(c, 1, p);
         }
-    }
-    // queries
-    const long long rows = (long long)c.B * a.H * a.n;
-#pragma unroll 1
-    for (long long r = (long long)blk * kRows + in; r - in < rows; r += (long long)blocks * kRows) {
-        float s = 0.f, f = 0.f;
-        if (r < rows) {
-            const int t = (int)(r % a.n), hq = (int)(r / a.n % a.H), b = (int)(r / a.n / a.H);
-            const int cnt = a.counts ? a.counts[b] : a.n;
-            if (t < cnt && t < a.n) {
-                s = squares(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + b * a.qs[0] + hq * a.qs[1] + t * a.qs[2] + part * 8), c.half);
-                f = g.scale * logf((float)(c.lens[b] - cnt + t + 1));
-            }
-        }
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (part == 0 && r < rows) g.s.qscale[r] = f / fmaxf(sqrtf(s), 1e-12f);
     }
 }
 
@@ -604,6 +587,10 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
     constexpr bool kOnePass = MODE == kSoftmax || MODE == kLssa;
     constexpr bool kSepP = D == 64;
     constexpr int kSBufs = PHASE == kStats ? 2 : 1;
+    // kValues, d = 128: P lies over S, so that a product of scores waits for the weights of the one before.
+    // The two halves of a tile's keys are then products of their own, and their warpgroups take turns (512 rows
+    // on 128K, LSSAR: 737 -> 572 us).  Not in softmax, whose warpgroups exchange each tile's maxima (77 -> 84 us).
+    constexpr bool kSplit = PHASE == kValues && !kSepP && MODE != kSoftmax;
     constexpr int kPCol = 256, kOCol = kSepP ? 384 : 256;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -615,14 +602,13 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned *err = c.err;
 
-    ptx::launch_dependents();
     if (threadIdx.x == 0) {
         auto init = [](uint64_t *b, uint32_t count) { ptx::mbar_init(ptx::smem_u32(b), count); };
         for (int i = 0; i < 2; ++i) {
             init(&sh->q_full[i], 256);
             for (int j = 0; j < 2; ++j) {
                 init(&sh->s_full[i][j], 1);
-                init(&sh->s_free[i][j], 256);
+                init(&sh->s_free[i][j], kSplit ? 128 : 256);
             }
             init(&sh->p_full[i], 256);
             init(&sh->p_free[i], 1);
@@ -651,8 +637,10 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sh->tmem;
-    // the plan, the norms and (kValues) the statistics are there from here on
+    // The plan, the norms and (kValues) the statistics are there from here on.  (What is launched next
+    // may read the plan at once, and waits for the rest.)
     ptx::grid_dependency_wait();
+    ptx::launch_dependents();
 
     const uint32_t nap = warp == 0 ? kNapProducer : 0u;
     auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) -> bool {
@@ -859,13 +847,28 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             };
-            auto issue_pv = [&](uint32_t vslot, bool accumulate) {
-                const uint64_t dv = dv0 + (uint64_t)((vslot * TB) >> 4);
+            // keys [from, from + 16 n) of the tile
+            auto issue_pv = [&](uint32_t vslot, int from, int n, bool accumulate) {
+                const uint64_t dv = dv0 + (uint64_t)((vslot * TB + from * 128) >> 4);
+                const uint32_t words = kSepP ? tmem + kPCol + 64 * w + from / 2 : tmem + w * kKeys + from;
                 if (ptx::elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        ptx::mma_ts(tmem + kOCol + w * D, kSepP ? tmem + kPCol + 64 * w + 8 * k : tmem + w * kKeys + (k / 4) * 64 + (k % 4) * 8,
-                                    dv + (uint64_t)((k * 2048) >> 4), g.idesc_pv, (accumulate || k > 0) ? 1u : 0u);
+                    for (int k = 0; k < n; ++k)
+                        ptx::mma_ts(tmem + kOCol + w * D, words + 8 * k, dv + (uint64_t)((k * 2048) >> 4), g.idesc_pv, (accumulate || k > 0) ? 1u : 0u);
+                }
+                __syncwarp();
+            };
+            // kSplit: scores of 64 keys
+            auto issue_half = [&](uint32_t kslot, int h) {
+                const uint64_t dq = dq0 + (uint64_t)((w * TB) >> 4), dk = dk0 + (uint64_t)((kslot * TB + h * 8192) >> 4);
+                const uint32_t full = LSSAR_AT(s_full) + 16 * w + 8 * h, col = tmem + w * kKeys + h * 64;
+                if (ptx::elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
+                        ptx::mma_ss(col, dq + off, dk + off, g.idesc_s64, k > 0);
+                    }
+                    ptx::mma_commit(full);
                 }
                 __syncwarp();
             };
@@ -884,7 +887,14 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     }
                 } else {
                     if (!(ok = acquire(kslot))) break;
-                    if (live && !(ok = issue_s(kslot))) break;
+                    if constexpr (kSplit) {
+                        if (live) {
+                            issue_half(kslot, 0);
+                            issue_half(kslot, 1);
+                        }
+                    } else {
+                        if (live && !(ok = issue_s(kslot))) break;
+                    }
                     commit(LSSAR_AT(kv_empty) + 8 * kslot);
                     for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
                         const bool next = kt + 1 < it.kt1;
@@ -897,22 +907,31 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                         if (!(ok = acquire(vslot))) break;
                         if (live) {
                             clear_rows(vslot, it.len - kt * kKeys);
-                            // d = 64: P is in its columns; d = 128: over S, which its release says
-                            if constexpr (kSepP) {
-                                if (!(ok = wait_all(LSSAR_AT(p_full) + 8 * w, pv & 1, kErrPFull))) break;
+                            auto o_is_free = [&] {
+                                return kt > it.kt0 || segs == 0 || wait_all(LSSAR_AT(o_free) + 8 * w, (segs - 1) & 1, kErrOFree);
+                            };
+                            if constexpr (kSplit) {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    // this half's weights are in place of its scores
+                                    if (!(ok = wait_all(LSSAR_AT(s_free) + 16 * w + 8 * h, pv & 1, kErrSFree))) break;
+                                    if (h == 0 && !(ok = o_is_free())) break;
+                                    ptx::tc_fence_after();
+                                    issue_pv(vslot, 64 * h, 4, kt > it.kt0 || h > 0);
+                                    // (before the commits that nothing waits for: each takes some 300 cycles)
+                                    if (next) issue_half(kslot, h);
+                                }
+                                if (!ok) break;
                             } else {
-                                if (!(ok = wait_all((LSSAR_AT(s_free) + 16 * (w) + 8 * (0)), pv & 1, kErrSFree))) break;
-                            }
-                            ptx::tc_fence_after();
-                            if (kt == it.kt0 && segs > 0) {
-                                if (!(ok = wait_all(LSSAR_AT(o_free) + 8 * w, (segs - 1) & 1, kErrOFree))) break;
+                                if (!(ok = wait_all(kSepP ? LSSAR_AT(p_full) + 8 * w : LSSAR_AT(s_free) + 16 * w, pv & 1, kErrPFull)) || !(ok = o_is_free())) break;
                                 ptx::tc_fence_after();
+                                // (at d = 128 P's words are over the first half of each half of S)
+                                issue_pv(vslot, 0, kSepP ? 8 : 4, kt > it.kt0);
+                                if constexpr (!kSepP) issue_pv(vslot, 64, 4, true);
+                                if constexpr (kSepP) commit(LSSAR_AT(p_free) + 8 * w);
+                                else if (next && !(ok = issue_s(kslot))) break;
                             }
-                            issue_pv(vslot, kt > it.kt0);
                             ++pv;
-                            // (what the score warps wait for first: a commit takes some 300 cycles)
-                            if constexpr (kSepP) commit(LSSAR_AT(p_free) + 8 * w);
-                            else if (next && !(ok = issue_s(kslot))) break;
                             if (!next) {
                                 commit(LSSAR_AT(o_full) + 8 * w);
                                 ++segs;
@@ -935,7 +954,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
         const uint32_t p_col = kSepP ? tmem + lane_addr + kPCol + 64 * w + 32 * half : s_col;
         const uint32_t o_col = tmem + lane_addr + kOCol + w * D + half * (D / 2);
         dcheck(tmem_in_range(s_col, tmem, 64, 512) && (PHASE == kStats || tmem_in_range(o_col, tmem, D / 2, 512)), err, kDbgTmem);
-        const uint32_t s_full = LSSAR_AT(s_full) + 16 * w, s_free = LSSAR_AT(s_free) + 16 * w;
+        const uint32_t s_full = LSSAR_AT(s_full) + 16 * w + (kSplit ? 8 * half : 0), s_free = LSSAR_AT(s_free) + 16 * w + (kSplit ? 8 * half : 0);
         const uint32_t p_done = (kSepP ? LSSAR_AT(p_full) + 8 * w : s_free), p_free = LSSAR_AT(p_free) + 8 * w;
         // this row's place in the exchange arrays, of the first parity, and the other half's
         const uint32_t mine = (w * 2 + half) * (kTileRows * 4) + 4 * in, others = (w * 2 + (half ^ 1)) * (kTileRows * 4) + 4 * in;
@@ -968,16 +987,36 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             }
             return true;
         };
-        // ... they are there
+        // ... they are there; the normalised modes need their norms, whose halves meet next
+        uint32_t meets = 0;
         auto hand_over = [&](bool some) {
             if (!some) return;
             asm volatile("cp.async.wait_all;" ::: "memory");
             ptx::fence_proxy_async_smem();
             ptx::mbar_arrive(LSSAR_AT(q_full) + 8 * w);
+            if constexpr (kNorm) {
+                const uint32_t row = sq + w * TB + (D == 128 ? half * (kTileRows * 128) : 0) + in * 128;
+                float s = 0.f;
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    uint4 u;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(row + (((D == 128 ? x : half * 4 + x) ^ (in & 7)) << 4)) : "memory");
+                    s += squares(u, c.half);
+                }
+                ptx::st_shared_f32(LSSAR_AT(qq) + (meets & 1) * kParity + mine, s);
+            }
+        };
+        // the two halves of this tile's rows have written what they exchange
+        auto meet = [&] {
+            ptx::mbar_arrive(LSSAR_AT(halves) + 8 * w);
+            return wait_all(LSSAR_AT(halves) + 8 * w, meets++ & 1, kErrHalves);
         };
         bool some = false;
         ok = gather(0, some);
-        if (ok) hand_over(some);
+        if (ok) {
+            hand_over(some);
+            ok = meet();
+        }
         // 32 products of the tile from column 32 x of this half on, as they are
         auto load = [&](uint32_t (&z)[32], uint32_t col) {
             ptx::tmem_ld32(col, z);
@@ -990,7 +1029,10 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             if (kt0 < 0) break;
             if (rows <= w * kTileRows) {                         // none of this tile's
                 tiles += kt1 - kt0;
-                if ((ok = gather(items.i + 1, some))) hand_over(some);
+                if ((ok = gather(items.i + 1, some))) {
+                    hand_over(some);
+                    ok = meet();
+                }
                 release_item();
                 continue;
             }
@@ -1002,8 +1044,9 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             Row row = {};
             row.a = g.scale;
             if constexpr (kNorm) {
-                const int hq = LSSAR_ITEM(h) * g.G + v % g.G;
-                row.a = g.s.qscale[((size_t)LSSAR_ITEM(b) * a.H + hq) * a.n + LSSAR_ITEM(t0) + v / g.G];
+                const uint32_t at = LSSAR_AT(qq) + (meets - 1 & 1) * kParity;
+                const float qq = ptx::ld_shared_f32(at + mine) + ptx::ld_shared_f32(at + others);
+                row.a = g.scale * logf((float)(limit + 1)) / fmaxf(sqrtf(qq), 1e-12f);
             }
             int form = kMixed;
             if constexpr (PHASE == kValues && is_reweight(MODE)) {
@@ -1035,7 +1078,11 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 if (!(ok = wait_all(s_full + 8 * buf, sb.parity(), kErrSFull))) break;
                 ++sb.i;
                 ptx::tc_fence_after();
-                if (kt + 1 == kt1 && !(ok = gather(items.i + 1, some))) break;      // (the last product with this q is done)
+                if (kt + 1 == kt1) {
+                    // the last product with this q is done (kSplit: the other half's too)
+                    if (kSplit && !(ok = wait_all(LSSAR_AT(s_full) + 16 * w + 8 * (half ^ 1), (sb.i - 1) & 1, kErrSFull))) break;
+                    if (!(ok = gather(items.i + 1, some))) break;
+                }
                 if (!live) {
                     // none of the item's rows: the barriers only
                     ptx::tc_fence_before();
@@ -1136,20 +1183,13 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                         if constexpr (MODE == kSoftmax) form = __any_sync(0xffffffffu, fabsf(row.ref) > 65536.f) ? kAccurate : kMixed;
                     }
                 }
-                uint32_t zz[2][32];
-                load(zz[0], col);
-                ptx::tmem_ld32(col + 32, zz[1]);                      // on its way while the first is weighted
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < 2; ++x) {
-                    uint32_t (&z)[32] = zz[x];
-                    uint32_t pk[16];
-                    if (x == 1) {
-                        ptx::tmem_ld_wait();
-                        ptx::reg_fence(z);
-                        if (kSepP) {
-                            ptx::tc_fence_before();
-                            ptx::mbar_arrive(s_free);                 // the next product may write here
-                        }
+                    uint32_t z[32], pk[16];
+                    load(z, col + x * 32);
+                    if (kSepP && x == 1) {
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(s_free);                     // the next product may write here
                     }
                     if constexpr (MODE != kSoftmax) to_z<kNorm>(z, knorm + x * 128, row.a);
                     if (masked) mask(z, last - x * 32, kMasked);
@@ -1184,23 +1224,28 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 }
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
+                if constexpr (kSplit && kOnePass) {
+                    // (the first half's product must not start while the other half's columns of O are rescaled)
+                    if (__any_sync(0xffffffffu, raise)) {
+                        ptx::mbar_arrive(LSSAR_AT(tile_max) + 32 * w + 8 * quarter);
+                        if (!(ok = wait_all(LSSAR_AT(tile_max) + 32 * w + 8 * quarter, exchanges++ & 1, kErrTileMax))) break;
+                    }
+                }
                 ptx::mbar_arrive(p_done);
                 ++pv;
             }
             if (!ok) break;
             hand_over(some);
             // the two halves of a row meet
-            const uint32_t par = segs & 1;
+            const uint32_t par = meets & 1;
             const float part = (acc.x + acc.y) + sum_run;
             ptx::st_shared_f32(LSSAR_AT(s) + par * kParity + mine, part);
             const float m_part = MODE == kSigmoidRw ? -m_run : fmaxf(m_run, kLowest);
             if constexpr (PHASE == kStats) ptx::st_shared_f32(LSSAR_AT(m) + par * kParity + mine, m_part);
-            ptx::mbar_arrive(LSSAR_AT(halves) + 8 * w);
-            if (!(ok = wait_all(LSSAR_AT(halves) + 8 * w, par, kErrHalves))) break;
+            if (!(ok = meet())) break;
             const float other = ptx::ld_shared_f32(LSSAR_AT(s) + par * kParity + others);
             const bool valid = w * kTileRows + in < rows;
             if constexpr (PHASE == kStats) {
-                ++segs;
                 if (half == 0 && valid) {
                     const float m1 = ptx::ld_shared_f32(LSSAR_AT(m) + par * kParity + others), m = fmaxf(m_part, m1);
                     const float s = MODE == kSoftmaxRw ? part * ptx::ex2(m_part - m) + other * ptx::ex2(m1 - m) : part + other;
@@ -1274,17 +1319,23 @@ template <int D, bool HALF, bool RELATIVE>
 __global__ void __launch_bounds__(kJoinThreads) attend_join(const __grid_constant__ Args g) {
     const PagedAttend &a = g.a;
     const PagedCache &c = a.c;
-    ptx::grid_dependency_wait();
-    const Header head = *g.s.head;
+    const Header head = *g.s.head;             // the plan is there (see attend_kernel)
     const int cta = blockIdx.x + 1;
     const long long x = (long long)cta * head.run;
-    if (x >= head.total) return;
-    const int4 en = g.s.entries[g.s.first[cta]];
-    // the item's first tile, behind its cost
-    const int h = (int)(x - en.w) / en.z, start = en.w + h * en.z + kItemCost;
-    if (start >= x || x - head.run > start) return;
-    const int last = (start + en.z - kItemCost - 1) / head.run, cnt = a.counts ? a.counts[en.x] : a.n, t0 = en.y * g.tokens;
-    const int rows = min(g.tokens, cnt - t0) * g.G;
+    bool some = x < head.total;
+    int4 en = make_int4(0, 0, 1, 0);
+    int h = 0, last = 0, rows = 0, t0 = 0;
+    if (some) {
+        en = g.s.entries[g.s.first[cta]];
+        h = (int)(x - en.w) / en.z;
+        const int start = en.w + h * en.z + kItemCost;         // the item's first tile, behind its cost
+        some = start < x && x - head.run <= start;
+        last = (start + en.z - kItemCost - 1) / head.run;
+        t0 = en.y * g.tokens;
+        rows = min(g.tokens, (a.counts ? a.counts[en.x] : a.n) - t0) * g.G;
+    }
+    ptx::grid_dependency_wait();               // the segments' parts too (in every block: the call's end waits for them)
+    if (!some) return;
     constexpr int kLanes = D / 4, kStep = kJoinThreads / kLanes;
     const int part = threadIdx.x % kLanes;
 #pragma unroll 1
