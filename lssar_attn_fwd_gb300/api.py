@@ -469,8 +469,8 @@ def _per_sequence(name, t, B, dev):
     import torch
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.shape != (B,) or not t.is_contiguous() or not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"{name} must be a contiguous int32 [B] tensor on the cache's device")
+    if t.dtype is not torch.int32 or t.shape != (B,) or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous int32 [B] tensor on the same device")
     return t.data_ptr()
 
 
@@ -607,20 +607,6 @@ def lssar_paged_evict(k_pages, v_pages, table, lens, scores, positions, keep, re
     return lens_out, scores_out, positions_out
 
 
-def _rows(name, t, shape, dtype, dev):
-    """The strides of a [B, H, n, d] tensor of rows, d contiguous."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or t.get_device() != dev:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on the same device")
-    st = t.stride()
-    if st[3] != 1 and t.numel():
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return _pack_3(*st[:3])
-
-
-def _same_place(x, y):
-    return x.data_ptr() == y.data_ptr() and x.stride() == y.stride()
-
-
 def lssar_paged_attend(q, k_pages, v_pages, table, lens, counts=None, p=3, mode=MODE_LSSAR, out=None, stream=None):
     """The rows of a chunk of new tokens against a paged cache, in every mode.
 
@@ -637,17 +623,18 @@ def lssar_paged_attend(q, k_pages, v_pages, table, lens, counts=None, p=3, mode=
     desc, B, Hkv, cap, d, dev = _paged_cache(k_pages, v_pages, table, lens)
     if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
         raise ValueError("q must be [B, H, n, d] with the cache's B and d")
-    shape, dtype = q.shape, k_pages.dtype
-    strides = _rows("q", q, shape, dtype, dev)
+    shape, dtype, strides = q.shape, k_pages.dtype, q.stride()
+    if q.dtype is not dtype or q.get_device() != dev or strides[3] != 1:
+        raise ValueError("q must have the cache's type and device, d contiguous")
     if out is None:
-        new = torch.empty if counts is None else torch.zeros
-        make = lambda: new(shape, dtype=dtype, device=q.device)   # noqa: E731
-        out = make() if stream is None else _make(stream, dev, make)
-    elif (out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or not out.is_cuda
-          or out.get_device() != dev):
+        if counts is None:
+            out = _like(q) if stream is None else _make(stream, dev, lambda: _like(q))
+        else:
+            out = q.new_zeros(shape) if stream is None else _make(stream, dev, lambda: q.new_zeros(shape))
+    elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be a contiguous [B, H, n, d] tensor of q's type on the cache's device")
-    _paged_call("lssar_paged_attend", dev, stream, desc, q.data_ptr(), strides, out.data_ptr(), shape[1], shape[2],
-                _per_sequence("counts", counts, B, dev), _int32("p", p), _int32("mode", mode))
+    _paged_call("lssar_paged_attend", dev, stream, desc, q.data_ptr(), _pack_3(*strides[:3]), out.data_ptr(), shape[1],
+                shape[2], _per_sequence("counts", counts, B, dev), _int32("p", p), _int32("mode", mode))
     return out
 
 
@@ -673,48 +660,52 @@ class Rotary:
                                  _int32("rot_dim", self.rot_dim), bool(interleaved), self.SCALINGS[scaling])
 
 
+def _like(x):
+    """A new contiguous tensor of x's shape and type (a third of new_empty's host time)."""
+    import torch
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
+
+
+def _turned(what, x, y, shape, strides, dtype, dev, stream):
+    """The tensor that takes the turned rows of x: a new one, y apart from x, or x itself."""
+    if y is None:
+        return _like(x) if stream is None else _make(stream, dev, lambda: _like(x))
+    if (y.shape != shape or y.dtype is not dtype or y.get_device() != dev
+            or not (y.is_contiguous() or (y.data_ptr() == x.data_ptr() and y.stride() == strides))):
+        raise ValueError(f"{what}_out must be {what} itself or a contiguous tensor like it")
+    return y
+
+
 def _rope(name, q, k, rotary, positions, q_out, k_out, stream):
     import torch
-    for t in (q, q if k is None else k):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("q and k must be torch tensors")
-        if not t.is_cuda or t.dim() != 4 or (t.dtype is not torch.bfloat16 and t.dtype is not torch.float16):
-            raise ValueError("q and k must be bfloat16 or float16 CUDA tensors [B, heads, L, d]")
-    (B, H, L, d), dtype, dev = q.shape, q.dtype, q.get_device()
-    if k is None:
-        if k_out is not None:
-            raise ValueError("k_out needs k")
-    elif (k.shape[0], k.shape[2], k.shape[3]) != (B, L, d):
-        raise ValueError("q and k must share B, L and d")
+    if not isinstance(q, torch.Tensor) or not (k is None or isinstance(k, torch.Tensor)):
+        raise TypeError("q and k must be torch tensors")
+    dtype, dev, shape, strides = q.dtype, q.get_device(), q.shape, q.stride()
+    if dev < 0 or len(shape) != 4 or (dtype is not torch.bfloat16 and dtype is not torch.float16) or strides[3] != 1:
+        raise ValueError("q must be a bfloat16 or float16 CUDA tensor [B, heads, L, d], d contiguous")
+    B, H, L, d = shape
     if not isinstance(rotary, Rotary) or rotary.d != d:
         raise ValueError("rotary must be a Rotary of q's head dimension")
-    per_token = 0
+    per_token, at = 0, None
     if positions is not None:
-        per_token = int(positions.dim() == 2)
+        per_token, at = int(positions.dim() == 2), positions.data_ptr()
         if (positions.dtype is not torch.int32 or positions.shape != ((B, L) if per_token else (B,))
-                or not positions.is_contiguous() or not positions.is_cuda or positions.get_device() != dev):
+                or not positions.is_contiguous() or positions.get_device() != dev):
             raise ValueError("positions must be a contiguous int32 [B] or [B, L] tensor on q's device")
-    outs = []
-    for what, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            outs.append(None)
-        elif y is None:
-            make = lambda: torch.empty(x.shape, dtype=dtype, device=x.device)   # noqa: E731,B023
-            outs.append(make() if stream is None else _make(stream, dev, make))
-        elif _same_place(x, y) and y.shape == x.shape and y.dtype is dtype:
-            outs.append(y)
-        elif (y.shape != x.shape or y.dtype is not dtype or not y.is_contiguous() or not y.is_cuda
-              or y.get_device() != dev):
-            raise ValueError(f"{what}_out must be {what} itself or a contiguous tensor like it")
-        else:
-            outs.append(y)
-    args = []
-    for x, y in ((q, outs[0]), (k, outs[1])):
-        args += [None, None, None, 0] if x is None else [x.data_ptr(), _rows("q and k", x, x.shape, dtype, dev),
-                                                         y.data_ptr(), x.shape[1]]
-    _paged_call(name, dev, stream, *args, B, L, d, DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP16, rotary.desc,
-                None if positions is None else positions.data_ptr(), per_token)
-    return outs[0], outs[1]
+    k_args = None, None, None, 0
+    if k is not None:
+        k_shape, k_strides = k.shape, k.stride()
+        if (len(k_shape) != 4 or k_shape[0] != B or k_shape[2] != L or k_shape[3] != d or k.dtype is not dtype
+                or k.get_device() != dev or k_strides[3] != 1):
+            raise ValueError("k must share q's B, L, d, type and device, d contiguous")
+        k_out = _turned("k", k, k_out, k_shape, k_strides, dtype, dev, stream)
+        k_args = k.data_ptr(), _pack_3(*k_strides[:3]), k_out.data_ptr(), k_shape[1]
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    q_out = _turned("q", q, q_out, shape, strides, dtype, dev, stream)
+    _paged_call(name, dev, stream, q.data_ptr(), _pack_3(*strides[:3]), q_out.data_ptr(), H, *k_args, B, L, d,
+                DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_FP16, rotary.desc, at, per_token)
+    return q_out, k_out
 
 
 def lssar_rope(q, k, rotary, positions=None, q_out=None, k_out=None, stream=None):
@@ -754,28 +745,34 @@ def lssar_paged_append_rope(q, k_new, v_new, k_pages, v_pages, table, lens, rota
         raise ValueError("rotary must be a Rotary of the cache's head dimension")
     dtype, q_shape = k_pages.dtype, q.shape
     if q_out is None:
-        new = torch.empty if counts is None else torch.zeros
-        make = lambda: new(q_shape, dtype=dtype, device=q.device)   # noqa: E731
-        q_out = make() if stream is None else _make(stream, dev, make)
+        if counts is None:
+            q_out = _like(q) if stream is None else _make(stream, dev, lambda: _like(q))
+        else:
+            q_out = q.new_zeros(q_shape) if stream is None else _make(stream, dev, lambda: q.new_zeros(q_shape))
+    elif q_out.shape != q_shape or q_out.dtype is not dtype or q_out.get_device() != dev:
+        raise ValueError("q_out must have q's shape, type and device")
     result = q_out
-    if q_out.shape != q_shape:
-        raise ValueError("q_out must have q's shape")
-    one = lambda t: t.unsqueeze(2) if t.dim() == 3 else t   # noqa: E731
-    q, q_out, k_new, v_new = one(q), one(q_out), one(k_new), one(v_new)
-    if q.dim() != 4 or k_new.dim() != 4:
-        raise ValueError("q, k_new and v_new must be [B, heads, n, d]")
-    n, rows = k_new.shape[2], (B, Hkv, k_new.shape[2], d)
-    kst, vst = _rows("k_new", k_new, rows, dtype, dev), _rows("v_new", v_new, rows, dtype, dev)
-    qst = _rows("q", q, (B, q.shape[1], n, d), dtype, dev)
-    _rows("q_out", q_out, q.shape, dtype, dev)
-    if not q_out.is_contiguous() and not _same_place(q, q_out):
+    if len(q_shape) == 3:                                    # one token
+        q, q_out, k_new, v_new = q.unsqueeze(2), q_out.unsqueeze(2), k_new.unsqueeze(2), v_new.unsqueeze(2)
+        q_shape = q.shape
+    shape = k_new.shape
+    if (len(q_shape) != 4 or len(shape) != 4 or v_new.shape != shape or shape[0] != B or shape[1] != Hkv or shape[3] != d
+            or q_shape[0] != B or q_shape[2] != shape[2] or q_shape[3] != d):
+        raise ValueError("q must be [B, H, n, d], k_new and v_new [B, Hkv, n, d], with the cache's B, Hkv and d")
+    if (q.dtype is not dtype or k_new.dtype is not dtype or v_new.dtype is not dtype or q.get_device() != dev
+            or k_new.get_device() != dev or v_new.get_device() != dev):
+        raise ValueError("q, k_new and v_new must have the cache's type and device")
+    n, qst, kst, vst = shape[2], q.stride(), k_new.stride(), v_new.stride()
+    if n and (qst[3] != 1 or kst[3] != 1 or vst[3] != 1):
+        raise ValueError("the last dimension of q, k_new and v_new must be contiguous")
+    if not (q_out.is_contiguous() or (q_out.data_ptr() == q.data_ptr() and q_out.stride() == qst)):
         raise ValueError("q_out must be contiguous, or q itself")
     if lens_out is None:
         lens_out = torch.empty_like(lens) if stream is None else _make(stream, dev, lambda: torch.empty_like(lens))
     slots = (B, Hkv, cap)
-    _paged_call("lssar_paged_append_rope", dev, stream, desc, q.data_ptr(), qst, q_out.data_ptr(), q.shape[1],
-                k_new.data_ptr(), kst, v_new.data_ptr(), vst, n, rotary.desc, _per_sequence("counts", counts, B, dev),
-                _per_sequence("first_positions", first_positions, B, dev),
+    _paged_call("lssar_paged_append_rope", dev, stream, desc, q.data_ptr(), _pack_3(*qst[:3]), q_out.data_ptr(), q_shape[1],
+                k_new.data_ptr(), _pack_3(*kst[:3]), v_new.data_ptr(), _pack_3(*vst[:3]), n, rotary.desc,
+                _per_sequence("counts", counts, B, dev), _per_sequence("first_positions", first_positions, B, dev),
                 _slots("scores", scores, slots, torch.float32, dev), _slots("positions", positions, slots, torch.int32, dev),
                 _per_sequence("lens_out", lens_out, B, dev))
     return result, lens_out
@@ -785,22 +782,21 @@ def _pages(table, lens, free_pages, free_count, free_out, stream):
     """Checks the tensors of a page table and a list of free pages; returns (B,
     max_pages, n_pages, free_out, device index)."""
     import torch
-    for t in (table, lens, free_pages, free_count):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("table, lens, free_pages and free_count must be torch tensors")
-    if not table.is_cuda or table.dtype is not torch.int32 or table.dim() != 2 or not table.is_contiguous():
+    T, i32 = torch.Tensor, torch.int32
+    if not (isinstance(table, T) and isinstance(lens, T) and isinstance(free_pages, T) and isinstance(free_count, T)):
+        raise TypeError("table, lens, free_pages and free_count must be torch tensors")
+    dev, shape = table.get_device(), table.shape
+    if dev < 0 or table.dtype is not i32 or len(shape) != 2 or not table.is_contiguous():
         raise ValueError("table must be a contiguous int32 [B, max_pages] CUDA tensor")
-    dev, (B, max_pages) = table.get_device(), table.shape
     if free_out is None:
         free_out = torch.empty_like(free_count) if stream is None else _make(stream, dev, lambda: torch.empty_like(free_count))
-    if free_pages.dim() != 1:
-        raise ValueError("free_pages must be [n_pages]")
-    n_pages = free_pages.shape[0]
-    for name, t, shape in (("lens", lens, (B,)), ("free_pages", free_pages, (n_pages,)), ("free_count", free_count, (1,)),
-                           ("free_out", free_out, (1,))):
-        if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or not t.is_cuda or t.get_device() != dev:
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on the table's device")
-    return B, max_pages, n_pages, free_out, dev
+    elif free_out.shape != (1,) or free_out.dtype is not i32 or free_out.get_device() != dev:
+        raise ValueError("free_out must be an int32 [1] tensor on the table's device")
+    if free_pages.dim() != 1 or free_pages.dtype is not i32 or not free_pages.is_contiguous() or free_pages.get_device() != dev:
+        raise ValueError("free_pages must be a contiguous int32 [n_pages] tensor on the table's device")
+    if free_count.shape != (1,) or free_count.dtype is not i32 or free_count.get_device() != dev:
+        raise ValueError("free_count must be an int32 [1] tensor on the table's device")
+    return shape[0], shape[1], free_pages.shape[0], free_out, dev
 
 
 def lssar_paged_reserve(table, lens, counts, page_size, free_pages, free_count, counts_out=None, free_out=None, stream=None):
@@ -820,7 +816,7 @@ def lssar_paged_reserve(table, lens, counts, page_size, free_pages, free_count, 
     if counts_out is None:
         counts_out = torch.empty_like(lens) if stream is None else _make(stream, dev, lambda: torch.empty_like(lens))
     _paged_call("lssar_paged_reserve", dev, stream, table.data_ptr(), max_pages, _int32("page_size", page_size),
-                lens.data_ptr(), _per_sequence("counts", counts, B, dev), B, free_pages.data_ptr(), n_pages,
+                _per_sequence("lens", lens, B, dev), _per_sequence("counts", counts, B, dev), B, free_pages.data_ptr(), n_pages,
                 free_count.data_ptr(), _per_sequence("counts_out", counts_out, B, dev), free_out.data_ptr())
     return counts_out, free_out
 
@@ -835,7 +831,7 @@ def lssar_paged_release(table, lens, lens_new, page_size, free_pages, free_count
         raise ValueError("lens_new is needed")
     B, max_pages, n_pages, free_out, dev = _pages(table, lens, free_pages, free_count, free_out, stream)
     _paged_call("lssar_paged_release", dev, stream, table.data_ptr(), max_pages, _int32("page_size", page_size),
-                lens.data_ptr(), _per_sequence("lens_new", lens_new, B, dev), B, free_pages.data_ptr(), n_pages,
+                _per_sequence("lens", lens, B, dev), _per_sequence("lens_new", lens_new, B, dev), B, free_pages.data_ptr(), n_pages,
                 free_count.data_ptr(), free_out.data_ptr())
     return free_out
 
