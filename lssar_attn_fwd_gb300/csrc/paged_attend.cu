@@ -71,8 +71,8 @@ cudaError_t launch_paged_attend(const PagedAttend &pr, void *ws, int sms, cudaSt
     g.idesc_s64 = ptx::idesc_f16(!c.half, attend::kTileRows, 64, false, false);
     g.idesc_pv = ptx::idesc_f16(!c.half, attend::kTileRows, c.d, false, true);
     CUtensorMap km, vm;
-    if (!make_page_map(&km, c.k, c.half, c.d, c.Hkv * c.page_size, c.n_pages, c.page_stride, g.piece_rows) ||
-        !make_page_map(&vm, c.v, c.half, c.d, c.Hkv * c.page_size, c.n_pages, c.page_stride, g.piece_rows))
+    if (!make_group_map(&km, c.k, c.half, c.d, c.Hkv * c.page_size, c.n_pages, c.page_stride, g.piece_rows) ||
+        !make_group_map(&vm, c.v, c.half, c.d, c.Hkv * c.page_size, c.n_pages, c.page_stride, g.piece_rows))
         return cudaErrorInvalidValue;
     using namespace attend;
     Launch *const launch[5][2] = {{softmax_d64, softmax_d128}, {lssa_d64, lssa_d128}, {lssar_d64, lssar_d128},

@@ -25,8 +25,8 @@
 //   attend_join      adds the segments of the items that lie in several runs.
 // Each is a programmatic dependent of the one before it.
 //
-// Structure of attend (640 threads): warp 0 the TMA producer of K, V (a piece of a page at a
-// time) and key norms; warps 1, 2 issue the tcgen05.mma of one tile each; warp 3 has no role; four warpgroups of score
+// Structure of attend (640 threads): warp 0 the TMA producer of K (a piece of a page at a time) and of
+// key norms, warp 3 that of V; warps 1, 2 issue the tcgen05.mma of one tile each; four warpgroups of score
 // warps, two per tile, each half of its columns: thread = row (TMEM lane).  They also gather the rows of q
 // (any strides, any group) of the next segment during the last step of this one.  Warps whose 32 rows hold none of the item's skip the arithmetic.
 // TMEM (512 columns): kStats: S of tile w, two buffers each, at 256 w + 128 buffer.  kValues: S_w at
@@ -61,7 +61,7 @@ static_assert(128 * kCtrlRegs + 512 * kScoreRegs <= kThreads * kLaunchRegs, "reg
 // the one before that (kStats, d = 64; the others leave fewer tiles between).
 constexpr int kInfo = 16;
 constexpr int kItems = 4;                     // depth of the queue of segments
-constexpr int kItemCost = 2;                  // what an item costs beside its tiles, in tiles (they are numbered before its first)
+constexpr int kItemCost = 3;                  // what an item costs beside its tiles, in tiles (they are numbered before its first)
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint32_t kNapProducer = 200;   // ns between its polls of a barrier
 constexpr float kLowest = -3.0e38f;           // below every score, and finite
@@ -582,7 +582,8 @@ template <int D, int MODE, bool HALF, int PHASE>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm, const __grid_constant__ Args g) {
     using C = Cfg<D>;
-    constexpr int NS = C::kStages, TB = C::kTile;
+    constexpr int TB = C::kTile, kGroup = 16 * D;
+    constexpr int NR = PHASE == kStats ? C::kStages : C::kStages / 2;       // stages of keys, and (kValues) of values
     constexpr bool kNorm = uses_normalised_qk(MODE);
     constexpr bool kOnePass = MODE == kSoftmax || MODE == kLssa;
     constexpr bool kSepP = D == 64;
@@ -623,7 +624,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
         }
         for (int i = 0; i < kItems; ++i) {
             init(&sh->item_full[i], 1);
-            init(&sh->item_empty[i], 2 + 16);
+            init(&sh->item_empty[i], (PHASE == kValues ? 3 : 2) + 16);
         }
         sh->abort_flag = 0;
         ptx::fence_mbar_init();
@@ -642,7 +643,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
     ptx::grid_dependency_wait();
     ptx::launch_dependents();
 
-    const uint32_t nap = warp == 0 ? kNapProducer : 0u;
+    const uint32_t nap = warp == 0 || warp == 3 ? kNapProducer : 0u;
     auto wait_all = [&](uint32_t bar, uint32_t parity, unsigned code) -> bool {
         return __all_sync(0xffffffffu, wait_bar(bar, parity, shared, err, code, nap));
     };
@@ -661,21 +662,17 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
 
     if (warp < kScoreWarp0) {
         if constexpr (PHASE == kValues) ptx::setmaxnreg_dec<kCtrlRegs>();
-        if (warp == 0) {
-            // ------------------------------------------------------------ producer
-            if (ptx::elect_one()) {
-                ptx::prefetch_tensormap(&km);
-                if (PHASE == kValues) ptx::prefetch_tensormap(&vm);
-            }
-            const Header head = *g.s.head;
+        if (warp == 0 || warp == 3) {
+            // ------------------------------------------------------------ producers: keys (and the segments), values
+            const bool keys = warp == 0;
+            const CUtensorMap *map = keys ? &km : &vm;
             const int piece_rows = g.piece_rows, ps = c.page_size;
-            const int t1 = min((long long)head.total, (long long)(blockIdx.x + 1) * head.run);
-            long long t = (long long)blockIdx.x * head.run;
-            Ring<NS> kv;
-            uint32_t info = 0;             // tiles of keys asked for
+            const uint32_t first_stage = keys ? 0 : NR;
+            Ring<NR> kv;
             bool ok = true;
-            int pg = -1, row = 0;          // of this lane's piece of the tile asked for: page (-1 past the end, -2 no page), row
+            int pg = -1, row = 0;          // of this lane's piece of the tile looked up: page (-1 past the end, -2 no page), row
             Item it = {};
+            if (ptx::elect_one()) ptx::prefetch_tensormap(map);
             auto look_up = [&](int kt) {
                 const int s0 = kt * kKeys + lane * piece_rows, i = s0 / ps;
                 pg = -1;
@@ -684,117 +681,101 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 pg = paged_page(c, it.b, i);
                 if (pg < 0) pg = -2;
             };
-            // (norms: the tile whose keys these are, -1 for values)
-            auto push = [&](const CUtensorMap *map, int page, int y, int norms) -> bool {
-                const uint32_t s = kv.slot();
-                if (kv.reused() && !wait_all(LSSAR_AT(kv_empty) + 8 * s, kv.parity() ^ 1, kErrKvEmpty)) return false;
-                const unsigned there = __ballot_sync(0xffffffffu, page >= 0);
-                const uint32_t full = (LSSAR_AT(kv_full) + 8 * s), dst = ring + s * TB + lane * piece_rows * 128;
-                if (lane == 0) {
-                    const int groups = piece_rows / 8;
-                    unsigned absent = 0xffffu;
-                    for (int i = 0; i * piece_rows < kKeys; ++i)
-                        if (there >> i & 1) absent &= ~(((1u << groups) - 1) << (i * groups));
-                    sh->absent[s] = absent;
-                    ptx::mbar_arrive_expect_tx(full, (uint32_t)__popc(there) * piece_rows * D * 2 + (kNorm && norms >= 0 ? kKeys * 4 : 0));
-                    if (kNorm && norms >= 0) {
-                        const long long at = ((long long)it.b * c.Hkv + it.h) * g.cap128 + (long long)norms * kKeys;
-                        if (dcheck((norms + 1) * kKeys <= g.cap128 && it.b < c.B, err, kDbgBulk))
-                            ptx::bulk_load(LSSAR_AT(knorm) + info % kInfo * (kKeys * 4), g.s.knorm + at, kKeys * 4, full);
-                    }
-                }
-                if (norms >= 0) ++info;
-                __syncwarp();
-                if (page >= 0 && dcheck(y >= 0 && y + piece_rows <= c.Hkv * ps && page < c.n_pages, err, kDbgTma)) {
-                    ptx::tma_load_3d(dst, map, full, 0, y, page);
-                    if (D == 128) ptx::tma_load_3d(dst + kKeys * 128, map, full, 64, y, page);
-                }
-                ++kv.i;
-                return true;
-            };
-            auto push_keys = [&](int kt, int slot) -> bool {
-                // the first slot of a page that is none
-                if (__any_sync(0xffffffffu, pg == -2)) {
-                    const int first = __reduce_min_sync(0xffffffffu, pg == -2 ? kt * kKeys + lane * piece_rows : 0x7fffffff);
-                    if (lane == 0) {
-                        volatile int *bad = &sh->items[slot].first_bad;
-                        *bad = min(*bad, first);
-                    }
-                }
-                return push(&km, pg, row, kt);
-            };
-            int e = 0, h = 0, kt = 0;
-            int4 en = make_int4(0, 0, 0, 0);
-            if (t < t1) {
-                e = g.s.first[blockIdx.x];
-                en = g.s.entries[e];
-                h = (int)(t - en.w) / en.z;
-                kt = (int)(t - en.w) - h * en.z;
-            }
-            while (ok) {
-                const uint32_t slot = items.slot();
-                if (items.reused() && !wait_all(LSSAR_AT(item_empty) + 8 * slot, items.parity() ^ 1, kErrItem)) break;
-                // (tiles of the item up to the run's end; none where only its cost lies before it)
-                const int kt1 = t < t1 ? (int)min((long long)en.z, kt + t1 - t) - kItemCost : 0;
-                it.kt0 = -1;
-                if (kt1 > 0) {
-                    const int cnt = a.counts ? a.counts[en.x] : a.n;
-                    it.b = en.x;
-                    it.h = h;
-                    it.t0 = en.y * g.tokens;
-                    it.rows = min(g.tokens, cnt - it.t0) * g.G;
-                    it.len = c.lens[en.x];
-                    it.base = it.len - cnt;
-                    it.nk = en.z - kItemCost;
-                    it.kt0 = max(kt - kItemCost, 0);
-                    it.kt1 = kt1;
-                    it.item = e * c.Hkv + h;
-                    it.start = en.w + h * en.z + kItemCost;
-                    it.first_bad = 0x7fffffff;
-                    if (!dcheck(e < head.entries && h < c.Hkv && it.kt1 > it.kt0 && it.rows > 0 && it.rows <= g.rows, err, kDbgItem)) it.kt0 = -1;
-                }
-                if (lane == 0) {
-                    sh->items[slot] = it;
-                    ptx::mbar_arrive(LSSAR_AT(item_full) + 8 * slot);
-                }
-                __syncwarp();
-                ++items.i;
-                if (it.kt0 < 0) break;
+            // the tiles of the segment, whose queue entry is `slot`
+            auto load_tiles = [&](uint32_t slot) {
                 look_up(it.kt0);
-                if constexpr (PHASE == kStats) {
-                    for (int k = it.kt0; ok && k < it.kt1; ++k) {
-                        ok = push_keys(k, slot);
-                        if (k + 1 < it.kt1) look_up(k + 1);
-                    }
-                } else {
-                    int vpg = pg, vrow = row;
-                    ok = push_keys(it.kt0, slot);
-                    for (int k = it.kt0; ok && k < it.kt1; ++k) {
-                        const int page = vpg, y = vrow;
-                        if (k + 1 < it.kt1) {
-                            look_up(k + 1);
-                            vpg = pg;
-                            vrow = row;
-                            ok = push_keys(k + 1, slot);
+#pragma unroll 1
+                for (int k = it.kt0; ok && k < it.kt1; ++k) {
+                    const int page = pg, y = row;
+                    if (k + 1 < it.kt1) look_up(k + 1);          // (arrives while this one waits for its stage)
+                    const uint32_t s = first_stage + kv.slot(), full = LSSAR_AT(kv_full) + 8 * s;
+                    if (kv.reused() && !(ok = wait_all(LSSAR_AT(kv_empty) + 8 * s, kv.parity() ^ 1, kErrKvEmpty))) break;
+                    const unsigned there = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -2);
+                    if (lane == 0) {
+                        const int groups = piece_rows / 8;
+                        unsigned absent = 0xffffu;
+                        for (int i = 0; i * piece_rows < kKeys; ++i)
+                            if (there >> i & 1) absent &= ~(((1u << groups) - 1) << (i * groups));
+                        sh->absent[s] = absent;
+                        if (keys && bad) {                        // the first slot of a page that is none
+                            volatile int *first = &sh->items[slot].first_bad;
+                            *first = min(*first, k * kKeys + (__ffs(bad) - 1) * piece_rows);
                         }
-                        if (ok) ok = push(&vm, page, y, -1);
+                        const bool norms = kNorm && keys;
+                        ptx::mbar_arrive_expect_tx(full, (uint32_t)__popc(there) * piece_rows * D * 2 + (norms ? kKeys * 4 : 0));
+                        const long long at = ((long long)it.b * c.Hkv + it.h) * g.cap128 + (long long)k * kKeys;
+                        if (norms && dcheck((k + 1) * kKeys <= g.cap128 && it.b < c.B, err, kDbgBulk))
+                            ptx::bulk_load(LSSAR_AT(knorm) + kv.i % kInfo * (kKeys * 4), g.s.knorm + at, kKeys * 4, full);
+                    }
+                    __syncwarp();
+                    if (page >= 0 && dcheck(y >= 0 && y + piece_rows <= c.Hkv * ps && page < c.n_pages, err, kDbgTma))
+                        ptx::tma_load_5d(ring + s * TB + lane * piece_rows * D * 2, map, full, 0, 0, 0, y >> 3, page);
+                    ++kv.i;
+                }
+            };
+            if (keys) {
+                const Header head = *g.s.head;
+                const int t1 = min((long long)head.total, (long long)(blockIdx.x + 1) * head.run);
+                long long t = (long long)blockIdx.x * head.run;
+                int e = 0, h = 0, kt = 0;
+                int4 en = make_int4(0, 0, 0, 0);
+                if (t < t1) {
+                    e = g.s.first[blockIdx.x];
+                    en = g.s.entries[e];
+                    h = (int)(t - en.w) / en.z;
+                    kt = (int)(t - en.w) - h * en.z;
+                }
+                while (ok) {
+                    const uint32_t slot = items.slot();
+                    if (items.reused() && !wait_all(LSSAR_AT(item_empty) + 8 * slot, items.parity() ^ 1, kErrItem)) break;
+                    // (tiles of the item up to the run's end; none where only its cost lies before it)
+                    const int kt1 = t < t1 ? (int)min((long long)en.z, kt + t1 - t) - kItemCost : 0;
+                    it.kt0 = -1;
+                    if (kt1 > 0) {
+                        const int cnt = a.counts ? a.counts[en.x] : a.n;
+                        it.b = en.x;
+                        it.h = h;
+                        it.t0 = en.y * g.tokens;
+                        it.rows = min(g.tokens, cnt - it.t0) * g.G;
+                        it.len = c.lens[en.x];
+                        it.base = it.len - cnt;
+                        it.nk = en.z - kItemCost;
+                        it.kt0 = max(kt - kItemCost, 0);
+                        it.kt1 = kt1;
+                        it.item = e * c.Hkv + h;
+                        it.start = en.w + h * en.z + kItemCost;
+                        it.first_bad = 0x7fffffff;
+                        if (!dcheck(e < head.entries && h < c.Hkv && it.kt1 > it.kt0 && it.rows > 0 && it.rows <= g.rows, err, kDbgItem)) it.kt0 = -1;
+                    }
+                    if (lane == 0) {
+                        sh->items[slot] = it;
+                        ptx::mbar_arrive(LSSAR_AT(item_full) + 8 * slot);
+                    }
+                    __syncwarp();
+                    ++items.i;
+                    if (it.kt0 < 0) break;
+                    load_tiles(slot);
+                    t += kt1 + kItemCost - kt;
+                    kt = 0;
+                    if (t < t1 && ++h == c.Hkv) {
+                        h = 0;
+                        en = g.s.entries[++e];
                     }
                 }
-                t += kt1 + kItemCost - kt;
-                kt = 0;
-                if (t < t1 && ++h == c.Hkv) {
-                    h = 0;
-                    en = g.s.entries[++e];
+            } else if constexpr (PHASE == kValues) {
+                while (ok && next_item(it)) {
+                    release_item();
+                    load_tiles(0);
                 }
             }
             // no copy may be in flight when the CTA ends
-            for (uint32_t i = kv.i > NS ? kv.i - NS : 0; i < kv.i; ++i)
-                wait_bar((LSSAR_AT(kv_full) + 8 * (i % NS)), (i / NS) & 1, shared, err, kErrDrain, nap, false);
+            for (uint32_t i = kv.i > NR ? kv.i - NR : 0; i < kv.i; ++i)
+                wait_bar(LSSAR_AT(kv_full) + 8 * (first_stage + i % NR), (i / NR) & 1, shared, err, kErrDrain, nap, false);
             __syncwarp();
-        } else if (warp < 3) {
+        } else {
             // ------------------------------------------------------------ MMA of tile w
             const int w = warp - 1;
-            Ring<NS> kv;
+            Ring<NR> keys, values;
             Ring<kSBufs> sb;               // S of this tile
             uint32_t pv = 0, qs = 0, segs = 0;     // P.V products issued; q tiles taken, segments ended, of this tile
             bool ok = true;
@@ -802,16 +783,18 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 if (ptx::elect_one()) ptx::mma_commit(bar);
                 __syncwarp();
             };
-            auto acquire = [&](uint32_t &slot) -> bool {
-                slot = kv.slot();
-                if (!wait_all(LSSAR_AT(kv_full) + 8 * slot, kv.parity(), kErrKvFull)) return false;
-                ++kv.i;
+            // the stage of the next tile of keys, or of values
+            auto acquire = [&](Ring<NR> &tiles, uint32_t first, uint32_t &stage) -> bool {
+                stage = first + tiles.slot();
+                if (!wait_all(LSSAR_AT(kv_full) + 8 * stage, tiles.parity(), kErrKvFull)) return false;
+                ++tiles.i;
                 ptx::tc_fence_after();
                 return true;
             };
             const uint64_t dq0 = ptx::smem_desc_sw128(sq, tc::kKmajorLbo, tc::kKmajorSbo);
-            const uint64_t dk0 = ptx::smem_desc_sw128(ring, tc::kKmajorLbo, tc::kKmajorSbo);
-            const uint64_t dv0 = ptx::smem_desc_sw128(ring, tc::kVLbo, tc::kVSbo);
+            // keys and values: groups of 8 rows, kGroup bytes apart, the 64-column blocks of a group 1024 bytes
+            const uint64_t dk0 = ptx::smem_desc_sw128(ring, tc::kKmajorLbo, kGroup);
+            const uint64_t dv0 = ptx::smem_desc_sw128(ring, 1024, kGroup);
             // S = q k^T of the K tile in kslot (its buffer is free once the score warps have read it)
             auto issue_s = [&](uint32_t kslot) -> bool {
                 const uint32_t buf = sb.slot();
@@ -824,8 +807,8 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 if (ptx::elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
-                        ptx::mma_ss(col, dq + off, dk + off, g.idesc_s, k > 0);
+                        const uint32_t q_off = ((k / 4) * 16384 + (k % 4) * 32) >> 4, k_off = ((k / 4) * 1024 + (k % 4) * 32) >> 4;
+                        ptx::mma_ss(col, dq + q_off, dk + k_off, g.idesc_s, k > 0);
                     }
                     ptx::mma_commit(full);
                 }
@@ -842,31 +825,31 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     if (r >= left || (absent >> (r >> 3) & 1)) {
 #pragma unroll
                         for (int x = 0; x < D / 8; ++x)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + vslot * TB + (x >> 3) * 16384 + r * 128 + (x & 7) * 16), "r"(0) : "memory");
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + vslot * TB + (r >> 3) * kGroup + (x >> 3) * 1024 + (r & 7) * 128 + (x & 7) * 16), "r"(0) : "memory");
                     }
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             };
             // keys [from, from + 16 n) of the tile
             auto issue_pv = [&](uint32_t vslot, int from, int n, bool accumulate) {
-                const uint64_t dv = dv0 + (uint64_t)((vslot * TB + from * 128) >> 4);
+                const uint64_t dv = dv0 + (uint64_t)((vslot * TB + from / 8 * kGroup) >> 4);
                 const uint32_t words = kSepP ? tmem + kPCol + 64 * w + from / 2 : tmem + w * kKeys + from;
                 if (ptx::elect_one()) {
 #pragma unroll
                     for (int k = 0; k < n; ++k)
-                        ptx::mma_ts(tmem + kOCol + w * D, words + 8 * k, dv + (uint64_t)((k * 2048) >> 4), g.idesc_pv, (accumulate || k > 0) ? 1u : 0u);
+                        ptx::mma_ts(tmem + kOCol + w * D, words + 8 * k, dv + (uint64_t)((k * 2 * kGroup) >> 4), g.idesc_pv, (accumulate || k > 0) ? 1u : 0u);
                 }
                 __syncwarp();
             };
             // kSplit: scores of 64 keys
             auto issue_half = [&](uint32_t kslot, int h) {
-                const uint64_t dq = dq0 + (uint64_t)((w * TB) >> 4), dk = dk0 + (uint64_t)((kslot * TB + h * 8192) >> 4);
+                const uint64_t dq = dq0 + (uint64_t)((w * TB) >> 4), dk = dk0 + (uint64_t)((kslot * TB + h * 8 * kGroup) >> 4);
                 const uint32_t full = LSSAR_AT(s_full) + 16 * w + 8 * h, col = tmem + w * kKeys + h * 64;
                 if (ptx::elect_one()) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
-                        ptx::mma_ss(col, dq + off, dk + off, g.idesc_s64, k > 0);
+                        const uint32_t q_off = ((k / 4) * 16384 + (k % 4) * 32) >> 4, k_off = ((k / 4) * 1024 + (k % 4) * 32) >> 4;
+                        ptx::mma_ss(col, dq + q_off, dk + k_off, g.idesc_s64, k > 0);
                     }
                     ptx::mma_commit(full);
                 }
@@ -881,12 +864,12 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 uint32_t kslot, vslot;
                 if constexpr (PHASE == kStats) {
                     for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
-                        if (!(ok = acquire(kslot))) break;
+                        if (!(ok = acquire(keys, 0, kslot))) break;
                         if (live) ok = issue_s(kslot);
                         commit(LSSAR_AT(kv_empty) + 8 * kslot);
                     }
                 } else {
-                    if (!(ok = acquire(kslot))) break;
+                    if (!(ok = acquire(keys, 0, kslot))) break;
                     if constexpr (kSplit) {
                         if (live) {
                             issue_half(kslot, 0);
@@ -898,13 +881,13 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     commit(LSSAR_AT(kv_empty) + 8 * kslot);
                     for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
                         const bool next = kt + 1 < it.kt1;
-                        if (next && !(ok = acquire(kslot))) break;
+                        if (next && !(ok = acquire(keys, 0, kslot))) break;
                         if constexpr (kSepP) {
                             // the next scores as soon as the score warps have these
                             if (live && next && !(ok = issue_s(kslot))) break;
                             if (next) commit(LSSAR_AT(kv_empty) + 8 * kslot);
                         }
-                        if (!(ok = acquire(vslot))) break;
+                        if (!(ok = acquire(values, NR, vslot))) break;
                         if (live) {
                             clear_rows(vslot, it.len - kt * kKeys);
                             auto o_is_free = [&] {
@@ -1180,6 +1163,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                             row.ref = top;
                             acc = __fmul2_rn(acc, make_float2(alpha, alpha));
                         }
+                        if constexpr (MODE == kLssa) form = __all_sync(0xffffffffu, row.ref >= 0.f) ? kMixed : kAccurate;
                         if constexpr (MODE == kSoftmax) form = __any_sync(0xffffffffu, fabsf(row.ref) > 65536.f) ? kAccurate : kMixed;
                     }
                 }
@@ -1204,10 +1188,6 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     ptx::tmem_st16(p_col + x * 16, pk);
                 }
                 if (!ok) break;
-                // (the tile that raised the last row to 0 was still weighted in the accurate form)
-                if constexpr (MODE == kLssa) {
-                    if (form == kAccurate && __all_sync(0xffffffffu, row.ref >= 0.f)) form = kMixed;
-                }
                 if constexpr (kOnePass) {
                     if (kt > kt0 && __any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
@@ -1226,7 +1206,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 ptx::tc_fence_before();
                 if constexpr (kSplit && kOnePass) {
                     // (the first half's product must not start while the other half's columns of O are rescaled)
-                    if (__any_sync(0xffffffffu, raise)) {
+                    if (kt > kt0 && __any_sync(0xffffffffu, raise)) {
                         ptx::mbar_arrive(LSSAR_AT(tile_max) + 32 * w + 8 * quarter);
                         if (!(ok = wait_all(LSSAR_AT(tile_max) + 32 * w + 8 * quarter, exchanges++ & 1, kErrTileMax))) break;
                     }

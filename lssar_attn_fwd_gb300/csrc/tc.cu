@@ -152,6 +152,19 @@ bool make_page_map(CUtensorMap *m, const void *base, bool half, int d, int rows,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_group_map(CUtensorMap *m, const void *base, bool half, int d, int rows, int n_pages, long long page_stride,
+                    int box_rows) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[5] = {64, 8, (cuuint64_t)d / 64, (cuuint64_t)rows / 8, (cuuint64_t)n_pages};
+    cuuint64_t strides[4] = {(cuuint64_t)d * 2, 128, (cuuint64_t)d * 16, (cuuint64_t)page_stride * 2};
+    cuuint32_t box[5] = {64, 8, (cuuint32_t)d / 64, (cuuint32_t)box_rows / 8, 1};
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return enc(m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base),
+               dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 std::mutex g_sym_mutex;
 unsigned *g_err_ptr[64] = {};

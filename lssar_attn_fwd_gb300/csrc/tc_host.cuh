@@ -29,6 +29,11 @@ bool make_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, int BH, 
 bool make_page_map(CUtensorMap *m, const void *base, bool half, int d, int rows, int n_pages, long long page_stride,
                    int box_rows);
 
+// The same pages as groups of 8 rows, [n_pages][rows / 8][d / 64][8][64], so that one copy takes box_rows
+// whole rows (a multiple of 8): in shared memory the 64-column blocks of a group lie behind one another.
+bool make_group_map(CUtensorMap *m, const void *base, bool half, int d, int rows, int n_pages, long long page_stride,
+                    int box_rows);
+
 // Device address of the library's error word on the current device.
 cudaError_t error_word_ptr(unsigned **out);
 
