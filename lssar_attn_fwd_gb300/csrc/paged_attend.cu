@@ -16,7 +16,7 @@ Layout layout(const PagedAttend &pr, int sms) {
     l.tokens = attend::kPairRows / l.G;
     l.rows = (pr.n < l.tokens ? pr.n : l.tokens) * l.G;
     l.cap128 = (c.capacity() + attend::kKeys - 1) / attend::kKeys * attend::kKeys;
-    const size_t pairs = (size_t)c.B * ((pr.n + l.tokens - 1) / l.tokens), items = pairs * c.Hkv, tiles = items * (l.cap128 / attend::kKeys + attend::kItemCost);
+    const size_t pairs = (size_t)c.B * ((pr.n + l.tokens - 1) / l.tokens), items = pairs * c.Hkv, tiles = items * (2 * (l.cap128 / attend::kKeys) + attend::kItemCost);
     l.ctas = (int)(tiles < (size_t)sms ? tiles : sms);
     const bool norms = uses_normalised_qk(pr.mode), reweight = is_reweight(pr.mode);
     auto r = [](size_t x) { return (x + 255) & ~(size_t)255; };
@@ -34,7 +34,7 @@ Layout layout(const PagedAttend &pr, int sms) {
 
 long long paged_attend_tiles(const PagedAttend &pr) {
     const long long tokens = attend::kPairRows / (pr.H / pr.c.Hkv), pairs = (pr.n + tokens - 1) / tokens;
-    const long long tiles = (pr.c.capacity() + 63) / 64 + attend::kItemCost;      // (the prologue's tiles may be of 64 keys)
+    const long long tiles = (pr.c.capacity() + 63) / 64 + 1 + attend::kItemCost;      // units of cost of an item (at least the prologue's tiles)
     return (long long)pr.c.B * pr.c.Hkv * pairs > (1LL << 31) ? 1LL << 62 : (long long)pr.c.B * pr.c.Hkv * pairs * tiles;
 }
 

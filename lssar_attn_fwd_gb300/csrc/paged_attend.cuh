@@ -61,12 +61,15 @@ static_assert(128 * kCtrlRegs + 512 * kScoreRegs <= kThreads * kLaunchRegs, "reg
 // the one before that (kStats, d = 64; the others leave fewer tiles between).
 constexpr int kInfo = 16;
 constexpr int kItems = 4;                     // depth of the queue of segments
-constexpr int kItemCost = 3;                  // what an item costs beside its tiles, in tiles (they are numbered before its first)
+// What a work item costs, in the units that its run is counted in: of each tile of keys, and beside them (these
+// are numbered before its first tile).  An item of one tile of rows takes a tile of keys in half the time.
+__host__ __device__ constexpr int tile_cost(int rows) { return rows > 128 ? 2 : 1; }
+constexpr int kItemCost = 6;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint32_t kNapProducer = 200;   // ns between its polls of a barrier
 constexpr float kLowest = -3.0e38f;           // below every score, and finite
 enum : unsigned { kErrItem = 61, kErrQ, kErrKvFull, kErrKvEmpty, kErrSFull, kErrSFree, kErrPFull, kErrPFree, kErrOFull, kErrOFree,
-                  kErrHalves, kErrTileMax, kErrDrain };
+                  kErrHalves, kErrTileMax, kErrDrain, kErrJoint };
 
 // One-pass modes: log2 of the largest weight of a row lies in kRoom + [0, kLag] (fp16, whose
 // least step is 2^-24, needs the room; softplus up to 117 leaves less of it).
@@ -79,13 +82,13 @@ constexpr float kTopFp16 = 32768.f;           // re-weighting: the largest weigh
 constexpr float kNoLift = -118.f;             // LSSA: below every score
 
 struct Header {
-    int total, entries, run;                  // tiles, entries, tiles per CTA
+    int total, entries, run;                  // units of cost, entries, units per CTA
 };
 
 struct Scratch {
     Header *head;
-    int4 *entries;        // {sequence, pair, tiles of the pair and its cost, number of the first of them}
-    int *first;           // [ctas] entry of each CTA's first tile
+    int4 *entries;        // {sequence, pair, cost of an item, number of the first item's first unit}
+    int *first;           // [ctas] entry of each CTA's first unit
     float *knorm;         // [B, Hkv, cap128] 1 / |k|
     float2 *stats;        // [item + cta][rows]: m, S1 of a segment's rows
     float2 *sums;         // [2 cta + last][rows]: reference, sum of w
@@ -114,7 +117,8 @@ struct Item {
     int b, h, t0, rows;   // first token, valid rows of the pair
     int base, len;        // slots before the chunk, cached tokens
     int nk, kt0, kt1;     // tiles of the item; those of this segment
-    int item, start;      // number of the item, of its first tile (its cost comes before)
+    int step;             // 2: one tile of rows, whose keys both row slots share, every other tile
+    int item, start;      // number of the item, of its first tile's first unit (its cost comes before)
     int first_bad;        // first slot of a page that is none
 };
 
@@ -123,9 +127,10 @@ struct __align__(16) Shared {
     float m[2][2][2][kTileRows], s[2][2][2][kTileRows];   // [meeting parity][tile][half][row]
     float qq[2][2][2][kTileRows];                         // sum of squares of the next row of q, likewise
     float tmax[2][2][2][kTileRows];                       // [step parity][tile][half][row]
+    float other[2][kTileRows][2];                         // [join parity][row]: the second slot's sums
     uint64_t q_full[2];
     uint64_t s_full[2][2], s_free[2][2];                  // [tile][buffer], or (kSplit) [tile][half]
-    uint64_t p_full[2], p_free[2], o_full[2], o_free[2], halves[2];
+    uint64_t p_full[2], p_free[2], o_full[2], o_free[2], halves[2], joint;
     uint64_t tile_max[2][4];
     uint64_t kv_full[8], kv_empty[8];
     uint64_t item_full[kItems], item_empty[kItems];
@@ -144,6 +149,9 @@ struct Cfg {
     static constexpr int kSmem = kShared + (int)sizeof(Shared) + 1024;
 };
 static_assert(Cfg<64>::kSmem <= 232448 && Cfg<128>::kSmem <= 232448, "shared memory");
+
+// Rows of the pair that starts at token t0, of a sequence with `count` new tokens.
+__device__ __forceinline__ int rows_of_pair(const Args &g, int count, int t0) { return min(g.tokens, count - t0) * g.G; }
 
 // Tiles of a pair that starts at token t0, of a sequence with `count` new tokens after `base`.
 __host__ __device__ __forceinline__ int tiles_of_pair(int base, int count, int t0, int tokens) {
@@ -224,16 +232,20 @@ static __device__ __noinline__ void make_plan(const Args &g) {
         const int pairs = (cnt + g.tokens - 1) / g.tokens;
         long long mine = 0;
 #pragma unroll 1
-        for (int m = 0; m < pairs; ++m) mine += kItemCost + tiles_of_pair(len - cnt, cnt, m * g.tokens, g.tokens);
+        for (int m = 0; m < pairs; ++m) {
+            const int rows = rows_of_pair(g, cnt, m * g.tokens);
+            mine += kItemCost + tile_cost(rows) * tiles_of_pair(len - cnt, cnt, m * g.tokens, g.tokens);
+        }
         long long e = pairs, t = mine * c.Hkv, te, tt;
         block_prefix(e, t, te, tt, part);
         e += entries;
         t += tiles;
 #pragma unroll 1
         for (int m = 0; m < pairs; ++m) {
-            const int nk = kItemCost + tiles_of_pair(len - cnt, cnt, m * g.tokens, g.tokens);
-            g.s.entries[e++] = make_int4(b, m, nk, (int)t);
-            t += (long long)nk * c.Hkv;
+            const int rows = rows_of_pair(g, cnt, m * g.tokens);
+            const int cost = kItemCost + tile_cost(rows) * tiles_of_pair(len - cnt, cnt, m * g.tokens, g.tokens);
+            g.s.entries[e++] = make_int4(b, m, cost, (int)t);
+            t += (long long)cost * c.Hkv;
         }
         entries += te;
         tiles += tt;
@@ -250,7 +262,7 @@ static __device__ __noinline__ void make_plan(const Args &g) {
         }
     }
     __syncthreads();
-    const int run = max(1, (int)((tiles + g.ctas - 1) / g.ctas));
+    const int run = max(2, (int)((tiles + g.ctas - 1) / g.ctas));      // (2: a tile's last unit lies in every run)
     if (threadIdx.x == 0) *g.s.head = Header{(int)tiles, (int)entries, run};
     for (int cta = threadIdx.x; cta < g.ctas; cta += kPrepThreads) {
         const long long t = (long long)cta * run;
@@ -578,6 +590,25 @@ struct Ring {
     __device__ __forceinline__ bool reused() const { return i >= N; }
 };
 
+// The rows of q of the segment at shared address `it` for tile slot w: this thread's half of row `in`.
+template <int D>
+__device__ __noinline__ bool gather_rows(const Args &g, uint32_t it, uint32_t sq, int w, int half, int in) {
+    const PagedAttend &a = g.a;
+    auto next = [&](size_t offset) { return ptx::ld_shared_s32(it + (uint32_t)offset); };
+    const int rows = next(offsetof(Item, rows)), kt0 = next(offsetof(Item, kt0)), shared_rows = next(offsetof(Item, step)) - 1;
+    if (kt0 < 0 || kt0 + shared_rows * w >= next(offsetof(Item, kt1))) return false;
+    const int v = min((shared_rows ? 0 : w * kTileRows) + in, rows - 1), tok = v / g.G, head = next(offsetof(Item, h)) * g.G + v - tok * g.G;
+    const uint16_t *src = static_cast<const uint16_t *>(a.q) + next(offsetof(Item, b)) * a.qs[0] + head * a.qs[1] +
+                          (next(offsetof(Item, t0)) + tok) * a.qs[2] + half * (D / 2);
+    const uint32_t dst = sq + w * Cfg<D>::kTile + (D == 128 ? half * (kTileRows * 128) : 0) + in * 128;
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+        const int piece = D == 128 ? x : half * 4 + x;
+        cp_async16(dst + ((piece ^ (in & 7)) << 4), src + x * 8);
+    }
+    return true;
+}
+
 template <int D, int MODE, bool HALF, int PHASE>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm, const __grid_constant__ Args g) {
@@ -618,6 +649,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             init(&sh->halves[i], 256);
             for (int j = 0; j < 4; ++j) init(&sh->tile_max[i][j], 64);
         }
+        init(&sh->joint, PHASE == kStats ? 256 : 512);
         for (int i = 0; i < 8; ++i) {
             init(&sh->kv_full[i], 1);
             init(&sh->kv_empty[i], 2);
@@ -717,35 +749,43 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 const Header head = *g.s.head;
                 const int t1 = min((long long)head.total, (long long)(blockIdx.x + 1) * head.run);
                 long long t = (long long)blockIdx.x * head.run;
-                int e = 0, h = 0, kt = 0;
+                int e = 0, h = 0, at = 0;       // the item, and the unit of it
                 int4 en = make_int4(0, 0, 0, 0);
                 if (t < t1) {
                     e = g.s.first[blockIdx.x];
                     en = g.s.entries[e];
                     h = (int)(t - en.w) / en.z;
-                    kt = (int)(t - en.w) - h * en.z;
+                    at = (int)(t - en.w) - h * en.z;
                 }
                 while (ok) {
                     const uint32_t slot = items.slot();
                     if (items.reused() && !wait_all(LSSAR_AT(item_empty) + 8 * slot, items.parity() ^ 1, kErrItem)) break;
-                    // (tiles of the item up to the run's end; none where only its cost lies before it)
-                    const int kt1 = t < t1 ? (int)min((long long)en.z, kt + t1 - t) - kItemCost : 0;
+                    // the tiles of the item whose last unit lies in the run
                     it.kt0 = -1;
-                    if (kt1 > 0) {
+                    if (t < t1) {
                         const int cnt = a.counts ? a.counts[en.x] : a.n;
                         it.b = en.x;
                         it.h = h;
                         it.t0 = en.y * g.tokens;
-                        it.rows = min(g.tokens, cnt - it.t0) * g.G;
+                        it.rows = rows_of_pair(g, cnt, it.t0);
                         it.len = c.lens[en.x];
                         it.base = it.len - cnt;
-                        it.nk = en.z - kItemCost;
-                        it.kt0 = max(kt - kItemCost, 0);
-                        it.kt1 = kt1;
+                        const int cost = kItemCost, each = tile_cost(it.rows), end = (int)min((long long)en.z, at + t1 - t);
+                        it.nk = (en.z - cost) / each;
+                        it.kt0 = max(at - cost, 0) / each;
+                        it.kt1 = max(end - cost, 0) / each;
                         it.item = e * c.Hkv + h;
-                        it.start = en.w + h * en.z + kItemCost;
+                        it.start = en.w + h * en.z + cost;
+                        t += end - at;
+                        at = 0;
+                        it.step = it.rows > kTileRows ? 1 : 2;
                         it.first_bad = 0x7fffffff;
-                        if (!dcheck(e < head.entries && h < c.Hkv && it.kt1 > it.kt0 && it.rows > 0 && it.rows <= g.rows, err, kDbgItem)) it.kt0 = -1;
+                        if (!dcheck(e < head.entries && h < c.Hkv && it.kt1 >= it.kt0 && it.rows > 0 && it.rows <= g.rows, err, kDbgItem)) it.kt0 = -1;
+                        if (t < t1 && ++h == c.Hkv) {
+                            h = 0;
+                            en = g.s.entries[++e];
+                        }
+                        if (it.kt0 >= 0 && it.kt0 == it.kt1) continue;      // none (part of the item's cost, of a tile's)
                     }
                     if (lane == 0) {
                         sh->items[slot] = it;
@@ -755,12 +795,6 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     ++items.i;
                     if (it.kt0 < 0) break;
                     load_tiles(slot);
-                    t += kt1 + kItemCost - kt;
-                    kt = 0;
-                    if (t < t1 && ++h == c.Hkv) {
-                        h = 0;
-                        en = g.s.entries[++e];
-                    }
                 }
             } else if constexpr (PHASE == kValues) {
                 while (ok && next_item(it)) {
@@ -855,74 +889,94 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 }
                 __syncwarp();
             };
+            // the stage of tile kt, past those before it, which are the other slot's
+            auto take = [&](Ring<NR> &tiles, uint32_t first, int &pos, int kt, uint32_t &stage) -> bool {
+                while (acquire(tiles, first, stage)) {
+                    if (pos++ == kt) return true;
+                    if (lane == 0) ptx::mbar_arrive(LSSAR_AT(kv_empty) + 8 * stage);
+                }
+                return false;
+            };
             Item it;
             while (ok && next_item(it)) {
                 release_item();
-                const bool live = it.rows > w * kTileRows;
-                if (live && !(ok = wait_all(LSSAR_AT(q_full) + 8 * w, qs++ & 1, kErrQ))) break;
-                ptx::tc_fence_after();
+                const int step = it.step, begin = it.kt0 + (step == 2 ? w : 0);
+                const bool live = begin < it.kt1;
+                int kpos = it.kt0, vpos = it.kt0;
                 uint32_t kslot, vslot;
-                if constexpr (PHASE == kStats) {
-                    for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
-                        if (!(ok = acquire(keys, 0, kslot))) break;
-                        if (live) ok = issue_s(kslot);
-                        commit(LSSAR_AT(kv_empty) + 8 * kslot);
-                    }
-                } else {
-                    if (!(ok = acquire(keys, 0, kslot))) break;
-                    if constexpr (kSplit) {
-                        if (live) {
-                            issue_half(kslot, 0);
-                            issue_half(kslot, 1);
+                if (live) {
+                    if (!(ok = wait_all(LSSAR_AT(q_full) + 8 * w, qs++ & 1, kErrQ))) break;
+                    ptx::tc_fence_after();
+                    if constexpr (PHASE == kStats) {
+                        for (int kt = begin; ok && kt < it.kt1; kt += step) {
+                            if (!(ok = take(keys, 0, kpos, kt, kslot)) || !(ok = issue_s(kslot))) break;
+                            commit(LSSAR_AT(kv_empty) + 8 * kslot);
                         }
                     } else {
-                        if (live && !(ok = issue_s(kslot))) break;
+                        if (!(ok = take(keys, 0, kpos, begin, kslot))) break;
+                        if constexpr (kSplit) {
+                            issue_half(kslot, 0);
+                            issue_half(kslot, 1);
+                        } else {
+                            if (!(ok = issue_s(kslot))) break;
+                        }
+                        commit(LSSAR_AT(kv_empty) + 8 * kslot);
                     }
-                    commit(LSSAR_AT(kv_empty) + 8 * kslot);
-                    for (int kt = it.kt0; ok && kt < it.kt1; ++kt) {
-                        const bool next = kt + 1 < it.kt1;
-                        if (next && !(ok = acquire(keys, 0, kslot))) break;
+                }
+                if constexpr (PHASE == kValues) {
+                    for (int kt = begin; ok && kt < it.kt1; kt += step) {
+                        const bool next = kt + step < it.kt1;
+                        if (next && !(ok = take(keys, 0, kpos, kt + step, kslot))) break;
                         if constexpr (kSepP) {
                             // the next scores as soon as the score warps have these
-                            if (live && next && !(ok = issue_s(kslot))) break;
+                            if (next && !(ok = issue_s(kslot))) break;
                             if (next) commit(LSSAR_AT(kv_empty) + 8 * kslot);
                         }
-                        if (!(ok = acquire(values, NR, vslot))) break;
-                        if (live) {
-                            clear_rows(vslot, it.len - kt * kKeys);
-                            auto o_is_free = [&] {
-                                return kt > it.kt0 || segs == 0 || wait_all(LSSAR_AT(o_free) + 8 * w, (segs - 1) & 1, kErrOFree);
-                            };
-                            if constexpr (kSplit) {
+                        if (!(ok = take(values, NR, vpos, kt, vslot))) break;
+                        clear_rows(vslot, it.len - kt * kKeys);
+                        auto o_is_free = [&] {
+                            return kt > begin || segs == 0 || wait_all(LSSAR_AT(o_free) + 8 * w, (segs - 1) & 1, kErrOFree);
+                        };
+                        if constexpr (kSplit) {
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    // this half's weights are in place of its scores
-                                    if (!(ok = wait_all(LSSAR_AT(s_free) + 16 * w + 8 * h, pv & 1, kErrSFree))) break;
-                                    if (h == 0 && !(ok = o_is_free())) break;
-                                    ptx::tc_fence_after();
-                                    issue_pv(vslot, 64 * h, 4, kt > it.kt0 || h > 0);
-                                    // (before the commits that nothing waits for: each takes some 300 cycles)
-                                    if (next) issue_half(kslot, h);
-                                }
-                                if (!ok) break;
-                            } else {
-                                if (!(ok = wait_all(kSepP ? LSSAR_AT(p_full) + 8 * w : LSSAR_AT(s_free) + 16 * w, pv & 1, kErrPFull)) || !(ok = o_is_free())) break;
+                            for (int h = 0; h < 2; ++h) {
+                                // this half's weights are in place of its scores
+                                if (!(ok = wait_all(LSSAR_AT(s_free) + 16 * w + 8 * h, pv & 1, kErrSFree))) break;
+                                if (h == 0 && !(ok = o_is_free())) break;
                                 ptx::tc_fence_after();
-                                // (at d = 128 P's words are over the first half of each half of S)
-                                issue_pv(vslot, 0, kSepP ? 8 : 4, kt > it.kt0);
-                                if constexpr (!kSepP) issue_pv(vslot, 64, 4, true);
-                                if constexpr (kSepP) commit(LSSAR_AT(p_free) + 8 * w);
-                                else if (next && !(ok = issue_s(kslot))) break;
+                                issue_pv(vslot, 64 * h, 4, kt > begin || h > 0);
+                                // (before the commits that nothing waits for: each takes some 300 cycles)
+                                if (next) issue_half(kslot, h);
                             }
-                            ++pv;
-                            if (!next) {
-                                commit(LSSAR_AT(o_full) + 8 * w);
-                                ++segs;
-                            }
+                            if (!ok) break;
+                        } else {
+                            if (!(ok = wait_all(kSepP ? LSSAR_AT(p_full) + 8 * w : LSSAR_AT(s_free) + 16 * w, pv & 1, kErrPFull)) || !(ok = o_is_free())) break;
+                            ptx::tc_fence_after();
+                            // (at d = 128 P's words are over the first half of each half of S)
+                            issue_pv(vslot, 0, kSepP ? 8 : 4, kt > begin);
+                            if constexpr (!kSepP) issue_pv(vslot, 64, 4, true);
+                            if constexpr (kSepP) commit(LSSAR_AT(p_free) + 8 * w);
+                            else if (next && !(ok = issue_s(kslot))) break;
+                        }
+                        ++pv;
+                        if (!next) {
+                            commit(LSSAR_AT(o_full) + 8 * w);
+                            ++segs;
                         }
                         commit(LSSAR_AT(kv_empty) + 8 * vslot);
                         if (!kSepP && next) commit(LSSAR_AT(kv_empty) + 8 * kslot);
                     }
+                }
+                // the last tiles may be the other slot's
+                while (ok && kpos < it.kt1) {
+                    if (!(ok = acquire(keys, 0, kslot))) break;
+                    ++kpos;
+                    if (lane == 0) ptx::mbar_arrive(LSSAR_AT(kv_empty) + 8 * kslot);
+                }
+                while (ok && PHASE == kValues && vpos < it.kt1) {
+                    if (!(ok = acquire(values, NR, vslot))) break;
+                    ++vpos;
+                    if (lane == 0) ptx::mbar_arrive(LSSAR_AT(kv_empty) + 8 * vslot);
                 }
             }
             __syncwarp();
@@ -944,7 +998,8 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
         constexpr uint32_t kParity = 4 * kTileRows * 4;
         constexpr float kMasked = MODE == kSigmoidRw ? INFINITY : -INFINITY;
         Ring<kSBufs> sb;
-        uint32_t pv = 0, segs = 0, exchanges = 0;
+        uint32_t pv = 0, exchanges = 0, joints = 0;
+        uint32_t own_segs = 0, other_segs = 0;                   // segments with this slot, with the other
         uint32_t tiles = 0;            // tiles of keys that the CTA has taken
         const int run = g.s.head->run;
         bool ok = true;
@@ -953,21 +1008,8 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
         // The next segment's rows of q (any strides, any group): each thread half of its row, into the tile
         // that the last product of the segment before has read.  Returns whether this tile has any.
         auto gather = [&](uint32_t slot, bool &some) -> bool {
-            const uint32_t it = LSSAR_AT(items) + slot % kItems * (uint32_t)sizeof(Item);
             if (!wait_all(LSSAR_AT(item_full) + 8 * (slot % kItems), slot / kItems & 1, kErrItem)) return false;
-            auto next = [&](size_t offset) { return ptx::ld_shared_s32(it + (uint32_t)offset); };
-            const int rows = next(offsetof(Item, rows));
-            some = next(offsetof(Item, kt0)) >= 0 && rows > w * kTileRows;
-            if (!some) return true;
-            const int v = min(w * kTileRows + in, rows - 1), tok = v / g.G, head = next(offsetof(Item, h)) * g.G + v - tok * g.G;
-            const uint16_t *src = static_cast<const uint16_t *>(a.q) + next(offsetof(Item, b)) * a.qs[0] + head * a.qs[1] +
-                                  (next(offsetof(Item, t0)) + tok) * a.qs[2] + half * (D / 2);
-            const uint32_t dst = sq + w * TB + (D == 128 ? half * (kTileRows * 128) : 0) + in * 128;
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
-                const int piece = D == 128 ? x : half * 4 + x;
-                cp_async16(dst + ((piece ^ (in & 7)) << 4), src + x * 8);
-            }
+            some = gather_rows<D>(g, LSSAR_AT(items) + slot % kItems * (uint32_t)sizeof(Item), sq, w, half, in);
             return true;
         };
         // ... they are there; the normalised modes need their norms, whose halves meet next
@@ -1008,9 +1050,12 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
         };
         while (ok) {
             if (!wait_all(LSSAR_AT(item_full) + 8 * items.slot(), items.parity(), kErrItem)) break;
-            const int kt0 = LSSAR_ITEM(kt0), kt1 = LSSAR_ITEM(kt1), rows = LSSAR_ITEM(rows);
+            const int kt0 = LSSAR_ITEM(kt0), kt1 = LSSAR_ITEM(kt1), rows = LSSAR_ITEM(rows), step = LSSAR_ITEM(step);
             if (kt0 < 0) break;
-            if (rows <= w * kTileRows) {                         // none of this tile's
+            // this slot's first tile, and its first row of the item
+            const int begin = kt0 + (step - 1) * w, row0 = step == 1 ? w * kTileRows : 0;
+            if (begin >= kt1) {                                  // nothing for this slot
+                ++other_segs;
                 tiles += kt1 - kt0;
                 if ((ok = gather(items.i + 1, some))) {
                     hand_over(some);
@@ -1019,8 +1064,8 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 release_item();
                 continue;
             }
-            const bool live = rows > w * kTileRows + quarter * 32;
-            const int v = min(w * kTileRows + in, rows - 1);     // row of the pair (past the last: the last)
+            const bool live = rows > row0 + quarter * 32;
+            const int v = min(row0 + in, rows - 1);              // row of the pair (past the last: the last)
             // last slot that the row attends to, and that of the warp's first row
             const int limit = LSSAR_ITEM(base) + LSSAR_ITEM(t0) + v / g.G;
             const int least = __shfl_sync(0xffffffffu, limit, 0);
@@ -1035,7 +1080,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             if constexpr (PHASE == kValues && is_reweight(MODE)) {
                 // the row's maximum and sum from the segments of its item
                 float m = kLowest, s1 = 0.f;
-                const int start = LSSAR_ITEM(start), c0 = start / run, c1 = (start + LSSAR_ITEM(nk) - 1) / run;
+                const int start = LSSAR_ITEM(start), each = tile_cost(rows), c0 = (start + each - 1) / run, c1 = (start + LSSAR_ITEM(nk) * each - 1) / run;
                 const float2 *part = g.s.stats + (size_t)LSSAR_ITEM(item) * g.rows + v;
 #pragma unroll 4
                 for (int cta = c0; cta <= c1; ++cta) {
@@ -1056,12 +1101,12 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             }
             float m_run = MODE == kSigmoidRw ? INFINITY : MODE == kLssar ? kLowest : -INFINITY, sum_run = 0.f;
             float2 acc = make_float2(0.f, 0.f);
-            for (int kt = kt0; kt < kt1; ++kt, ++tiles) {
+            for (int kt = begin; kt < kt1; kt += step) {
                 const uint32_t buf = sb.slot(), col = s_col + buf * kKeys;
                 if (!(ok = wait_all(s_full + 8 * buf, sb.parity(), kErrSFull))) break;
                 ++sb.i;
                 ptx::tc_fence_after();
-                if (kt + 1 == kt1) {
+                if (kt + step >= kt1) {
                     // the last product with this q is done (kSplit: the other half's too)
                     if (kSplit && !(ok = wait_all(LSSAR_AT(s_full) + 16 * w + 8 * (half ^ 1), (sb.i - 1) & 1, kErrSFull))) break;
                     if (!(ok = gather(items.i + 1, some))) break;
@@ -1078,7 +1123,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     }
                     continue;
                 }
-                const uint32_t knorm = LSSAR_AT(knorm) + tiles % kInfo * (kKeys * 4) + half * 256;
+                const uint32_t knorm = LSSAR_AT(knorm) + (tiles + (kt - kt0)) % kInfo * (kKeys * 4) + half * 256;
                 const int last = limit - kt * kKeys - half * 64;      // last column of the half that is not masked
                 const bool masked = least < kt * kKeys + half * 64 + 63;
                 if constexpr (PHASE == kStats) {
@@ -1189,7 +1234,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 }
                 if (!ok) break;
                 if constexpr (kOnePass) {
-                    if (kt > kt0 && __any_sync(0xffffffffu, raise)) {
+                    if (kt > begin && __any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
                         for (int x = 0; x < D / 2; x += 16) {
                             uint32_t o[16];
@@ -1206,7 +1251,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 ptx::tc_fence_before();
                 if constexpr (kSplit && kOnePass) {
                     // (the first half's product must not start while the other half's columns of O are rescaled)
-                    if (kt > kt0 && __any_sync(0xffffffffu, raise)) {
+                    if (kt > begin && __any_sync(0xffffffffu, raise)) {
                         ptx::mbar_arrive(LSSAR_AT(tile_max) + 32 * w + 8 * quarter);
                         if (!(ok = wait_all(LSSAR_AT(tile_max) + 32 * w + 8 * quarter, exchanges++ & 1, kErrTileMax))) break;
                     }
@@ -1215,6 +1260,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 ++pv;
             }
             if (!ok) break;
+            tiles += kt1 - kt0;
             hand_over(some);
             // the two halves of a row meet
             const uint32_t par = meets & 1;
@@ -1224,13 +1270,35 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             if constexpr (PHASE == kStats) ptx::st_shared_f32(LSSAR_AT(m) + par * kParity + mine, m_part);
             if (!(ok = meet())) break;
             const float other = ptx::ld_shared_f32(LSSAR_AT(s) + par * kParity + others);
-            const bool valid = w * kTileRows + in < rows;
+            const bool valid = row0 + in < rows;
+            // Two slots with the same rows: the first adds the second's part to its own.
+            const bool both = step == 2 && kt0 + 1 < kt1, second = both && w == 1;
+            const uint32_t joint_at = (joints & 1) * (2 * kTileRows * 4) + 8 * in;
+            auto join = [&](float x, float y) -> bool {           // the second's pair of values in place, or there
+                if (second) {
+                    if (joints > 0 && !wait_all(LSSAR_AT(joint), (joints - 1) & 1, kErrJoint)) return false;
+                    if (half == 0) {
+                        ptx::st_shared_f32(LSSAR_AT(other) + joint_at, x);
+                        ptx::st_shared_f32(LSSAR_AT(other) + joint_at + 4, y);
+                    }
+                }
+                ptx::mbar_arrive(LSSAR_AT(joint));
+                return second || wait_all(LSSAR_AT(joint), joints & 1, kErrJoint);
+            };
             if constexpr (PHASE == kStats) {
-                if (half == 0 && valid) {
-                    const float m1 = ptx::ld_shared_f32(LSSAR_AT(m) + par * kParity + others), m = fmaxf(m_part, m1);
-                    const float s = MODE == kSoftmaxRw ? part * ptx::ex2(m_part - m) + other * ptx::ex2(m1 - m) : part + other;
+                if (half == 0) {
+                    const float m1 = ptx::ld_shared_f32(LSSAR_AT(m) + par * kParity + others);
+                    float m = fmaxf(m_part, m1), s = MODE == kSoftmaxRw ? part * ptx::ex2(m_part - m) + other * ptx::ex2(m1 - m) : part + other;
+                    if (both) {
+                        if (!(ok = join(m, s))) break;
+                        const float mo = ptx::ld_shared_f32(LSSAR_AT(other) + joint_at), so = ptx::ld_shared_f32(LSSAR_AT(other) + joint_at + 4);
+                        const float top = fmaxf(m, mo);
+                        s = MODE == kSoftmaxRw ? s * ptx::ex2(m - top) + so * ptx::ex2(mo - top) : s + so;
+                        m = top;
+                        ++joints;
+                    }
                     const long long at = LSSAR_ITEM(item) + (long long)blockIdx.x;
-                    if (dcheck(v < g.rows, err, kDbgGlobal)) g.s.stats[at * g.rows + v] = make_float2(m, s);
+                    if (valid && !second && dcheck(v < g.rows, err, kDbgGlobal)) g.s.stats[at * g.rows + v] = make_float2(m, s);
                 }
                 release_item();
                 continue;
@@ -1238,8 +1306,32 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             // (half 0's part first in both, so that both see the same sum)
             float sum = half == 0 ? part + other : other + part;
             if (limit >= LSSAR_ITEM(first_bad)) sum = NAN;
-            if (!(ok = wait_all(LSSAR_AT(o_full) + 8 * w, segs & 1, kErrOFull))) break;
-            ++segs;
+            float ref = MODE == kSoftmax ? row.x : row.ref, f = 1.f, fo = 0.f;      // the parts' factors
+            if (both) {
+                if (!(ok = join(ref, sum))) break;
+                fo = 1.f;
+                if (!second) {
+                    const float ro = ptx::ld_shared_f32(LSSAR_AT(other) + joint_at), so = ptx::ld_shared_f32(LSSAR_AT(other) + joint_at + 4);
+                    if constexpr (kOnePass) {
+                        const float top = fmaxf(ref, ro);
+                        f = ptx::ex2(ref - top);
+                        fo = ptx::ex2(ro - top);
+                        ref = top;
+                    }
+                    sum = sum * f + so * fo;
+                }
+                ++joints;
+            }
+            if (!second) {
+                if (!(ok = wait_all(LSSAR_AT(o_full) + 8 * w, own_segs & 1, kErrOFull))) break;
+                if (both && !(ok = wait_all(LSSAR_AT(o_full) + 8 * (w ^ 1), other_segs & 1, kErrOFull))) break;
+            }
+            ++own_segs;
+            if (step == 1 || both) ++other_segs;
+            if (second) {
+                release_item();
+                continue;
+            }
             ptx::tc_fence_after();
             const int b = LSSAR_ITEM(b), hq = LSSAR_ITEM(h) * g.G + v % g.G, t = LSSAR_ITEM(t0) + v / g.G;
             const bool whole = kt0 == 0 && kt1 == LSSAR_ITEM(nk);
@@ -1248,12 +1340,18 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             const size_t to = (size_t)place * g.rows + v;
             const bool in_range = dcheck(b < c.B && hq < a.H && t < a.n && v < g.rows && place < 2 * g.ctas, err, kDbgGlobal);
             const float inv = 1.f / sum;
-            if (valid && in_range && !whole && half == 0) g.s.sums[to] = make_float2(MODE == kSoftmax ? row.x : row.ref, sum);
+            if (valid && in_range && !whole && half == 0) g.s.sums[to] = make_float2(ref, sum);
             if (live) {
 #pragma unroll 1
                 for (int x = 0; x < D / 64; ++x) {
                     uint32_t o[32];
                     load(o, o_col + x * 32);
+                    if (both) {
+                        uint32_t p[32];
+                        load(p, o_col + D + x * 32);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f + __uint_as_float(p[j]) * fo);
+                    }
                     if (!valid || !in_range) continue;
                     if (whole) {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + (((size_t)b * a.H + hq) * a.n + t) * D + half * (D / 2) + x * 32);
@@ -1276,6 +1374,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             }
             ptx::tc_fence_before();
             ptx::mbar_arrive(LSSAR_AT(o_free) + 8 * w);
+            if (both) ptx::mbar_arrive(LSSAR_AT(o_free) + 8 * (w ^ 1));
             release_item();
         }
 #undef LSSAR_ITEM
@@ -1308,11 +1407,12 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const __grid_constan
     if (some) {
         en = g.s.entries[g.s.first[cta]];
         h = (int)(x - en.w) / en.z;
-        const int start = en.w + h * en.z + kItemCost;         // the item's first tile, behind its cost
-        some = start < x && x - head.run <= start;
-        last = (start + en.z - kItemCost - 1) / head.run;
         t0 = en.y * g.tokens;
-        rows = min(g.tokens, (a.counts ? a.counts[en.x] : a.n) - t0) * g.G;
+        rows = rows_of_pair(g, a.counts ? a.counts[en.x] : a.n, t0);
+        // the runs of its first and last tile
+        const int each = tile_cost(rows), start = en.w + h * en.z + kItemCost;
+        last = (en.w + (h + 1) * en.z - 1) / head.run;
+        some = (start + each - 1) / head.run == cta - 1 && last >= cta;
     }
     ptx::grid_dependency_wait();               // the segments' parts too (in every block: the call's end waits for them)
     if (!some) return;
