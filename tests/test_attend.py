@@ -495,3 +495,121 @@ def test_calls_on_two_streams_at_once(torch_mod):
     assert api.device_error_word() == 0
     for i in (0, 1):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+def test_chunks_of_too_many_tiles_are_refused(lib):
+    # 65535 sequences x 32 pairs of tiles x 2055 units, 8192 key heads x 64 x 4103: more than an int numbers
+    c = desc(B=65535, Hkv=1, max_pages=8192, page_stride=1024)
+    assert attend(lib, c, qs=(1 << 20, 64, 8192), H=128, n=64, mode=0) == -2
+    c = desc(B=4096, Hkv=2, max_pages=16384, page_stride=2048)
+    assert attend(lib, c, qs=(1 << 22, 64, 128), H=2, n=16384, mode=0) == -2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("p", [2, 4, 5, 6, 7, 9, 16, 27, 45, 127, 243, 1000, 1024])
+@pytest.mark.parametrize("mode", [MODE_LSSAR, MODE_SOFTMAX_RW])
+def test_exponents(torch_mod, mode, p):
+    c = Cache(torch_mod, [200, 3, 41], 2, 64, 16, seed=p)
+    check_attend(torch_mod, c, chunk_q(c, 4, 41), [30, 3, 41], mode, p)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,half", [(64, False), (128, False), (64, True), (128, True)])
+def test_chunks_of_one_tile_of_rows_beside_larger_ones(torch_mod, d, half):
+    # items of at most 128 rows (both row slots share their keys) of 1, 2, 3, .. tiles, between items of more rows:
+    # several of either kind for each SM, in any order
+    lens = [40, 128, 129, 256, 257, 384, 385, 700, 130, 1, 300, 900] * 4
+    counts = [3, 100, 1, 40, 257, 64, 2, 300, 130, 1, 129, 128] * 4
+    c = Cache(torch_mod, lens, 9, d, 16, half=half, seed=d)
+    some = [sorted({0, n // 2, n - 1, min(127, n - 1), min(128, n - 1)}) for n in counts]
+    q = chunk_q(c, 18, 300)
+    for b, n in enumerate(counts):
+        q[b, :, n:] = float("nan")
+    for mode, p in MODES:
+        check_attend(torch_mod, c, q, counts, mode, p, some)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_pages_under_one_tile_of_rows(torch_mod, d):
+    # 40 rows on 1 to 4 tiles, whose slots take turns: NaN where a row attends to the page, the same bits elsewhere
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    c = Cache(torch, [60, 200, 330, 500], 2, d, 16, seed=6)
+    q = chunk_q(c, 2, 40)
+    for mode in (MODE_LSSAR, MODE_SOFTMAX, MODE_LSSA, MODE_SIGMOID_RW):
+        good = api.lssar_paged_attend(q, *c.args(), mode=mode)
+        assert api.device_error_word() == 0 and good.isfinite().all()
+        for b, n in enumerate(c.lens.tolist()):
+            for column in sorted({0, 9, 17, 26, (n - 20) // 16}):
+                if 16 * column >= n:
+                    continue
+                table = c.table.clone()
+                table[b, column] = -1
+                out = api.lssar_paged_attend(q, c.k, c.v, table, c.lens, mode=mode)
+                assert api.device_error_word() == PAGE
+                first = max(0, 16 * column - (n - 40))           # row t attends to slots up to n - 40 + t
+                want = good.clone()
+                want[b, :, first:] = float("nan")
+                assert torch.equal(out.isnan(), want.isnan()), (mode, b, column)
+                assert torch.equal(out.nan_to_num(), want.nan_to_num()), (mode, b, column)
+
+
+@pytest.mark.gpu
+def test_results_on_another_stream_take_no_block_in_use(torch_mod):
+    # blocks of the results' sizes, just freed on the current stream, are still written by what is queued there
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    c = Cache(torch, [40, 30], 2, 64, 16, seed=3)
+    lens, counts = ints(torch, 20, 2), ints(torch, 1, 3)
+    q, new, r = chunk_q(c, 4, 8), chunk_q(c, 2, 8), api.Rotary(64)
+    free, count = torch.arange(40, dtype=torch.int32).cuda(), ints(torch, 30)
+    calls = [lambda s: [api.lssar_paged_attend(q, *c.args(), stream=s)],
+             lambda s: list(api.lssar_rope(q, new, r, stream=s)),
+             lambda s: list(api.lssar_rope_bwd(q, new, r, stream=s)),
+             lambda s: list(api.lssar_paged_append_rope(q, new, new, c.k, c.v, c.table, lens, r, stream=s)),
+             lambda s: list(api.lssar_paged_reserve(c.table.clone(), lens, counts, 16, free, count, stream=s)),
+             lambda s: [api.lssar_paged_release(c.table, ints(torch, 40, 30), lens, 16, free.clone(), count, stream=s)]]
+    side = torch.cuda.Stream()
+    for i, call in enumerate(calls):
+        want = call(None)
+        torch.cuda.synchronize()
+        for stream in (side, side.cuda_stream):
+            blocks = [torch.empty_like(w) for w in want for _ in range(4)]
+            torch.cuda._sleep(100_000_000)     # about 50 ms
+            for b in blocks:
+                b.fill_(77)
+            del blocks, b
+            got = call(stream)
+            torch.cuda.synchronize()
+            for a, w in zip(got, want):
+                view = torch.int16 if w.element_size() == 2 else torch.int32
+                assert torch.equal(a.view(view), w.view(view)), i
+    assert api.device_error_word() == 0
+
+
+@pytest.mark.gpu
+def test_debug_build_of_a_serving_step(torch_mod, monkeypatch):
+    # pages, appends and chunks of both kinds in the debug-check build: the same bits, nothing recorded
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api, build
+    build.build(debug=True)
+    results = []
+    for lib in (api.load_library(), api.load_debug_library()):
+        monkeypatch.setattr(api, "_LIB", lib)
+        s, got = Serving(torch, 5, width=40, n_pages=120), []
+        for want in ([500, 30, 200], [64, 9, 1], [1, 300, 40], [70, 70, 128]):
+            got += [x.clone() for x in s.chunk(*s.inputs(max(want)), ints(torch, *want))]
+            before = s.lens.clone()
+            s.lens.copy_(s.after), s.free_count.copy_(s.fo), s.seen.add_(s.counts)
+            if want[1] == 9:
+                before.copy_(s.lens)
+                s.lens[0] = 0
+                s.seen[0] = 0
+                s.free_count.copy_(api.lssar_paged_release(s.table, before, s.lens, s.page, s.free, s.free_count))
+        torch.cuda.synchronize()
+        assert api.device_error_word() == 0
+        results.append(got + [s.k, s.v, s.table, s.lens, s.free_count, s.scores, s.positions])
+    for a, b in zip(*results):
+        view = torch.int16 if a.element_size() == 2 else torch.int32
+        assert torch.equal(a.view(view), b.view(view))
