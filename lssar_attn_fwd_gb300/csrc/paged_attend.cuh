@@ -1127,6 +1127,70 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 const int last = limit - kt * kKeys - half * 64;      // last column of the half that is not masked
                 const bool masked = least < kt * kKeys + half * 64 + 63;
                 if constexpr (PHASE == kStats) {
+                    if constexpr (MODE == kLssar) {
+                        // Softplus by one exponential a score, in one block with the norms' products; again (rare), or
+                        // under a mask, with the choice made for each 32 columns.
+                        bool again = masked;
+                        if (!masked) {
+                            uint32_t r0[32], r1[32];
+                            load(r0, col);
+                            float2 sum = acc, prod[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
+                            to_z<kNorm>(r0, knorm, row.a);
+                            float top = max_of(r0, -INFINITY);
+                            softplus_sum<false>(r0, sum, prod[0]);
+                            load(r1, col + 32);
+                            to_z<kNorm>(r1, knorm + 128, row.a);
+                            top = max_of(r1, top);
+                            softplus_sum<false>(r1, sum, prod[1]);
+                            m_run = fmaxf(m_run, top);
+                            again = __any_sync(0xffffffffu, top < 0.f);
+                            if (!again) {
+                                acc = sum;
+                                sum_run += ptx::lg2((prod[0].x * prod[0].y) * (prod[1].x * prod[1].y));
+                            }
+                        }
+                        if (again) {
+#pragma unroll 1
+                            for (int x = 0; x < 2; ++x) {
+                                uint32_t z[32];
+                                load(z, col + x * 32);
+                                to_z<kNorm>(z, knorm + x * 128, row.a);
+                                if (masked) mask(z, last - x * 32, kMasked);
+                                const float top = max_of(z, -INFINITY);
+                                m_run = fmaxf(m_run, top);
+                                float2 prod = make_float2(1.f, 1.f);
+                                if (__any_sync(0xffffffffu, top < 0.f)) {
+                                    softplus_sum<true>(z, acc, prod);
+                                } else {
+                                    softplus_sum<false>(z, acc, prod);
+                                    sum_run += ptx::lg2(prod.x * prod.y);
+                                }
+                            }
+                        }
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(s_free + 8 * buf);           // the next product may write here
+                        continue;
+                    }
+                    if constexpr (MODE == kSigmoidRw) {
+                        const float2 one = make_float2(1.f, 1.f);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t z[32];
+                            load(z, col + x * 32);
+                            to_z<kNorm>(z, knorm + x * 128, row.a);
+                            if (masked) mask(z, last - x * 32, kMasked);
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                const float2 y = pair_at(z, j);
+                                m_run = min3(m_run, y.x, y.y);
+                                const float2 e = __fadd2_rn(make_float2(ptx::ex2(y.x), ptx::ex2(y.y)), one);
+                                acc = __fadd2_rn(acc, make_float2(ptx::rcp(e.x), ptx::rcp(e.y)));
+                            }
+                        }
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(s_free + 8 * buf);
+                        continue;
+                    }
                     uint32_t r0[32], r1[32];
                     ptx::tmem_ld32(col, r0);
                     ptx::tmem_ld32(col + 32, r1);
@@ -1141,32 +1205,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                         mask(r0, last, kMasked);
                         mask(r1, last - 32, kMasked);
                     }
-                    if constexpr (MODE == kSoftmaxRw) {
-                        tc::softmax_tile_stats(r0, r1, m_run, sum_run);
-                    } else if constexpr (MODE == kSigmoidRw) {
-                        const float2 one = make_float2(1.f, 1.f);
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const float2 x = pair_at(r0, j), y = pair_at(r1, j);
-                            m_run = min3(min3(m_run, x.x, x.y), y.x, y.y);
-                            const float2 vx = __fadd2_rn(make_float2(ptx::ex2(x.x), ptx::ex2(x.y)), one);
-                            const float2 vy = __fadd2_rn(make_float2(ptx::ex2(y.x), ptx::ex2(y.y)), one);
-                            acc = __fadd2_rn(acc, make_float2(ptx::rcp(vx.x), ptx::rcp(vx.y)));
-                            acc = __fadd2_rn(acc, make_float2(ptx::rcp(vy.x), ptx::rcp(vy.y)));
-                        }
-                    } else {
-                        const float top = max_of(r1, max_of(r0, -INFINITY));
-                        m_run = fmaxf(m_run, top);
-                        float2 prod[2] = {make_float2(1.f, 1.f), make_float2(1.f, 1.f)};
-                        if (__any_sync(0xffffffffu, top < 0.f)) {
-                            softplus_sum<true>(r0, acc, prod[0]);
-                            softplus_sum<true>(r1, acc, prod[1]);
-                        } else {
-                            softplus_sum<false>(r0, acc, prod[0]);
-                            softplus_sum<false>(r1, acc, prod[1]);
-                            sum_run += ptx::lg2((prod[0].x * prod[0].y) * (prod[1].x * prod[1].y));
-                        }
-                    }
+                    if constexpr (MODE == kSoftmaxRw) tc::softmax_tile_stats(r0, r1, m_run, sum_run);
                     continue;
                 }
                 bool raise = false;
