@@ -349,7 +349,15 @@ int lssar_paged_evict(const lssar_paged_cache_t *cache, const float *scores, con
  * A value that is infinite or NaN among the cached tokens reaches the rows of
  * the chunk that attend to it, and may reach rows up to 383 slots before it.
  * The sums have a fixed order: the same call on the same device gives the same
- * bits.  Errors as lssar_paged_decode.
+ * bits.  Three launches (softmax, LSSA) or four (re-weighting modes).  K and V are
+ * read once for each block of T = floor(256 Hkv / H) tokens, K twice in the
+ * re-weighting modes and once more for its norms where the mode has them.  Scratch
+ * from the library's pool, by what the table and n have room for: 16 bytes for each
+ * of B ceil(n / T) blocks; 4 bytes for each key head and slot (modes with norms); 8
+ * bytes for each of min(n, T) H / Hkv rows of B Hkv ceil(n / T) + SMs items
+ * (re-weighting modes); 8 (d + 1) bytes for each of SMs * min(n, T) H / Hkv rows.
+ * Errors as lssar_paged_decode; SHAPE also where
+ * B Hkv ceil(n / T) (ceil(capacity / 64) + 7) passes 2^31 - 2^16.
  */
 int lssar_paged_attend(const lssar_paged_cache_t *cache, const void *q, const long long *q_strides, void *out, int H,
                        int n, const int *counts, int p, int mode, cudaStream_t stream);
@@ -566,9 +574,10 @@ const char *lssar_status_string(int status);
 
 /*
  * Reads and clears the device error word of the current device: 0 when no
- * kernel of this library has hit a bounded wait or a bad length (51) or page
- * number (52) of a paged cache since the last call, else the code (of a wait:
- * its 1-based pipeline stage) of the first.  Synchronises
+ * kernel of this library has hit a bounded wait or a bad length, count (51) or
+ * page number (52) of a paged cache since the last call, else the code (of a
+ * wait: its pipeline stage, from 1 in the forward, 21 in the backward, 41 in the
+ * decode step, 53 in the paged one, 61 in the paged chunk) of the first.  Synchronises
  * the current device.  Returns LSSAR_OK or LSSAR_ERR_CUDA.
  */
 int lssar_device_error_word(unsigned int *word);

@@ -9,26 +9,33 @@
 // Scores are products of the inputs' own bits, scaled in fp32 afterwards: 1/|k| of each cached
 // key comes from a prologue that reads them once, |q| from the gathered rows.
 //
-// What bounds it: the score warps.  Each score costs about 10 issue slots in the
-// re-weighting modes (two passes), against 4d flops of tensor work and, at 256 rows per
-// key, 4d / 256 bytes.
+// What bounds it: the score warps.  A score costs 5 instructions in the statistics pass (one of them a
+// special function), 7 in the values pass at p = 15, and as much again in waits, barriers and loads of
+// whole tiles; against that stand 4 d flops of tensor work and, at 256 rows per key, 4 d / 256 bytes.
+// Measured (kernels alone): 2K rows on 14K tokens, 12 heads of 64, LSSAR p = 15: 103 + 181 us (issue slots
+// 66 and 61 % busy, tensor pipe 20 and 23 %); 512 rows on 128K, 16/2 heads of 128: 270 + 500 us (69 and 57 %,
+// tensor 43 and 46 %); four prompts of 4K, 16 heads of 128, LSSA: 350 us (48 %, tensor 38 %).
 //
 // Split.  A work item is a pair of 128-row tiles of the rows (token, head of the group) of one
-// key head: floor(256 / G) tokens.  Its K tiles of 128 keys are numbered through (sequence, pair,
-// key head, tile); each CTA takes an equal run of them wherever items begin or end, as in
-// the decode step, so that chunks and contexts of any mix load the SMs evenly.  The part of an
-// item in one run is a segment.  The numbering needs the lengths, which are on the device:
+// key head: floor(256 / G) tokens.  What an item costs, its K tiles of 128 keys and a share for its own beginning
+// and end, is numbered through in units (sequence, pair, key head, tile); each CTA takes an equal run of them
+// wherever items begin or end, as in the decode step, so that chunks and contexts of any mix load the SMs evenly.
+// The part of an item in one run is a segment.  The numbering needs the lengths, which are on the device:
 //   attend_prepare   plans it (one block), while the other blocks work out the norms;
 //   attend<kStats>   re-weighting modes: scores -> (m, S1) of each segment's rows;
 //   attend<kValues>  row constants from all of the item's segments, scores again,
 //                    weights, sum of w v; writes the rows of whole items;
 //   attend_join      adds the segments of the items that lie in several runs.
-// Each is a programmatic dependent of the one before it.
+// Each is a programmatic dependent of the one before it.  Small calls are their latencies: 64 rows on 200 tokens
+// take 28 us of device time (shortest runs of 5, 9, 12 or 16 units in place of 2: 30, 29, 41, 43).
 //
 // Structure of attend (640 threads): warp 0 the TMA producer of K (a piece of a page at a time) and of
-// key norms, warp 3 that of V; warps 1, 2 issue the tcgen05.mma of one tile each; four warpgroups of score
+// key norms, warp 3 that of V (one producer for both: 397 us in place of 393 on the prompts, and 29.5 in place of
+// 26.8 on pages of 24 rows); warps 1, 2 issue the tcgen05.mma of one tile each; four warpgroups of score
 // warps, two per tile, each half of its columns: thread = row (TMEM lane).  They also gather the rows of q
-// (any strides, any group) of the next segment during the last step of this one.  Warps whose 32 rows hold none of the item's skip the arithmetic.
+// (any strides, any group) of the next segment during the last step of this one.  Warps whose 32 rows hold none of
+// the item's skip the arithmetic.  An item of one tile of rows has them in both row slots, which take turns with its
+// tiles of keys and add up at the end (16 ragged sequences, 32/8 heads of 128: 77 -> 69 us).
 // TMEM (512 columns): kStats: S of tile w, two buffers each, at 256 w + 128 buffer.  kValues: S_w at
 // 128 w; d = 64: P_w at 256 + 64 w, O_w at 384 + 64 w; d = 128: P_w over S_w, O_w at 256 + 128 w.
 #pragma once
@@ -55,14 +62,18 @@ constexpr int kScoreWarp0 = 4;
 // (128 x 64 + 512 x 104 = 640 x 96).
 constexpr int kLaunchRegs = 96, kCtrlRegs = 64, kScoreRegs = 104;
 static_assert(128 * kCtrlRegs + 512 * kScoreRegs <= kThreads * kLaunchRegs, "register split");
-// Tiles whose key norms are in shared memory.  They come with the tile's keys, and their slot is used again 16
-// tiles later: the stage of tile j's keys was given up by both MMA warps after they issued the scores of a
-// tile j - 8 or later, for which the score warps had read the scores of the tile two before, and the norms of
-// the one before that (kStats, d = 64; the others leave fewer tiles between).
+// Tiles whose key norms are in shared memory.  They come with the tile's keys, and the place of tile j's is used
+// again for tile j + 16, which waits until both MMA warps have passed tile j + 8 (kStats, d = 64; the others have
+// fewer stages).  A row slot that still reads the norms of j is in j's item, so that the queue of kItems holds the
+// eight tiles after j in that item and three more at most; of n tiles of one of them the slot takes n or n / 2
+// (rounded down), two or more of the eight in all; and the second product of scores after j's waits
+// for s_free of j's, which follows the reading of its norms.
 constexpr int kInfo = 16;
 constexpr int kItems = 4;                     // depth of the queue of segments
 // What a work item costs, in the units that its run is counted in: of each tile of keys, and beside them (these
-// are numbered before its first tile).  An item of one tile of rows takes a tile of keys in half the time.
+// are numbered before its first tile).  An item of one tile of rows takes a tile of keys in half the time.  (Items
+// of both kinds at 6, units: ragged 68.5 us, pages of 24 18.8 us; 4: 67.4, 21.2; 8: 71.8, 19.9; none at all: prompts
+// 393 us in place of 360.)
 __host__ __device__ constexpr int tile_cost(int rows) { return rows > 128 ? 2 : 1; }
 constexpr int kItemCost = 6;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
