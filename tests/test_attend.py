@@ -613,3 +613,49 @@ def test_debug_build_of_a_serving_step(torch_mod, monkeypatch):
     for a, b in zip(*results):
         view = torch.int16 if a.element_size() == 2 else torch.int32
         assert torch.equal(a.view(view), b.view(view))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode,p", MODES)
+def test_nothing_to_attend_and_whole_sequences(torch_mod, mode, p):
+    # no rows anywhere: out stays; the lengths themselves as counts: every row of every sequence
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    c = Cache(torch, [0, 5, 131, 0], 2, 64, 16, seed=9)
+    q = chunk_q(c, 4, 131)
+    out = torch.full((4, 4, 131, 64), 7.0, dtype=c.dt).cuda()
+    for lens in (c.lens, c.lens * 0):
+        api.lssar_paged_attend(q, c.k, c.v, c.table, lens, counts=ints(torch, 0, 0, 0, 0), p=p, mode=mode, out=out)
+        assert api.device_error_word() == 0 and (out == 7.0).all()
+    api.lssar_paged_attend(q, *c.args(), counts=c.lens, p=p, mode=mode, out=out)
+    assert api.device_error_word() == 0
+    check_attend(torch, c, q, c.lens.tolist(), mode, p, [[], range(5), [0, 1, 2, 3, 64, 126, 127, 128, 130], []], got=out)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 1), (64, 4)])
+@pytest.mark.parametrize("mode,p", MODES)
+def test_non_finite_inputs_stay_with_their_rows(torch_mod, mode, p, d, G):
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    lens, n, s = [700, 300], 600, 400
+    rows = [[0, 150, 298, 299], [5, 130, 299]]                # of the first: those before slot s (t attends to 101 + t)
+    for value in (float("nan"), float("inf"), -float("inf")):
+        # a key: the rows that attend to it and no others
+        c = Cache(torch, lens, 1, d, 16, seed=d)
+        q, counts = chunk_q(c, G, n), [n, 300]
+        c.k[c.table[0, s // 16].long(), 0, s % 16] = value
+        out = check_attend(torch, c, q, counts, mode, p, rows)
+        first = s - (lens[0] - n)
+        assert not out[0, :, first:].isfinite().any() and out[0, :, :first].isfinite().all() and out[1, :, :300].isfinite().all()
+        # a query: its row
+        c = Cache(torch, lens, 1, d, 16, seed=d)
+        q[0, 0, 77] = value
+        out = check_attend(torch, c, q, counts, mode, p, rows)
+        bad = ~out[:, :, :n].isfinite().all(-1)
+        assert bad[0, 0, 77] and bad.sum() == 1
+        # a value: no row that lies more than 383 slots before it, no other sequence
+        q[0, 0, 77] = 1.0
+        c.v[c.table[0, 699 // 16].long(), 0, 699 % 16] = value
+        out = check_attend(torch, c, q, counts, mode, p, [[0, 100, 215], [5, 130, 299]])
+        assert out[0, :, :216].isfinite().all() and out[1, :, :300].isfinite().all() and not out[0, :, 599].isfinite().any()
