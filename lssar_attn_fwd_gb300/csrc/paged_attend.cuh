@@ -83,11 +83,12 @@ enum : unsigned { kErrItem = 61, kErrQ, kErrKvFull, kErrKvEmpty, kErrSFull, kErr
                   kErrHalves, kErrTileMax, kErrDrain, kErrJoint };
 
 // One-pass modes: log2 of the largest weight of a row lies in kRoom + [0, kLag] (fp16, whose
-// least step is 2^-24, needs the room; softplus up to 117 leaves less of it).
+// least step is 2^-24, needs the room; softplus up to 117 leaves less of it; softmax's raises, with 13 and a
+// lag of 2, took 140 us instead of 132 on 512 rows on 32K, d = 128).
 template <int MODE, bool HALF>
 struct Range16 {
-    static constexpr float kRoom = !HALF ? 0.f : MODE == kSoftmax ? 13.f : 8.f;
-    static constexpr float kLag = !HALF ? 8.f : MODE == kSoftmax ? 2.f : 6.f;
+    static constexpr float kRoom = !HALF ? 0.f : MODE == kSoftmax ? 12.f : 8.f;
+    static constexpr float kLag = !HALF ? 8.f : MODE == kSoftmax ? 3.875f : 6.f;
 };
 constexpr float kTopFp16 = 32768.f;           // re-weighting: the largest weight in fp16
 constexpr float kNoLift = -118.f;             // LSSA: below every score
@@ -137,12 +138,12 @@ struct __align__(16) Shared {
     float knorm[kInfo][kKeys];
     float m[2][2][2][kTileRows], s[2][2][2][kTileRows];   // [meeting parity][tile][half][row]
     float qq[2][2][2][kTileRows];                         // sum of squares of the next row of q, likewise
-    float tmax[2][2][2][kTileRows];                       // [step parity][tile][half][row]
+    float tmax[2][2][2][kTileRows];                       // [step parity, or kTurns: 1 for references][tile][half][row]
     float other[2][kTileRows][2];                         // [join parity][row]: the second slot's sums
     uint64_t q_full[2];
     uint64_t s_full[2][2], s_free[2][2];                  // [tile][buffer], or (kSplit) [tile][half]
     uint64_t p_full[2], p_free[2], o_full[2], o_free[2], halves[2], joint;
-    uint64_t tile_max[2][4];
+    uint64_t tile_max[2][4], turn[2][2][4];               // [half][tile][quarter]
     uint64_t kv_full[8], kv_empty[8];
     uint64_t item_full[kItems], item_empty[kItems];
     Item items[kItems];
@@ -627,8 +628,14 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
     constexpr int kSBufs = PHASE == kStats ? 2 : 1;
     // kValues, d = 128: P lies over S, so that a product of scores waits for the weights of the one before.
     // The two halves of a tile's keys are then products of their own, and their warpgroups take turns (512 rows
-    // on 128K, LSSAR: 737 -> 572 us).  Not in softmax, whose warpgroups exchange each tile's maxima (77 -> 84 us).
-    constexpr bool kSplit = PHASE == kValues && !kSepP && MODE != kSoftmax;
+    // on 128K, LSSAR: 737 -> 572 us).
+    // Softmax: a half takes the reference of the turn before its own, which is the other half's, and raises it where
+    // its own maximum asks for that: O is rescaled, all of its columns, between the two turns' products.  Only the first
+    // tile's maxima meet (512 rows on 32K, 16/2 heads: 159 -> 134 us in bf16, 156 -> 132 in fp16; four prompts of 4K,
+    // 16 heads: 345 -> 308; 16 ragged sequences, segments of 7 tiles: 71.7 -> 74.6; with the maxima of every tile
+    // meeting, as products of their own, 84 in place of 77).
+    constexpr bool kSplit = PHASE == kValues && !kSepP;
+    constexpr bool kTurns = kSplit && MODE == kSoftmax;
     constexpr int kPCol = 256, kOCol = kSepP ? 384 : 256;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -653,7 +660,10 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             init(&sh->o_full[i], 1);
             init(&sh->o_free[i], 256);
             init(&sh->halves[i], 256);
-            for (int j = 0; j < 4; ++j) init(&sh->tile_max[i][j], 64);
+            for (int j = 0; j < 4; ++j) {
+                init(&sh->tile_max[i][j], 64);
+                for (int h = 0; h < 2; ++h) init(&sh->turn[h][i][j], 32);
+            }
         }
         init(&sh->joint, PHASE == kStats ? 256 : 512);
         for (int i = 0; i < 8; ++i) {
@@ -951,6 +961,8 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                                 if (h == 0 && !(ok = o_is_free())) break;
                                 ptx::tc_fence_after();
                                 issue_pv(vslot, 64 * h, 4, kt > begin || h > 0);
+                                // (no scores follow the last tile's first half: a warp that raises its rows' reference waits for this)
+                                if (kTurns && h == 0 && !next) commit(LSSAR_AT(p_free) + 8 * w);
                                 // (before the commits that nothing waits for: each takes some 300 cycles)
                                 if (next) issue_half(kslot, h);
                             }
@@ -1004,7 +1016,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
         constexpr uint32_t kParity = 4 * kTileRows * 4;
         constexpr float kMasked = MODE == kSigmoidRw ? INFINITY : -INFINITY;
         Ring<kSBufs> sb;
-        uint32_t pv = 0, exchanges = 0, joints = 0;
+        uint32_t pv = 0, exchanges = 0, turns = 0, joints = 0;
         uint32_t own_segs = 0, other_segs = 0;                   // segments with this slot, with the other
         uint32_t tiles = 0;            // tiles of keys that the CTA has taken
         const int run = g.s.head->run;
@@ -1041,6 +1053,11 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
         auto meet = [&] {
             ptx::mbar_arrive(LSSAR_AT(halves) + 8 * w);
             return wait_all(LSSAR_AT(halves) + 8 * w, meets++ & 1, kErrHalves);
+        };
+        // softmax: the exponents' offset for a reference (scores so large that their steps pass the room: without it)
+        auto offset_of = [](float ref) {
+            const float x = ref - Range16<MODE, HALF>::kRoom;
+            return ref - x <= Range16<MODE, HALF>::kRoom ? x : ref;
         };
         bool some = false;
         ok = gather(0, some);
@@ -1231,19 +1248,26 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                             top = max_of(z, top);
                         }
                         if constexpr (MODE == kSoftmax) top = __fmul_rn(top, row.a);      // (rounded as the scores are, in no FMA)
-                        const uint32_t at = LSSAR_AT(tmax) + (exchanges & 1) * kParity;
-                        ptx::st_shared_f32(at + mine, top);
-                        ptx::mbar_arrive(LSSAR_AT(tile_max) + 32 * w + 8 * quarter);
-                        if (!(ok = wait_all(LSSAR_AT(tile_max) + 32 * w + 8 * quarter, exchanges & 1, kErrTileMax))) break;
-                        top = fmaxf(top, ptx::ld_shared_f32(at + others));
-                        ++exchanges;
+                        if (kTurns && kt > begin) {
+                            if (!(ok = wait_all(LSSAR_AT(turn) + 64 * (half ^ 1) + 32 * w + 8 * quarter, (turns - (half ^ 1)) & 1, kErrTileMax))) break;
+                            const float ref = ptx::ld_shared_f32(LSSAR_AT(tmax) + kParity + others), x = offset_of(ref);
+                            const float f = ptx::ex2(row.x - x);
+                            acc = __fmul2_rn(acc, make_float2(f, f));
+                            row.x = x;
+                            row.ref = ref;
+                        } else {
+                            const uint32_t at = LSSAR_AT(tmax) + (kTurns ? 0u : (exchanges & 1) * kParity);     // (kTurns: references in the other)
+                            ptx::st_shared_f32(at + mine, top);
+                            ptx::mbar_arrive(LSSAR_AT(tile_max) + 32 * w + 8 * quarter);
+                            if (!(ok = wait_all(LSSAR_AT(tile_max) + 32 * w + 8 * quarter, exchanges & 1, kErrTileMax))) break;
+                            top = fmaxf(top, ptx::ld_shared_f32(at + others));
+                            ++exchanges;
+                        }
                         if constexpr (MODE == kLssa) top = fminf(top, 0.f);
                         raise = top - row.ref > Range16<MODE, HALF>::kLag || (MODE == kLssa && top >= 0.f && row.ref < 0.f);
                         if (raise) {
                             if constexpr (MODE == kSoftmax) {
-                                // (scores so large that their steps pass the room: without it)
-                                float x = top - Range16<MODE, HALF>::kRoom;
-                                if (!(top - x <= Range16<MODE, HALF>::kRoom)) x = top;
+                                const float x = offset_of(top);
                                 alpha = ptx::ex2(row.x - x);
                                 row.x = x;
                             } else {
@@ -1252,6 +1276,11 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                             }
                             row.ref = top;
                             acc = __fmul2_rn(acc, make_float2(alpha, alpha));
+                        }
+                        if constexpr (kTurns) {
+                            ptx::st_shared_f32(LSSAR_AT(tmax) + kParity + mine, row.ref);
+                            ptx::mbar_arrive(LSSAR_AT(turn) + 64 * half + 32 * w + 8 * quarter);
+                            ++turns;
                         }
                         if constexpr (MODE == kLssa) form = __all_sync(0xffffffffu, row.ref >= 0.f) ? kMixed : kAccurate;
                         if constexpr (MODE == kSoftmax) form = __any_sync(0xffffffffu, fabsf(row.ref) > 65536.f) ? kAccurate : kMixed;
@@ -1306,21 +1335,29 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 if (!ok) break;
                 if constexpr (kOnePass) {
                     if (kt > begin && __any_sync(0xffffffffu, raise)) {
+                        if constexpr (kTurns) {
+                            // the product of the turn before is done: the other half's next scores follow it
+                            const bool next = kt + step < kt1;
+                            const uint32_t bar = half == 0 || next ? LSSAR_AT(s_full) + 16 * w + 8 * (half ^ 1) : LSSAR_AT(p_free) + 8 * w;
+                            if (!(ok = wait_all(bar, (half == 0 ? sb.i - 1 : next ? sb.i : own_segs) & 1, kErrSFull))) break;
+                            ptx::tc_fence_after();
+                        }
+                        const uint32_t first = kTurns ? tmem + lane_addr + kOCol + w * D : o_col;
 #pragma unroll 1
-                        for (int x = 0; x < D / 2; x += 16) {
+                        for (int x = 0; x < (kTurns ? D : D / 2); x += 16) {
                             uint32_t o[16];
-                            ptx::tmem_ld16(o_col + x, o);
+                            ptx::tmem_ld16(first + x, o);
                             ptx::tmem_ld_wait();
                             ptx::reg_fence(o);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                            ptx::tmem_st16(o_col + x, o);
+                            ptx::tmem_st16(first + x, o);
                         }
                     }
                 }
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
-                if constexpr (kSplit && kOnePass) {
+                if constexpr (kSplit && MODE == kLssa) {
                     // (the first half's product must not start while the other half's columns of O are rescaled)
                     if (kt > begin && __any_sync(0xffffffffu, raise)) {
                         ptx::mbar_arrive(LSSAR_AT(tile_max) + 32 * w + 8 * quarter);
@@ -1335,12 +1372,13 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             hand_over(some);
             // the two halves of a row meet
             const uint32_t par = meets & 1;
-            const float part = (acc.x + acc.y) + sum_run;
+            float part = (acc.x + acc.y) + sum_run;
             ptx::st_shared_f32(LSSAR_AT(s) + par * kParity + mine, part);
             const float m_part = MODE == kSigmoidRw ? -m_run : fmaxf(m_run, kLowest);
             if constexpr (PHASE == kStats) ptx::st_shared_f32(LSSAR_AT(m) + par * kParity + mine, m_part);
+            if constexpr (kTurns) ptx::st_shared_f32(LSSAR_AT(m) + par * kParity + mine, row.x);
             if (!(ok = meet())) break;
-            const float other = ptx::ld_shared_f32(LSSAR_AT(s) + par * kParity + others);
+            float other = ptx::ld_shared_f32(LSSAR_AT(s) + par * kParity + others);
             const bool valid = row0 + in < rows;
             // Two slots with the same rows: the first adds the second's part to its own.
             const bool both = step == 2 && kt0 + 1 < kt1, second = both && w == 1;
@@ -1373,6 +1411,16 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 }
                 release_item();
                 continue;
+            }
+            if constexpr (kTurns) {
+                // the last turn's reference, half 1's, holds for both
+                const float x = ptx::ld_shared_f32(LSSAR_AT(m) + par * kParity + others);
+                if (half == 0) {
+                    part *= ptx::ex2(row.x - x);
+                    row.x = x;
+                } else {
+                    other *= ptx::ex2(x - row.x);
+                }
             }
             // (half 0's part first in both, so that both see the same sum)
             float sum = half == 0 ? part + other : other + part;
