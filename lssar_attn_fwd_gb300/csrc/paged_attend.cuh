@@ -147,7 +147,7 @@ struct __align__(16) Shared {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t item_full[kItems], item_empty[kItems];
     Item items[kItems];
-    unsigned absent[8];   // per stage of V: groups of 8 rows that no copy has filled
+    unsigned absent[8];   // per stage: groups of 8 rows that no copy has filled (keys: of pages that are none)
     uint32_t tmem;
     int abort_flag;
 };
@@ -741,9 +741,10 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     const unsigned there = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -2);
                     if (lane == 0) {
                         const int groups = piece_rows / 8;
-                        unsigned absent = 0xffffu;
+                        const unsigned pieces = keys ? bad : ~there;
+                        unsigned absent = 0;
                         for (int i = 0; i * piece_rows < kKeys; ++i)
-                            if (there >> i & 1) absent &= ~(((1u << groups) - 1) << (i * groups));
+                            if (pieces >> i & 1) absent |= ((1u << groups) - 1) << (i * groups);
                         sh->absent[s] = absent;
                         if (keys && bad) {                        // the first slot of a page that is none
                             volatile int *first = &sh->items[slot].first_bad;
@@ -866,20 +867,6 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 ++sb.i;
                 return true;
             };
-            // Rows of a V tile that hold nothing of the sequence (past its end, pages that are none): zeros,
-            // as their weight is 0 and what lies there may be infinite.
-            auto clear_rows = [&](uint32_t vslot, int left) {
-                const unsigned absent = *(volatile unsigned *)&sh->absent[vslot];
-                if (left >= kKeys && absent == 0) return;
-                for (int r = lane; r < kKeys; r += 32)
-                    if (r >= left || (absent >> (r >> 3) & 1)) {
-#pragma unroll
-                        for (int x = 0; x < D / 8; ++x)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + vslot * TB + (r >> 3) * kGroup + (x >> 3) * 1024 + (r & 7) * 128 + (x & 7) * 16), "r"(0) : "memory");
-                    }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-            };
             // keys [from, from + 16 n) of the tile
             auto issue_pv = [&](uint32_t vslot, int from, int n, bool accumulate) {
                 const uint64_t dv = dv0 + (uint64_t)((vslot * TB + from / 8 * kGroup) >> 4);
@@ -905,10 +892,28 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 }
                 __syncwarp();
             };
+            // Rows of a tile that hold nothing of the sequence: zeros.  Values: past its end and of pages that are none, as
+            // their weight is 0 and what lies there may be infinite.  Keys: of pages that are none, as rows that
+            // do attend to them have a say in the form of their warp's weights.
+            auto clear_rows = [&](uint32_t vslot, int left) {
+                const unsigned absent = *(volatile unsigned *)&sh->absent[vslot];
+                if (left >= kKeys && absent == 0) return;
+                for (int r = lane; r < kKeys; r += 32)
+                    if (r >= left || (absent >> (r >> 3) & 1)) {
+#pragma unroll
+                        for (int x = 0; x < D / 8; ++x)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + vslot * TB + (r >> 3) * kGroup + (x >> 3) * 1024 + (r & 7) * 128 + (x & 7) * 16), "r"(0) : "memory");
+                    }
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+            };
             // the stage of tile kt, past those before it, which are the other slot's
             auto take = [&](Ring<NR> &tiles, uint32_t first, int &pos, int kt, uint32_t &stage) -> bool {
                 while (acquire(tiles, first, stage)) {
-                    if (pos++ == kt) return true;
+                    if (pos++ == kt) {
+                        if (first == 0) clear_rows(stage, kKeys);
+                        return true;
+                    }
                     if (lane == 0) ptx::mbar_arrive(LSSAR_AT(kv_empty) + 8 * stage);
                 }
                 return false;

@@ -532,27 +532,32 @@ def test_chunks_of_one_tile_of_rows_beside_larger_ones(torch_mod, d, half):
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 def test_bad_pages_under_one_tile_of_rows(torch_mod, d):
-    # 40 rows on 1 to 4 tiles, whose slots take turns: NaN where a row attends to the page, the same bits elsewhere
+    # 40 rows on 1 to 4 tiles, whose slots take turns: NaN where a row attends to the page, the oracle's values elsewhere;
+    # the same bits whatever ran between, since nothing of what the tile held before is read
     torch = torch_mod
     from lssar_attn_fwd_gb300 import api
-    c = Cache(torch, [60, 200, 330, 500], 2, d, 16, seed=6)
-    q = chunk_q(c, 2, 40)
-    for mode in (MODE_LSSAR, MODE_SOFTMAX, MODE_LSSA, MODE_SIGMOID_RW):
-        good = api.lssar_paged_attend(q, *c.args(), mode=mode)
-        assert api.device_error_word() == 0 and good.isfinite().all()
+    c, other = Cache(torch, [60, 200, 330, 500], 2, d, 16, seed=6), Cache(torch, [900], 2, d, 16, seed=7)
+    other.k *= 100
+    q, q_other = chunk_q(c, 2, 40), chunk_q(other, 2, 300)
+    for mode, p in ((MODE_LSSAR, 3), (MODE_SOFTMAX, 1), (MODE_LSSA, 1), (MODE_SIGMOID_RW, 3), (MODE_SOFTMAX_RW, 3)):
+        good = check_attend(torch, c, q, None, mode, p)
         for b, n in enumerate(c.lens.tolist()):
-            for column in sorted({0, 9, 17, 26, (n - 20) // 16}):
+            for column in sorted({0, 9, 17, 19, 26, (n - 20) // 16}):
                 if 16 * column >= n:
                     continue
                 table = c.table.clone()
                 table[b, column] = -1
-                out = api.lssar_paged_attend(q, c.k, c.v, table, c.lens, mode=mode)
-                assert api.device_error_word() == PAGE
+                outs = []
+                for _ in range(3):
+                    outs.append(api.lssar_paged_attend(q, c.k, c.v, table, c.lens, p=p, mode=mode))
+                    assert api.device_error_word() == PAGE
+                    api.lssar_paged_attend(q_other, *other.args(), p=p, mode=mode)
                 first = max(0, 16 * column - (n - 40))           # row t attends to slots up to n - 40 + t
-                want = good.clone()
-                want[b, :, first:] = float("nan")
-                assert torch.equal(out.isnan(), want.isnan()), (mode, b, column)
-                assert torch.equal(out.nan_to_num(), want.nan_to_num()), (mode, b, column)
+                want = torch.zeros_like(good, dtype=torch.bool)
+                want[b, :, first:] = True
+                assert torch.equal(outs[0].isnan(), want), (mode, b, column)
+                assert all(torch.equal(x.nan_to_num(), outs[0].nan_to_num()) for x in outs[1:]), (mode, b, column)
+                check_attend(torch, c, q, None, mode, p, [range(first) if x == b else [0, 39] for x in range(4)], got=outs[0])
 
 
 @pytest.mark.gpu
