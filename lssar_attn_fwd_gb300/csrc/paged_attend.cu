@@ -22,7 +22,7 @@ Layout layout(const PagedAttend &pr, int sms) {
     auto r = [](size_t x) { return (x + 255) & ~(size_t)255; };
     l.entries = 256;
     l.first = l.entries + r(pairs * sizeof(int4));
-    l.knorm = l.first + r((size_t)l.ctas * 4);
+    l.knorm = l.first + r((size_t)l.ctas * 2 * sizeof(int4));
     l.stats = l.knorm + (norms ? r((size_t)c.B * c.Hkv * l.cap128 * 4) : 0);
     l.sums = l.stats + (reweight ? r((items + l.ctas) * l.rows * 8) : 0);
     l.o = l.sums + r((size_t)2 * l.ctas * l.rows * 8);
@@ -50,7 +50,7 @@ cudaError_t launch_paged_attend(const PagedAttend &pr, void *ws, int sms, cudaSt
     char *base = static_cast<char *>(ws);
     g.s.head = reinterpret_cast<attend::Header *>(base);
     g.s.entries = reinterpret_cast<int4 *>(base + l.entries);
-    g.s.first = reinterpret_cast<int *>(base + l.first);
+    g.s.first = reinterpret_cast<int4 *>(base + l.first);
     g.s.knorm = reinterpret_cast<float *>(base + l.knorm);
     g.s.stats = reinterpret_cast<float2 *>(base + l.stats);
     g.s.sums = reinterpret_cast<float2 *>(base + l.sums);

@@ -27,7 +27,8 @@
 //                    weights, sum of w v; writes the rows of whole items;
 //   attend_join      adds the segments of the items that lie in several runs.
 // Each is a programmatic dependent of the one before it.  Small calls are their latencies: 64 rows on 200 tokens
-// take 28 us of device time (shortest runs of 5, 9, 12 or 16 units in place of 2: 30, 29, 41, 43).
+// take 27.5 us of device time (shortest runs of 5, 9, 12 or 16 units in place of 2: 30, 29, 41, 43; 28 where a CTA
+// finds its first entry, and that entry's lengths, by further reads).
 //
 // Structure of attend (640 threads): warp 0 the TMA producer of K (a piece of a page at a time) and of
 // key norms, warp 3 that of V (one producer for both: 397 us in place of 393 on the prompts, and 29.5 in place of
@@ -100,7 +101,7 @@ struct Header {
 struct Scratch {
     Header *head;
     int4 *entries;        // {sequence, pair, cost of an item, number of the first item's first unit}
-    int *first;           // [ctas] entry of each CTA's first unit
+    int4 *first;          // [ctas][2]: the entry of each CTA's first unit; its number, new tokens, cached tokens
     float *knorm;         // [B, Hkv, cap128] 1 / |k|
     float2 *stats;        // [item + cta][rows]: m, S1 of a segment's rows
     float2 *sums;         // [2 cta + last][rows]: reference, sum of w
@@ -285,7 +286,9 @@ static __device__ __noinline__ void make_plan(const Args &g) {
             if (g.s.entries[mid].w <= t) lo = mid;
             else hi = mid - 1;
         }
-        g.s.first[cta] = lo;
+        const int4 en = g.s.entries[lo];
+        g.s.first[2 * cta] = en;
+        g.s.first[2 * cta + 1] = make_int4(lo, a.counts ? a.counts[en.x] : a.n, c.lens[en.x], 0);
     }
 }
 
@@ -460,7 +463,8 @@ enum Form : int {
 };
 
 // Of every 16 pairs, those whose softplus takes the polynomial: the rest of the work leaves the FMA pipe
-// more room in LSSA.
+// more room in LSSA.  (2K on 14K, 12 heads of 64, LSSA: 2 183 us, 5 173, 6 172, 8 167, 11 182; LSSAR p = 3: 2 and 4 194, 5
+// to 11 201 to 204.)
 template <int MODE>
 constexpr int kPolyPairs = MODE == kLssa ? 8 : 4;
 
@@ -764,13 +768,11 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
             };
             if (keys) {
                 const Header head = *g.s.head;
+                int4 en = g.s.first[2 * blockIdx.x], seq = g.s.first[2 * blockIdx.x + 1];      // (of a run without units: unused)
                 const int t1 = min((long long)head.total, (long long)(blockIdx.x + 1) * head.run);
                 long long t = (long long)blockIdx.x * head.run;
-                int e = 0, h = 0, at = 0;       // the item, and the unit of it
-                int4 en = make_int4(0, 0, 0, 0);
+                int e = seq.x, h = 0, at = 0;       // the item, and the unit of it
                 if (t < t1) {
-                    e = g.s.first[blockIdx.x];
-                    en = g.s.entries[e];
                     h = (int)(t - en.w) / en.z;
                     at = (int)(t - en.w) - h * en.z;
                 }
@@ -780,12 +782,12 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     // the tiles of the item whose last unit lies in the run
                     it.kt0 = -1;
                     if (t < t1) {
-                        const int cnt = a.counts ? a.counts[en.x] : a.n;
+                        const int cnt = seq.y;
                         it.b = en.x;
                         it.h = h;
                         it.t0 = en.y * g.tokens;
                         it.rows = rows_of_pair(g, cnt, it.t0);
-                        it.len = c.lens[en.x];
+                        it.len = seq.z;
                         it.base = it.len - cnt;
                         const int cost = kItemCost, each = tile_cost(it.rows), end = (int)min((long long)en.z, at + t1 - t);
                         it.nk = (en.z - cost) / each;
@@ -801,6 +803,8 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                         if (t < t1 && ++h == c.Hkv) {
                             h = 0;
                             en = g.s.entries[++e];
+                            seq.y = a.counts ? a.counts[en.x] : a.n;
+                            seq.z = c.lens[en.x];
                         }
                         if (it.kt0 >= 0 && it.kt0 == it.kt1) continue;      // none (part of the item's cost, of a tile's)
                     }
@@ -1529,10 +1533,10 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join(const __grid_constan
     int4 en = make_int4(0, 0, 1, 0);
     int h = 0, last = 0, rows = 0, t0 = 0;
     if (some) {
-        en = g.s.entries[g.s.first[cta]];
+        en = g.s.first[2 * cta];
         h = (int)(x - en.w) / en.z;
         t0 = en.y * g.tokens;
-        rows = rows_of_pair(g, a.counts ? a.counts[en.x] : a.n, t0);
+        rows = rows_of_pair(g, g.s.first[2 * cta + 1].y, t0);
         // the runs of its first and last tile
         const int each = tile_cost(rows), start = en.w + h * en.z + kItemCost;
         last = (en.w + (h + 1) * en.z - 1) / head.run;
