@@ -14,7 +14,7 @@
 // whole tiles; against that stand 4 d flops of tensor work and, at 256 rows per key, 4 d / 256 bytes.
 // Measured (kernels alone): 2K rows on 14K tokens, 12 heads of 64, LSSAR p = 15: 103 + 181 us (issue slots
 // 66 and 61 % busy, tensor pipe 20 and 23 %); 512 rows on 128K, 16/2 heads of 128: 270 + 500 us (69 and 57 %,
-// tensor 43 and 46 %); four prompts of 4K, 16 heads of 128, LSSA: 350 us (48 %, tensor 38 %).
+// tensor 43 and 46 %); four prompts of 4K, 16 heads of 128, LSSA: 350 us (47 %, tensor 38 %).
 //
 // Split.  A work item is a pair of 128-row tiles of the rows (token, head of the group) of one
 // key head: floor(256 / G) tokens.  What an item costs, its K tiles of 128 keys and a share for its own beginning
