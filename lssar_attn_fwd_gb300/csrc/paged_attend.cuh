@@ -148,7 +148,7 @@ struct __align__(16) Shared {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t item_full[kItems], item_empty[kItems];
     Item items[kItems];
-    unsigned absent[8];   // per stage: groups of 8 rows that no copy has filled (keys: of pages that are none)
+    unsigned absent[8];   // per stage of V: groups of 8 rows that no copy has filled
     uint32_t tmem;
     int abort_flag;
 };
@@ -592,6 +592,14 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// Row r of the tile of keys or values at `tile`: zeros.
+template <int D>
+__device__ __forceinline__ void clear_row(uint32_t tile, int r) {
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (r >> 3) * (16 * D) + (x >> 3) * 1024 + (r & 7) * 128 + (x & 7) * 16), "r"(0) : "memory");
+}
+
 // A ring of `N` barriers: slot and parity of use number `i`.
 template <int N>
 struct Ring {
@@ -743,12 +751,19 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     const uint32_t s = first_stage + kv.slot(), full = LSSAR_AT(kv_full) + 8 * s;
                     if (kv.reused() && !(ok = wait_all(LSSAR_AT(kv_empty) + 8 * s, kv.parity() ^ 1, kErrKvEmpty))) break;
                     const unsigned there = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -2);
+                    if (keys && bad) {
+                        // keys of pages that are none: zeros, as rows that do attend to them have a say in the form of
+                        // their warp's weights
+                        for (int r = lane; r < kKeys; r += 32)
+                            if (bad >> (r / piece_rows) & 1) clear_row<D>(ring + s * TB, r);
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                    }
                     if (lane == 0) {
                         const int groups = piece_rows / 8;
-                        const unsigned pieces = keys ? bad : ~there;
-                        unsigned absent = 0;
+                        unsigned absent = 0xffffu;
                         for (int i = 0; i * piece_rows < kKeys; ++i)
-                            if (pieces >> i & 1) absent |= ((1u << groups) - 1) << (i * groups);
+                            if (there >> i & 1) absent &= ~(((1u << groups) - 1) << (i * groups));
                         sh->absent[s] = absent;
                         if (keys && bad) {                        // the first slot of a page that is none
                             volatile int *first = &sh->items[slot].first_bad;
@@ -896,28 +911,20 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                 }
                 __syncwarp();
             };
-            // Rows of a tile that hold nothing of the sequence: zeros.  Values: past its end and of pages that are none, as
-            // their weight is 0 and what lies there may be infinite.  Keys: of pages that are none, as rows that
-            // do attend to them have a say in the form of their warp's weights.
+            // Rows of a V tile that hold nothing of the sequence (past its end, pages that are none): zeros,
+            // as their weight is 0 and what lies there may be infinite.
             auto clear_rows = [&](uint32_t vslot, int left) {
                 const unsigned absent = *(volatile unsigned *)&sh->absent[vslot];
                 if (left >= kKeys && absent == 0) return;
                 for (int r = lane; r < kKeys; r += 32)
-                    if (r >= left || (absent >> (r >> 3) & 1)) {
-#pragma unroll
-                        for (int x = 0; x < D / 8; ++x)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + vslot * TB + (r >> 3) * kGroup + (x >> 3) * 1024 + (r & 7) * 128 + (x & 7) * 16), "r"(0) : "memory");
-                    }
+                    if (r >= left || (absent >> (r >> 3) & 1)) clear_row<D>(ring + vslot * TB, r);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
             };
             // the stage of tile kt, past those before it, which are the other slot's
             auto take = [&](Ring<NR> &tiles, uint32_t first, int &pos, int kt, uint32_t &stage) -> bool {
                 while (acquire(tiles, first, stage)) {
-                    if (pos++ == kt) {
-                        if (first == 0) clear_rows(stage, kKeys);
-                        return true;
-                    }
+                    if (pos++ == kt) return true;
                     if (lane == 0) ptx::mbar_arrive(LSSAR_AT(kv_empty) + 8 * stage);
                 }
                 return false;
