@@ -1274,8 +1274,12 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                         } else {
                             const uint32_t at = LSSAR_AT(tmax) + (kTurns ? 0u : (exchanges & 1) * kParity);     // (kTurns: references in the other)
                             ptx::st_shared_f32(at + mine, top);
+                            // (LSSA in halves: half 0 learns here that the last tile's second product, which half 1's
+                            // scores followed, has left O)
+                            if constexpr (kSplit) ptx::tc_fence_before();
                             ptx::mbar_arrive(LSSAR_AT(tile_max) + 32 * w + 8 * quarter);
                             if (!(ok = wait_all(LSSAR_AT(tile_max) + 32 * w + 8 * quarter, exchanges & 1, kErrTileMax))) break;
+                            if constexpr (kSplit) ptx::tc_fence_after();
                             top = fmaxf(top, ptx::ld_shared_f32(at + others));
                             ++exchanges;
                         }
@@ -1378,6 +1382,8 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     if (kt > begin && __any_sync(0xffffffffu, raise)) {
                         ptx::mbar_arrive(LSSAR_AT(tile_max) + 32 * w + 8 * quarter);
                         if (!(ok = wait_all(LSSAR_AT(tile_max) + 32 * w + 8 * quarter, exchanges++ & 1, kErrTileMax))) break;
+                        ptx::tc_fence_after();           // (the other half's stores come before this arrival too)
+                        ptx::tc_fence_before();
                     }
                 }
                 ptx::mbar_arrive(p_done);
