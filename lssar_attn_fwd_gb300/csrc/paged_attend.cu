@@ -65,6 +65,7 @@ cudaError_t launch_paged_attend(const PagedAttend &pr, void *ws, int sms, cudaSt
     const int low = c.page_size & -c.page_size;
     g.piece_rows = low < attend::kKeys ? low : attend::kKeys;
     g.scale = !uses_normalised_qk(pr.mode) ? 1.4426950408889634f / sqrtf((float)c.d) : (pr.mode == kSigmoidRw ? -1.f : 1.f) * score_qmul(c.d);
+    g.exact_weights = exact_weights_requested() ? 1 : 0;
     g.power = {pr.p, 0, pr.p};
     for (; g.power.rest % 3 == 0; g.power.rest /= 3) ++g.power.cubes;
     g.idesc_s = ptx::idesc_f16(!c.half, attend::kTileRows, attend::kKeys, false, false);

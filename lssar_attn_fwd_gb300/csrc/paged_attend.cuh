@@ -121,6 +121,7 @@ struct Args {
     int cap128;           // capacity, a multiple of 128
     int piece_rows;       // rows of a page per copy
     float scale;          // log2e / sqrt(d), or +-log2e ln d
+    int exact_weights;    // 1: LSSAR rows never take the one-exponential weights
     Power power;
     uint32_t idesc_s, idesc_s64, idesc_pv;     // scores of 128 keys, of 64; sum of w v
 };
@@ -457,7 +458,7 @@ __device__ __forceinline__ void powers16(float2 (&x)[8], Power pw) {
 // How a warp evaluates its weights (a warp-uniform choice).
 enum Form : int {
     kMixed = 0,      // softplus by logarithms and a polynomial in turn, to about 2^-19 (1 + its value)
-    kOneExp = 1,     // LSSAR rows that meet the bound of fast_weights.cuh
+    kOneExp = 1,     // LSSAR rows that meet the bound of fast_weights.cuh (none with LSSAR_EXACT_WEIGHTS=1)
     kAccurate = 2    // to 2^-18 of its value and evenly: rows whose scores are all negative, or nearly equal;
                      // softmax: rows whose scores pass 2^16
 };
@@ -541,7 +542,7 @@ __device__ __forceinline__ bool with_form(int form, int p, F f) {
 // needs.  A row is uniform where the largest difference is within 1e-5 of the maximum, as in the
 // decode step.  Its weights: phi 2^126 clamped to 1, which is 1 for every score that is not masked.
 template <int MODE>
-__device__ __forceinline__ int row_constants(Row &row, float m, float s1, int n, int p) {
+__device__ __forceinline__ int row_constants(Row &row, float m, float s1, int n, int p, bool exact_weights) {
     const bool raw = MODE == kSoftmaxRw;
     const float lift = raw ? 1.f : ptx::ex2(-fminf(m, 0.f));
     const float theta = n <= 3 ? 0.f : s1 * lift / (float)n;
@@ -561,7 +562,7 @@ __device__ __forceinline__ int row_constants(Row &row, float m, float s1, int n,
     if (den < 0.0078125f * top || (!raw && m < 0.f)) return kAccurate;
     if constexpr (MODE == kLssar) {
         row.ck = 2.f * kHalfInvLn2 * row.kappa;
-        if (fast_weights_ok(theta, row.kappa, (float)n, p)) return kOneExp;
+        if (!exact_weights && fast_weights_ok(theta, row.kappa, (float)n, p)) return kOneExp;
     }
     return kMixed;
 }
@@ -1128,7 +1129,7 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                     s1 = MODE == kSoftmaxRw ? s1 * ptx::ex2(m - top) + x.y * ptx::ex2(x.x - top) : s1 + x.y;
                     m = top;
                 }
-                form = row_constants<MODE>(row, m, s1, limit + 1, a.p);
+                form = row_constants<MODE>(row, m, s1, limit + 1, a.p, g.exact_weights);
                 // one form for the warp: all rows or none by one exponential
                 const unsigned accurate = __ballot_sync(0xffffffffu, form == kAccurate), one = __ballot_sync(0xffffffffu, form == kOneExp);
                 form = accurate ? kAccurate : one == 0xffffffffu ? kOneExp : kMixed;

@@ -664,3 +664,34 @@ def test_non_finite_inputs_stay_with_their_rows(torch_mod, mode, p, d, G):
         c.v[c.table[0, 699 // 16].long(), 0, 699 % 16] = value
         out = check_attend(torch, c, q, counts, mode, p, [[0, 100, 215], [5, 130, 299]])
         assert out[0, :, :216].isfinite().all() and out[1, :, :300].isfinite().all() and not out[0, :, 599].isfinite().any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,half", [(64, False), (128, False), (64, True)])
+def test_exact_weights_are_kept_on_request(torch_mod, monkeypatch, d, half):
+    # LSSAR rows that meet the bound take the one-exponential softplus, which moves some bits; none do with
+    # LSSAR_EXACT_WEIGHTS=1, and the rows are then within the oracle's bound without its share for that form
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    n, count, p = 6000, 200, 15
+    c = Cache(torch, [n], 2, d, 64, half=half, seed=d)
+    q = chunk_q(c, 2, count)
+    run = lambda: api.lssar_paged_attend(q, *c.args(), p=p, mode=MODE_LSSAR)   # noqa: E731
+    monkeypatch.delenv("LSSAR_EXACT_WEIGHTS", raising=False)
+    default = run()
+    monkeypatch.setenv("LSSAR_EXACT_WEIGHTS", "1")
+    exact = run()
+    monkeypatch.setenv("LSSAR_EXACT_WEIGHTS", "0")
+    assert torch.equal(run(), default)
+    assert api.device_error_word() == 0
+    assert not torch.equal(exact, default)
+    half_step = torch.finfo(c.dt).eps / 2
+    tiny = 2.0 ** -25 if half else 0.0
+    kb, vb, got = po.gather(host(c.k), c.table[0].tolist(), n), po.gather(host(c.v), c.table[0].tolist(), n), host(exact)
+    for h in range(2):
+        for t in range(0, count, 7):
+            i = n - count + t + 1
+            ref, err = so.attend_row(host(q[:, h, t]), kb[:i, h], vb[:i, h], MODE_LSSAR, p, half_step)
+            err = err - 4e-4 * np.abs(vb[:i, h]).max(axis=0)
+            bad = np.abs(got[0, h, t] - ref) - (err + half_step * (np.abs(ref) + err) + tiny)
+            assert bad.max() <= 0, (h, t, bad.max(), err.max())
