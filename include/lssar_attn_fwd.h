@@ -399,9 +399,9 @@ typedef struct {
  *         multiples of 8 where the dimension is above 1.
  *   positions : device int32, or NULL: token t is at position t.  per_token 0:
  *         [B], token t of sequence b at positions[b] + t; 1: [B, L].
- *   q_out, k_out : contiguous, apart from everything else; or the input itself,
- *         which is then turned in place at its own strides (rows that do not
- *         overlap; q and k may be slices of one [B, L, heads, d] buffer).
+ *   q_out, k_out : contiguous, apart from everything else; or the input itself
+ *         (the same address), which is then turned in place at its own strides (rows
+ *         that do not overlap; q and k may be slices of one [B, L, heads, d] buffer).
  * d is 64 or 128, dtype an lssar_dtype_t, H and Hk at least 1.
  * lssar_rope_bwd turns back: the gradients with respect to the inputs from
  * those with respect to the outputs (the same arguments).

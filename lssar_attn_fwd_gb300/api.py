@@ -666,13 +666,20 @@ def _like(x):
     return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
+def _takes(y, x, shape, strides):
+    """Whether the rows of x can be turned into y: contiguous, or, at the same address, with
+    the strides of x itself (where they matter), which the library then goes by."""
+    if y.data_ptr() != x.data_ptr() or y.numel() == 0:
+        return y.is_contiguous()
+    return y.stride() == strides or all(n == 1 or a == b for n, a, b in zip(shape, y.stride(), strides))
+
+
 def _turned(what, x, y, shape, strides, dtype, dev, stream):
     """The tensor that takes the turned rows of x: a new one, y apart from x, or x itself."""
     if y is None:
         return _like(x) if stream is None else _make(stream, dev, lambda: _like(x))
-    if (y.shape != shape or y.dtype is not dtype or y.get_device() != dev
-            or not (y.is_contiguous() or (y.data_ptr() == x.data_ptr() and y.stride() == strides))):
-        raise ValueError(f"{what}_out must be {what} itself or a contiguous tensor like it")
+    if y.shape != shape or y.dtype is not dtype or y.get_device() != dev or not _takes(y, x, shape, strides):
+        raise ValueError(f"{what}_out must be {what} itself or a contiguous tensor apart from it")
     return y
 
 
@@ -765,8 +772,8 @@ def lssar_paged_append_rope(q, k_new, v_new, k_pages, v_pages, table, lens, rota
     n, qst, kst, vst = shape[2], q.stride(), k_new.stride(), v_new.stride()
     if n and (qst[3] != 1 or kst[3] != 1 or vst[3] != 1):
         raise ValueError("the last dimension of q, k_new and v_new must be contiguous")
-    if not (q_out.is_contiguous() or (q_out.data_ptr() == q.data_ptr() and q_out.stride() == qst)):
-        raise ValueError("q_out must be contiguous, or q itself")
+    if not _takes(q_out, q, q_shape, qst):
+        raise ValueError("q_out must be q itself or a contiguous tensor apart from it")
     if lens_out is None:
         lens_out = torch.empty_like(lens) if stream is None else _make(stream, dev, lambda: torch.empty_like(lens))
     slots = (B, Hkv, cap)

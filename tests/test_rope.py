@@ -313,3 +313,41 @@ def test_rope_on_streams_and_in_graphs(torch_mod):
     g.replay()
     want = api.lssar_rope(q, k, r, positions=pos)
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+@pytest.mark.gpu
+def test_outputs_at_the_inputs_address(torch_mod):
+    # the input itself turns in place, at its own strides; a tensor of other strides at its address is refused
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    B, H, L, d = 2, 4, 6, 64
+    r, g = api.Rotary(d), torch.Generator().manual_seed(8)
+    buf = torch.randn(B, L, H, d, generator=g).bfloat16().cuda()
+    keep, q = buf.clone(), buf.transpose(1, 2)
+    apart = torch.randn(B, H, L, d, generator=g).bfloat16().cuda()
+    other = buf.view(B, H, L, d)
+    for call in (api.lssar_rope, api.lssar_rope_bwd):
+        with pytest.raises(ValueError):
+            call(q, None, r, None, other)
+        with pytest.raises(ValueError):
+            call(apart, q, r, None, None, other)
+        with pytest.raises(ValueError):
+            call(other, None, r, None, q)
+    c = Cache(torch, [20, 20], 2, d, 16, seed=3)
+    lens, new = torch.tensor([3, 9], dtype=torch.int32).cuda(), torch.zeros(B, 2, L, d, dtype=torch.bfloat16).cuda()
+    for x, y in ((q, other), (other, q)):
+        with pytest.raises(ValueError):
+            api.lssar_paged_append_rope(x, new, new, c.k, c.v, c.table, lens, r, q_out=y)
+    assert torch.equal(buf, keep)
+    # the same elements by another view, strides of dimensions of one apart
+    want, _ = api.lssar_rope(q[:, :, :1], None, r)
+    x = q[:, :, :1]
+    y = x.as_strided(x.shape, (x.stride(0), x.stride(1), 8, 1))
+    got, _ = api.lssar_rope(x, None, r, q_out=y)
+    assert got is y and torch.equal(x, want) and torch.equal(buf[:, 1:], keep[:, 1:])
+    # one token, [B, H, d] in place
+    step = apart[:, :, 0]
+    want, _ = api.lssar_paged_append_rope(step, new[:, :, 0], new[:, :, 0], c.k, c.v, c.table, lens, r)
+    got, _ = api.lssar_paged_append_rope(step, new[:, :, 0], new[:, :, 0], c.k, c.v, c.table, lens, r, q_out=step)
+    assert got is step and torch.equal(step, want)
+    assert api.device_error_word() == 0
