@@ -420,7 +420,8 @@ int lssar_rope_bwd(const void *q, const long long *q_strides, void *q_out, int H
  * key is turned on its way to the pages, its query turned into q_out.
  *   q : [B, H, n, d] of the cache's type, q_strides as above; H >= 1.
  *   q_out : [B, H, n, d] contiguous, or q itself (in place).  Rows t >= counts[b]
- *         are not written, nor those of a sequence that is left alone.
+ *         are not written, nor those of a sequence that is left alone; without
+ *         counts, apart from q, the latter are zeros.
  * Other arguments, results and errors as lssar_paged_append and lssar_rope.
  */
 int lssar_paged_append_rope(const lssar_paged_cache_t *cache, const void *q, const long long *q_strides, void *q_out,

@@ -743,7 +743,8 @@ def lssar_paged_append_rope(q, k_new, v_new, k_pages, v_pages, table, lens, rota
     q: [B, H, n, d] (or [B, H, d] for one token) of the cache's type, strides as
     k_new's; token t of sequence b is at position first_positions[b] + t (default:
     lens[b] + t).  q_out: contiguous like q, or q itself (in place); rows t >=
-    counts[b] are not written, and zeros where the call makes q_out itself.
+    counts[b], and those of a sequence that is left alone, are not written, and zeros
+    where the call makes q_out itself or has no counts (not in place).
     Other arguments as :func:`lssar_paged_append`.  Returns (q_out, new lengths).
     """
     import torch

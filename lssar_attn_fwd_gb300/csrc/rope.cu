@@ -182,7 +182,18 @@ __global__ void __launch_bounds__(kThreads) append_rope_rows(const __grid_consta
     if (token >= (long long)c.B * a.n) return;
     const int b = (int)(token / a.n), t = (int)(token - (long long)b * a.n);
     const int len = c.lens[b], cnt = a.counts ? a.counts[b] : a.n;
-    if (t >= cnt || len < 0 || cnt > a.n || (long long)len + cnt > c.capacity()) return;
+    const int g0 = blockIdx.y * group, g1 = min(g0 + group, r.q.H + 2 * c.Hkv);
+    const RopeView &q = r.q;
+    if (len < 0 || cnt < 0 || cnt > a.n || (long long)len + cnt > c.capacity()) {
+        // left alone; without counts its rows of q are asked for all the same, and nothing may stay unwritten
+        if (a.counts || q.x == q.y) return;
+        for (int h = g0; h < min(g1, q.H); ++h) {
+            uint4 *row = reinterpret_cast<uint4 *>(q.y + b * q.ys[0] + h * q.ys[1] + t * q.ys[2]);
+            row[2 * unit] = row[2 * unit + 1] = make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
+    if (t >= cnt) return;
     const long long first = a.first ? a.first[b] : len;
     const int slot = len + t, i = slot / c.page_size, row = slot - i * c.page_size;
     const int page = c.table[(size_t)b * c.max_pages + i];
@@ -196,8 +207,6 @@ __global__ void __launch_bounds__(kThreads) append_rope_rows(const __grid_consta
         if (!known && unit == 0) atomicCAS(c.err, 0u, (unsigned)kErrPagedPage);
     }
     const Turn turn = make_turn(r.table, unit, first + t, false);
-    const int g0 = blockIdx.y * group, g1 = min(g0 + group, r.q.H + 2 * c.Hkv);
-    const RopeView &q = r.q;
     if (g0 < q.H && (q.x != q.y || turn.turns))
         turn_heads<T, INTER, true>(q.x + b * q.xs[0] + t * q.xs[2], q.xs[1], q.y + b * q.ys[0] + t * q.ys[2], q.ys[1], g0, min(g1, q.H), turn);
     if (!known || !dcheck(row >= 0 && row < c.page_size, c.err, kDbgGlobal)) return;

@@ -351,3 +351,38 @@ def test_outputs_at_the_inputs_address(torch_mod):
     got, _ = api.lssar_paged_append_rope(step, new[:, :, 0], new[:, :, 0], c.k, c.v, c.table, lens, r, q_out=step)
     assert got is step and torch.equal(step, want)
     assert api.device_error_word() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,H,d", [(1, 3, 64), (5, 4, 64), (70, 20, 128)])
+def test_append_rope_without_counts_leaves_no_row_unwritten(torch_mod, n, H, d):
+    # sequences that do not fit: zeros where the output is apart from q; untouched in place and where counts are given
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    c = Cache(torch, [160, 160, 160, 160], 2, d, 16, seed=6)
+    q, new = torch.randn(4, H, n, d, generator=c.g).to(c.dt).cuda(), torch.randn(4, 2, n, d, generator=c.g).to(c.dt).cuda()
+    r = api.Rotary(d, rot_dim=48)
+    lens = torch.tensor([161 - n, 10, -1, 2 ** 31 - 1], dtype=torch.int32).cuda()
+    good = torch.tensor([0, 10, 0, 0], dtype=torch.int32).cuda()
+    first = torch.tensor([0, 10, 3, 4], dtype=torch.int32).cuda()
+    append = lambda q, lens, **kw: api.lssar_paged_append_rope(q, new, new, c.k.clone(), c.v.clone(), c.table, lens, r,   # noqa: E731
+                                                               first_positions=first, **kw)
+    want, _ = append(q, good)
+    assert api.device_error_word() == 0
+    given = torch.full_like(q, 7.0)
+    append(q, lens, q_out=given)
+    made = []
+    for _ in range(4):                        # blocks that held something else
+        junk = [torch.full_like(q, 7.0) for _ in range(4)]
+        del junk
+        made.append(append(q, lens)[0])
+    assert api.device_error_word() == LENGTH
+    for out in (given, *made):
+        assert torch.equal(out[1], want[1]) and (out[[0, 2, 3]] == 0).all()
+    x = q.clone()
+    append(x, lens, q_out=x)
+    assert torch.equal(x[1], want[1]) and torch.equal(x[[0, 2, 3]], q[[0, 2, 3]])
+    given.fill_(7.0)
+    append(q, lens, counts=torch.full_like(lens, n), q_out=given)
+    assert torch.equal(given[1], want[1]) and (given[[0, 2, 3]] == 7.0).all()
+    assert api.device_error_word() == LENGTH
