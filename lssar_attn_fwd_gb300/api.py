@@ -457,8 +457,11 @@ def _paged_cache(k_pages, v_pages, table, lens):
 
 def _slots(name, t, shape, dtype, dev):
     """The pointer of a [B, Hkv, capacity] tensor of per-slot values, or None."""
+    import torch
     if t is None:
         return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous {dtype} [B, Hkv, max_pages * page_size] tensor on the cache's device")
     return t.data_ptr()
@@ -469,6 +472,8 @@ def _per_sequence(name, t, B, dev):
     import torch
     if t is None:
         return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
     if t.dtype is not torch.int32 or t.shape != (B,) or not t.is_contiguous() or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous int32 [B] tensor on the same device")
     return t.data_ptr()
@@ -621,6 +626,8 @@ def lssar_paged_attend(q, k_pages, v_pages, table, lens, counts=None, p=3, mode=
     """
     import torch
     desc, B, Hkv, cap, d, dev = _paged_cache(k_pages, v_pages, table, lens)
+    if not isinstance(q, torch.Tensor) or not (out is None or isinstance(out, torch.Tensor)):
+        raise TypeError("q and out must be torch tensors")
     if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
         raise ValueError("q must be [B, H, n, d] with the cache's B and d")
     shape, dtype, strides = q.shape, k_pages.dtype, q.stride()
@@ -678,6 +685,9 @@ def _turned(what, x, y, shape, strides, dtype, dev, stream):
     """The tensor that takes the turned rows of x: a new one, y apart from x, or x itself."""
     if y is None:
         return _like(x) if stream is None else _make(stream, dev, lambda: _like(x))
+    import torch
+    if not isinstance(y, torch.Tensor):
+        raise TypeError(f"{what}_out must be a torch tensor")
     if y.shape != shape or y.dtype is not dtype or y.get_device() != dev or not _takes(y, x, shape, strides):
         raise ValueError(f"{what}_out must be {what} itself or a contiguous tensor apart from it")
     return y
@@ -695,6 +705,8 @@ def _rope(name, q, k, rotary, positions, q_out, k_out, stream):
         raise ValueError("rotary must be a Rotary of q's head dimension")
     per_token, at = 0, None
     if positions is not None:
+        if not isinstance(positions, torch.Tensor):
+            raise TypeError("positions must be a torch tensor")
         per_token, at = int(positions.dim() == 2), positions.data_ptr()
         if (positions.dtype is not torch.int32 or positions.shape != ((B, L) if per_token else (B,))
                 or not positions.is_contiguous() or positions.get_device() != dev):
@@ -751,6 +763,9 @@ def lssar_paged_append_rope(q, k_new, v_new, k_pages, v_pages, table, lens, rota
     desc, B, Hkv, cap, d, dev = _paged_cache(k_pages, v_pages, table, lens)
     if not isinstance(rotary, Rotary) or rotary.d != d:
         raise ValueError("rotary must be a Rotary of the cache's head dimension")
+    T = torch.Tensor
+    if not (isinstance(q, T) and isinstance(k_new, T) and isinstance(v_new, T) and (q_out is None or isinstance(q_out, T))):
+        raise TypeError("q, k_new, v_new and q_out must be torch tensors")
     dtype, q_shape = k_pages.dtype, q.shape
     if q_out is None:
         if counts is None:
@@ -798,6 +813,8 @@ def _pages(table, lens, free_pages, free_count, free_out, stream):
         raise ValueError("table must be a contiguous int32 [B, max_pages] CUDA tensor")
     if free_out is None:
         free_out = torch.empty_like(free_count) if stream is None else _make(stream, dev, lambda: torch.empty_like(free_count))
+    elif not isinstance(free_out, T):
+        raise TypeError("free_out must be a torch tensor")
     elif free_out.shape != (1,) or free_out.dtype is not i32 or free_out.get_device() != dev:
         raise ValueError("free_out must be an int32 [1] tensor on the table's device")
     if free_pages.dim() != 1 or free_pages.dtype is not i32 or not free_pages.is_contiguous() or free_pages.get_device() != dev:
