@@ -376,8 +376,11 @@ int lssar_paged_attend(const lssar_paged_cache_t *cache, const void *q, const lo
  *   BANDS   f_c (g + (1 - g) / factor), g = clamp((r - low) / (high - low), 0, 1),
  *           r = original_length f_c / (2 pi): pairs that turn often within the
  *           trained length keep their frequency
- * Angles are taken modulo a turn in 64-bit fixed point, exact to 2^-33 turns at
- * every 32-bit position; the products are in fp32, rounded once.
+ * Angles are taken modulo a turn in 64-bit fixed point.  They are off by at most
+ * |m| 2^-50 turns (the frequencies' rounding as doubles: 2^-30 at a position of 10^6,
+ * 2^-19 at 2^31; with a base of 10000 about 2^-24 there; BANDS: 2 high /
+ * (high - low) times as much) and 2^-25 turns (their conversion to fp32).  The products are in
+ * fp32, rounded once.
  */
 typedef enum {
     LSSAR_ROPE_PLAIN = 0, LSSAR_ROPE_LINEAR = 1, LSSAR_ROPE_BASE = 2, LSSAR_ROPE_BANDS = 3

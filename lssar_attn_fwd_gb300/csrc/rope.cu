@@ -33,7 +33,7 @@ int rotary_table(const lssar_rotary_t *r, int d, RotaryTable *out) {
     const double base = r->scaling == LSSAR_ROPE_BASE ? r->base * std::pow(r->factor, (double)rot / (rot - 2)) : r->base;
     if (!std::isfinite(base)) return LSSAR_ERR_ROTARY;
     for (int c = 0; c < kMaxPairs; ++c) out->turn[c] = 0;
-    // by exp() for every eighth pair, and products between (8 x 3 x 2^-53 of each)
+    // by exp() for every eighth pair, and products between (at most 7 x 3 x 2^-53 of each)
     const double step = -2.0 / rot * std::log(base), ratio = std::exp(step);
     double g = 1.0;
     for (int c = 0; c < rot / 2; ++c) {

@@ -386,3 +386,50 @@ def test_append_rope_without_counts_leaves_no_row_unwritten(torch_mod, n, H, d):
     append(q, lens, counts=torch.full_like(lens, n), q_out=given)
     assert torch.equal(given[1], want[1]) and (given[[0, 2, 3]] == 7.0).all()
     assert api.device_error_word() == LENGTH
+
+
+def exact_turns(base, rot, c):
+    """Turns per position of pair c, as a Fraction of 2^-160."""
+    from decimal import Decimal, getcontext
+    from fractions import Fraction
+    getcontext().prec = 70
+    f = (Decimal(base).ln() * Decimal(-2 * c) / Decimal(rot)).exp()
+    # pi by Machin's formula
+    one = 1 << 220
+    atan = lambda x: sum((-1) ** i * (one // ((2 * i + 1) * x ** (2 * i + 1))) for i in range(170))   # noqa: E731
+    pi = Fraction(4 * (4 * atan(5) - atan(239)), one)
+    return Fraction(f) / (2 * pi)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("base", [10000.0, 1000000.0, 1.25])
+@pytest.mark.parametrize("near", [10 ** 6, 2 ** 31 - 2 ** 18])
+def test_rope_angles_to_their_bound(torch_mod, base, near):
+    # positions whose angle lies next to a half turn, where the output shows it: -sin of what is left
+    import math
+    from fractions import Fraction
+    torch = torch_mod
+    from lssar_attn_fwd_gb300 import api
+    d, pairs = 64, 32
+    positions, left = [], []
+    for c in range(pairs):
+        turn = exact_turns(base, d, c)
+        t64 = int(turn * 2 ** 64)
+        m = near + np.arange(2 ** 18, dtype=np.uint64)
+        with np.errstate(over="ignore"):
+            phase = (m * np.uint64(t64)).astype(np.uint64) << np.uint64(1)       # modulo half a turn
+        off = np.minimum(phase, ~phase).astype(np.float64)
+        best = int(m[off.argmin()])
+        x = turn * best * 2
+        positions.append(best)
+        left.append((-1.0 if round(x) % 2 else 1.0, math.sin(math.pi * float(x - round(x)))))
+    q = torch.zeros(pairs, 1, 1, d, dtype=torch.float16)
+    q[range(pairs), 0, 0, pairs + np.arange(pairs)] = 1.0        # (0, 1) -> (-sin, cos)
+    out, _ = api.lssar_rope(q.cuda(), None, api.Rotary(d, base=base), positions=torch.tensor(positions, dtype=torch.int32).cuda())
+    got = host(out)[range(pairs), 0, 0, range(pairs)]
+    for c, (m, (sign, s)) in enumerate(zip(positions, left)):
+        # the angle's bound; the sine's error and the output's half step, relative and absolute
+        bound = 2 * math.pi * (m * 2.0 ** -50 + 2.0 ** -25)
+        want = -sign * s
+        assert abs(got[c] - want) <= bound + (2.0 ** -11 + 2.0 ** -21) * (abs(want) + bound) + 2.0 ** -25, (c, m, got[c], want)
+    assert (np.abs([s for _, s in left]) < 0.01).sum() >= 20     # most of them do lie there
