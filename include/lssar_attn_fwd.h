@@ -348,6 +348,8 @@ int lssar_paged_evict(const lssar_paged_cache_t *cache, const float *scores, con
  * that page's slots.  What the rows of pages past lens[b] hold does not matter.
  * A value that is infinite or NaN among the cached tokens reaches the rows of
  * the chunk that attend to it, and may reach rows up to 383 slots before it.
+ * The rows' weights are added up nowhere: an eviction goes by those of
+ * lssar_paged_decode.
  * LSSAR weights with p >= 4 as in lssar_attn_fwd: by one exponential where its
  * bound allows, none with LSSAR_EXACT_WEIGHTS=1 in the environment.
  * The sums have a fixed order: the same call on the same device gives the same

@@ -621,8 +621,9 @@ def lssar_paged_attend(q, k_pages, v_pages, table, lens, counts=None, p=3, mode=
     rows of each sequence (default: n); row t < counts[b] attends to the first
     lens[b] - counts[b] + t + 1 cached tokens.  Returns out [B, H, n, d]
     (contiguous); rows t >= counts[b] are not written, and zeros where the call
-    makes out itself.  Runs asynchronously on ``stream`` (default: the current
-    stream).
+    makes out itself.  Adds nothing to an eviction's scores: those are
+    :func:`lssar_paged_decode`'s.  Runs asynchronously on ``stream`` (default: the
+    current stream).
     """
     import torch
     desc, B, Hkv, cap, d, dev = _paged_cache(k_pages, v_pages, table, lens)

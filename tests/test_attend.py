@@ -695,3 +695,34 @@ def test_exact_weights_are_kept_on_request(torch_mod, monkeypatch, d, half):
             err = err - 4e-4 * np.abs(vb[:i, h]).max(axis=0)
             bad = np.abs(got[0, h, t] - ref) - (err + half_step * (np.abs(ref) + err) + tiny)
             assert bad.max() <= 0, (h, t, bad.max(), err.max())
+
+
+@pytest.mark.gpu
+def test_weights_of_an_eviction_are_those_of_decode_steps(torch_mod):
+    # a prompt in two chunks leaves the scores at 0; a step of one token through the decode step adds up its weights,
+    # and the eviction keeps the tokens that have them
+    torch = torch_mod
+    s = Serving(torch, 3)
+    api, kv = s.api, (s.k, s.v, s.table)
+    for n in (40, 30):
+        s.chunk(*s.inputs(n), ints(torch, n, n, n))
+        s.lens.copy_(s.after), s.free_count.copy_(s.fo), s.seen.add_(s.counts)
+        assert (s.scores == 0).all()
+    q, k, v = s.inputs(1)
+    s.counts, s.free_count = api.lssar_paged_reserve(s.table, s.lens, ints(torch, 1, 1, 1), s.page, s.free, s.free_count)
+    q, s.lens = api.lssar_paged_append_rope(q, k, v, *kv, s.lens, s.rotary, counts=s.counts, first_positions=s.seen,
+                                            scores=s.scores, positions=s.positions)
+    out = api.lssar_paged_decode(q[:, :, 0], *kv, s.lens, p=15, scores=s.scores)
+    chunk = api.lssar_paged_attend(q, *kv, s.lens, p=15)[:, :, 0]
+    # each is within half a step and its weights' rounding of exact: 2^-8 of the largest |v|, below 5, twice
+    assert (out.float() - chunk.float()).abs().max() <= 2 ** -6 * 5
+    # two query heads to a key head, whose weights sum to 1: fp32 sums of 71
+    total = s.scores.sum(-1)
+    assert (total - 2).abs().max() <= 71 * 2.0 ** -23 * 2 + 2.0 ** -12
+    want = [[set(host(s.positions)[b, h, np.argsort(-host(s.scores)[b, h, :71], kind="stable")[:20]].astype(int)) for h in range(s.hkv)]
+            for b in range(s.B)]
+    lens, _, _ = api.lssar_paged_evict(*kv, s.lens, s.scores, s.positions, 20, recent=0, sinks=0)
+    assert lens.tolist() == [20] * 3 and api.device_error_word() == 0
+    for b in range(s.B):
+        for h in range(s.hkv):
+            assert set(s.positions[b, h, :20].tolist()) == want[b][h]
