@@ -985,13 +985,10 @@ attend_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CU
                             }
                             if (!ok) break;
                         } else {
-                            if (!(ok = wait_all(kSepP ? LSSAR_AT(p_full) + 8 * w : LSSAR_AT(s_free) + 16 * w, pv & 1, kErrPFull)) || !(ok = o_is_free())) break;
+                            if (!(ok = wait_all(LSSAR_AT(p_full) + 8 * w, pv & 1, kErrPFull)) || !(ok = o_is_free())) break;
                             ptx::tc_fence_after();
-                            // (at d = 128 P's words are over the first half of each half of S)
-                            issue_pv(vslot, 0, kSepP ? 8 : 4, kt > begin);
-                            if constexpr (!kSepP) issue_pv(vslot, 64, 4, true);
-                            if constexpr (kSepP) commit(LSSAR_AT(p_free) + 8 * w);
-                            else if (next && !(ok = issue_s(kslot))) break;
+                            issue_pv(vslot, 0, 8, kt > begin);
+                            commit(LSSAR_AT(p_free) + 8 * w);
                         }
                         ++pv;
                         if (!next) {
