@@ -355,11 +355,12 @@ int lssar_paged_evict(const lssar_paged_cache_t *cache, const float *scores, con
  * The sums have a fixed order: the same call on the same device gives the same
  * bits.  Three launches (softmax, LSSA) or four (re-weighting modes).  K and V are
  * read once for each block of T = floor(256 Hkv / H) tokens, K twice in the
- * re-weighting modes and once more for its norms where the mode has them.  Scratch
+ * re-weighting modes and once more for its norms where the mode has them (of every
+ * cached token, also of sequences without rows).  Scratch
  * from the library's pool, by what the table and n have room for: 16 bytes for each
  * of B ceil(n / T) blocks; 4 bytes for each key head and slot (modes with norms); 8
  * bytes for each of min(n, T) H / Hkv rows of B Hkv ceil(n / T) + SMs items
- * (re-weighting modes); 8 (d + 1) bytes for each of SMs * min(n, T) H / Hkv rows.
+ * (re-weighting modes); 8 (d + 2) bytes for each of SMs * min(n, T) H / Hkv rows.
  * Errors as lssar_paged_decode; SHAPE also where
  * B Hkv ceil(n / T) (ceil(capacity / 64) + 7) passes 2^31 - 2^16.
  */

@@ -1,4 +1,4 @@
-// Internal declarations of the paged key-value cache: append, decode, evict.
+// Internal declarations of the paged key-value cache: append, decode, evict, attention of a chunk, pages.
 #pragma once
 
 #include <cstdint>

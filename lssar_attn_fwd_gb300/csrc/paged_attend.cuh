@@ -9,12 +9,16 @@
 // Scores are products of the inputs' own bits, scaled in fp32 afterwards: 1/|k| of each cached
 // key comes from a prologue that reads them once, |q| from the gathered rows.
 //
-// What bounds it: the score warps.  A score costs 5 instructions in the statistics pass (one of them a
-// special function), 7 in the values pass at p = 15, and as much again in waits, barriers and loads of
-// whole tiles; against that stand 4 d flops of tensor work and, at 256 rows per key, 4 d / 256 bytes.
+// What bounds it: the score warps.  For 32 scores the statistics pass executes 7.1 warp instructions (4.9 of them
+// arithmetic, one a special function), the values pass at p = 15 11.7 (7.4); the others are branches, waits, indices
+// and loads.  Against that stand 4 d flops of tensor work a score and, at 256 rows per key, 4 d / 256 bytes.
 // Measured (kernels alone): 2K rows on 14K tokens, 12 heads of 64, LSSAR p = 15: 103 + 181 us (issue slots
-// 66 and 61 % busy, tensor pipe 20 and 23 %); 512 rows on 128K, 16/2 heads of 128: 270 + 500 us (69 and 57 %,
-// tensor 43 and 46 %); four prompts of 4K, 16 heads of 128, LSSA: 350 us (47 %, tensor 38 %).
+// 66 and 61 % busy, so that what is executed would fill 71 and 116 us; tensor pipe 20 and 23 %); 512 rows on 128K,
+// 16/2 heads of 128: 270 + 500 us (69 and 57 %, tensor 43 and 46 %); four prompts of 4K, 16 heads of 128, LSSA: 350 us
+// (47 %, tensor 38 %), softmax 308 us, where the dense forward, with its one MMA warp, products 128 keys wide and (LSSA)
+// normalised copies of the rows, takes 242 and 229.
+// The time depends on the scores: rows whose scores are all negative take the softplus evenly to its own value
+// (kAccurate, and the statistics twice): the 2K rows above take the call 537 us instead of 303.
 //
 // Split.  A work item is a pair of 128-row tiles of the rows (token, head of the group) of one
 // key head: floor(256 / G) tokens.  What an item costs, its K tiles of 128 keys and a share for its own beginning
@@ -471,6 +475,11 @@ constexpr int kPolyPairs = MODE == kLssa ? 8 : 4;
 
 // Weights of 16 scores (r[0..15]), summed into acc and packed into 8 words.  `pair0`: number of the
 // first pair in its chunk of 32.
+// They are rounded to the type of the values, half a step (2^-8 of each in bf16, 2^-11 in fp16): a tensor product takes both
+// operands in one type, and one more of what the rounding leaves would double the values' share of the tensor pipe.  The sum
+// takes them in fp32, as they were: the roundings, of either sign, average over the row.  Error of the output against
+// float64, in the norm, with fp32 weights and here: LSSA prompts 0.0016 and 0.0023, 64 rows on 200 0.0017 and
+// 0.0018, the other chunks of bf16 (0.0016 and 0.0017) and of fp16 (0.00021) the same, as the output's own rounding is.
 template <int MODE, bool HALF, int FORM, int P>
 __device__ __forceinline__ void weights16(const uint32_t *r, int pair0, const Row &row, Power p, float2 &acc, uint32_t *pk) {
     const auto both = [](float x) { return make_float2(x, x); };
