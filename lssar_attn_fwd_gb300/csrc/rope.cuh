@@ -13,10 +13,10 @@ constexpr int kMaxPairs = 64;   // rot_dim / 2
 
 // The turn of every pair, in turns per position as a 64-bit fraction: the phase of
 // position m is m * turn[c] modulo 2^64, exact for every 32-bit m.  The table's own
-// rounding, of doubles, is at most 27 x 2^-53 / 2 pi < 2^-50 turns: of a frequency f, 5 |ln f| x 2^-53 by
-// the exponent (at most 5 / e of a turn's radian) and 23 x 2^-53 by exp() and the products.  It grows to
-// 2^-19 turns at m = 2^31 (found: 2^-24 at a base of 10000, 2^-22 at the worst of 207 bases).  fp32 angles
-// would be off by 0.06 radians at a position of 10^6.
+// rounding, of doubles, is below 2^-50 turns per position: of a frequency f <= 1 it is at most
+// 5 |ln f| x 2^-53 by the exponent (f |ln f| <= 1 / e) and 25 x 2^-53 by exp(), the products and 2 pi, over 2 pi.
+// It grows to 2^-19 turns at m = 2^31 (found: 2^-24 at a base of 10000, 2^-22 at the worst of 207 bases).
+// fp32 angles would be off by 0.06 radians at a position of 10^6.
 struct RotaryTable {
     unsigned long long turn[kMaxPairs];
     int rot;             // elements that turn
